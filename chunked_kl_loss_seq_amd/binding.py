@@ -16,9 +16,18 @@ CKL_OK = 0
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
 PASSES = {"fused": 0, "fwd": 1, "bwd": 2}
-TIMING_KINDS = {"logits": 0, "rows": 1, "dh": 2, "dh_reduce": 3, "dw": 4, "other": 5, "topk": 6}
+TIMING_KINDS = {"logits": 0, "rows": 1, "dh": 2, "dh_reduce": 3, "dw": 4, "other": 5, "topk": 6, "embed": 7,
+                "sample": 8}
 
 _lib = None
+
+
+class Sampling(ctypes.Structure):
+    """ckl_sampling: one value for all rows, or a device array [N] where not null."""
+
+    _fields_ = [("temperature", ctypes.c_double), ("top_k", ctypes.c_int64), ("top_p", ctypes.c_double),
+                ("min_p", ctypes.c_double), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
 class CklError(RuntimeError):
@@ -55,6 +64,14 @@ def lib():
     L.ckl_bwd.restype = ctypes.c_int
     L.ckl_topk.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, vp, vp]
     L.ckl_topk.restype = ctypes.c_int
+    L.ckl_embed.argtypes = [ctypes.c_int, vp, vp, f32, i64, i64, i64, vp, vp]
+    L.ckl_embed.restype = ctypes.c_int
+    L.ckl_embed_bwd.argtypes = [ctypes.c_int, vp, vp, f32, i64, i64, i64, ctypes.c_int, vp, vp, u64, vp]
+    L.ckl_embed_bwd.restype = ctypes.c_int
+    L.ckl_embed_bwd_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(u64)]
+    L.ckl_embed_bwd_workspace.restype = ctypes.c_int
+    L.ckl_sample.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, ctypes.POINTER(Sampling), vp, vp, vp]
+    L.ckl_sample.restype = ctypes.c_int
     L.ckl_release_workspace.argtypes = []
     L.ckl_release_workspace.restype = None
     L.ckl_workspace_bytes_held.argtypes = []

@@ -291,7 +291,7 @@ struct TraceRange {
 };
 
 // ------------------------------------------------------------------ timing
-enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_KINDS };
+enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_KINDS };
 struct TimingState {
   bool on = false;
   std::vector<std::pair<hipEvent_t, hipEvent_t>> pool;
@@ -511,6 +511,15 @@ int run_impl(Pass pass, Dtype dt, const void* H, const void* W, const int32_t* i
 }
 
 inline bool dtype_ok(int dtype) { return dtype == CKL_DTYPE_BF16 || dtype == CKL_DTYPE_F32; }
+// Workgroups of 256 threads in one launch dimension, at most (exclusive).
+constexpr int64_t kMaxBlocks256 = (int64_t)1 << 24;
+
+int embed_shape(int64_t N, int64_t d, int64_t V) {
+  if (N < 0 || d <= 0 || V <= 0) return CKL_EINVAL;
+  if (d % 8 != 0 || d > (int64_t)1 << 20 || V > (int64_t)1 << 26 || N >= (int64_t)1 << 26) return CKL_EUNSUPPORTED;
+  return CKL_OK;
+}
+
 inline Dtype to_dt(int dtype) { return dtype == CKL_DTYPE_BF16 ? DT_BF16 : DT_F32; }
 
 }  // namespace
@@ -600,6 +609,84 @@ int ckl_topk(int dtype, const void* logits, int64_t N, int64_t V, int64_t K, int
   try {
     Timed t(T_TOPK, stream);
     CKL_TRY(launch_topk(to_dt(dtype), logits, N, V, K, ids_out, vals_out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_embed(int dtype, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V, void* out,
+              hipStream_t stream) {
+  if (!dtype_ok(dtype)) return CKL_EINVAL;
+  const int st = embed_shape(N, d, V);
+  if (st != CKL_OK || N == 0) return st;
+  if (!ids || !W || !out) return CKL_EINVAL;
+  if (!aligned(ids, 4) || !aligned(W, 16) || !aligned(out, 16)) return CKL_EINVAL;
+  try {
+    Timed t(T_EMBED, stream);
+    CKL_TRY(launch_embed(to_dt(dtype), ids, W, scale, N, d, V, out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_embed_bwd_workspace(int64_t N, int64_t d, int64_t V, uint64_t* bytes_out) {
+  if (!bytes_out) return CKL_EINVAL;
+  const int st = embed_shape(N, d, V);
+  if (st != CKL_OK) return st;
+  *bytes_out = embed_bwd_workspace(N, d, V);
+  return CKL_OK;
+}
+
+int ckl_embed_bwd(int dtype, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,
+                  int accumulate, float* dW, void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return CKL_EINVAL;
+  const int st = embed_shape(N, d, V);
+  if (st != CKL_OK) return st;
+  if (!dW || !aligned(dW, 16)) return CKL_EINVAL;
+  try {
+    if (N == 0) {  // no positions: a zero gradient, or nothing to add
+      if (!accumulate) CKL_TRY(launch_fill_f32(dW, V * d, 0.f, stream));
+      return CKL_OK;
+    }
+    if (!ids || !dY || !workspace) return CKL_EINVAL;
+    if (!aligned(ids, 4) || !aligned(dY, 16) || !aligned(workspace, 256)) return CKL_EINVAL;
+    if (workspace_bytes < embed_bwd_workspace(N, d, V)) return CKL_EINVAL;
+    if (embed_bwd_blocks(to_dt(dtype), N, d, V) >= kMaxBlocks256) return CKL_EUNSUPPORTED;
+    Timed t(T_EMBED, stream);
+    CKL_TRY(launch_embed_bwd(to_dt(dtype), ids, dY, scale, N, d, V, accumulate != 0, dW, workspace, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const float* u,
+               const ckl_sampling* how, int32_t* ids_out, float* logp_out, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return CKL_EINVAL;
+  if (N < 0 || V <= 0 || row_stride < 0) return CKL_EINVAL;
+  SampleParams p{1.0, 0, 1.0, 0.0, nullptr, nullptr, nullptr, nullptr};
+  if (how) {
+    p = SampleParams{how->temperature, how->top_k,  how->top_p, how->min_p,
+                     how->temperatures, how->top_ks, how->top_ps, how->min_ps};
+    // written so that NaN fails
+    if (!p.temperatures && !(p.temperature >= 0.0)) return CKL_EINVAL;
+    if (!p.top_ks && p.top_k < 0) return CKL_EINVAL;
+    if (!p.top_ps && !(p.top_p >= 0.0 && p.top_p <= 1.0)) return CKL_EINVAL;
+    if (!p.min_ps && !(p.min_p >= 0.0 && p.min_p <= 1.0)) return CKL_EINVAL;
+    if (!aligned(p.temperatures, 4) || !aligned(p.top_ks, 4) || !aligned(p.top_ps, 4) || !aligned(p.min_ps, 4))
+      return CKL_EINVAL;
+  }
+  if (V > (int64_t)1 << 26 || N >= (int64_t)1 << 23) return CKL_EUNSUPPORTED;
+  if (N == 0) return CKL_OK;
+  if (!logits || !u || !ids_out) return CKL_EINVAL;
+  if (!aligned(logits, dtype == CKL_DTYPE_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(ids_out, 4) ||
+      !aligned(logp_out, 4))
+    return CKL_EINVAL;
+  try {
+    Timed t(T_SAMPLE, stream);
+    CKL_TRY(launch_sample(to_dt(dtype), logits, N, V, row_stride, u, p, ids_out, logp_out, stream));
     return CKL_OK;
   } catch (...) {
     return CKL_EHIP;

@@ -90,6 +90,30 @@ int d_tile(Dtype dt, int64_t d);
 hipError_t launch_topk(Dtype dt, const void* x, int64_t N, int64_t V, int64_t K, int32_t* ids, float* vals,
                        hipStream_t s);
 
+// out[n] = scale W[ids[n]] (zeros for an id outside [0, V)), see kernels_embed.hip.
+hipError_t launch_embed(Dtype dt, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V,
+                        void* out, hipStream_t s);
+// dW[v] (+)= scale x the sum of dY's rows with id v; ws of embed_bwd_workspace bytes.
+uint64_t embed_bwd_workspace(int64_t N, int64_t d, int64_t V);
+hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,
+                            bool accumulate, float* dW, void* ws, hipStream_t s);
+// Workgroups of its largest launch.
+int64_t embed_bwd_blocks(Dtype dt, int64_t N, int64_t d, int64_t V);
+
+// Settings of a sampling call: one value for all rows, or a device array [N].
+struct SampleParams {
+  double temperature;
+  int64_t top_k;
+  double top_p, min_p;
+  const float* temperatures;
+  const int32_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+};
+// A token and its log-probability per row of x (rows ld elements apart), see kernels_sample.hip.
+hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t ld, const float* u,
+                         const SampleParams& p, int32_t* ids, float* logp, hipStream_t s);
+
 // Valid-token count n and scale 1/n (0 if n = 0) into scal (int64 n, float s).
 hipError_t launch_mask_count(const uint8_t* mask, int64_t N, void* scal, hipStream_t s);
 // Compaction of the chunk whose mask, H rows, ids and teacher logits start at

@@ -198,6 +198,72 @@ typedef enum { CKL_PASS_FUSED = 0, CKL_PASS_FWD = 1, CKL_PASS_BWD = 2 } ckl_pass
 int ckl_topk(int dtype, const void* logits, int64_t N, int64_t V, int64_t K, int32_t* ids_out, float* vals_out,
              hipStream_t stream);
 
+/* Token embedding: the other end of the vocabulary table whose head gradient
+ * the loss computes.
+ *   out[n] = scale W[ids[n]], rounded once to W's type
+ *   dtype     ckl_dtype of W and out
+ *   ids       int32 [N]; an id outside [0, V) is a position without a token:
+ *             its row of out is zeros
+ *   W         [V, d], out [N, d], 16-byte aligned
+ * N < 2^26, V <= 2^26, d % 8 == 0, d <= 2^20.  No workspace. */
+int ckl_embed(int dtype, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V, void* out,
+              hipStream_t stream);
+
+/* Gradient of ckl_embed with respect to W:
+ *   dW[v] (+)= scale (sum of dY[n] over the positions n with ids[n] = v)
+ *   dtype       ckl_dtype of dY [N, d]
+ *   accumulate  0: dW is overwritten, rows of absent tokens with zeros;
+ *               1: the sums are added to dW and rows of absent tokens are left
+ *               alone (tied weights: dW as a loss call wrote it)
+ *   dW          fp32 [V, d], 16-byte aligned
+ *   workspace   device buffer of at least ckl_embed_bwd_workspace bytes,
+ *               256-byte aligned; it need not be cleared, and no two calls
+ *               that may overlap may share it
+ * Sums are fp32 in a fixed order, so the result depends on the inputs alone.
+ * Positions without a token contribute nothing.  N = 0: dW = 0, or nothing.
+ * Shapes as for ckl_embed; CKL_EUNSUPPORTED also where a launch would pass
+ * 2^24 workgroups. */
+int ckl_embed_bwd(int dtype, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,
+                  int accumulate, float* dW, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+int ckl_embed_bwd_workspace(int64_t N, int64_t d, int64_t V, uint64_t* bytes_out);
+
+/* Settings of ckl_sample: one value for all rows or, where the array is not
+ * NULL, the row's value from a device array [N].  Single values outside their
+ * range are CKL_EINVAL; array values are taken as stated. */
+typedef struct ckl_sampling {
+  double temperature; /* >= 0; 0 (in an array also below 0 or NaN): the largest logit, lowest id first */
+  int64_t top_k;      /* 0 (in an array also below 0) or >= V: no limit */
+  double top_p;       /* [0, 1]; 1 (in an array also above 1 or NaN): no limit */
+  double min_p;       /* [0, 1]; 0 (in an array also below 0 or NaN): no limit; above 1 as 1 */
+  const float* temperatures;
+  const int32_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+} ckl_sampling;
+
+/* One token per row of logits from given random numbers.  In a row the tokens
+ * are ordered as ckl_topk orders them (logit descending, equal logits by id
+ * ascending).  With e_j = exp((l_j - l_max) / temperature), the kept prefix is
+ * the shortest of
+ *   the first top_k tokens,
+ *   the shortest prefix whose mass reaches top_p x the mass of those,
+ *   the tokens with e_j >= min_p,
+ * and never empty.  The token is the first of the order at which the
+ * cumulative mass exceeds u x the kept mass S: its probability is e / S.
+ *   logits    [N, V], rows row_stride >= 0 elements apart, elements of a row
+ *             adjacent, aligned to an element.  -inf and NaN are tokens that
+ *             cannot be drawn; where +inf occurs, its tokens share the row
+ *   u         fp32 [N] in [0, 1) (NaN and below 0 as 0, from 1 on as the
+ *             largest value below 1)
+ *   how       NULL: temperature 1, no limit
+ *   ids_out   int32 [N]; -1 for a row without a token that can be drawn
+ *   logp_out  fp32 [N] or NULL: log(e / S) of the drawn token (-inf for -1)
+ * Masses and borders are computed in 64 bits, so the token is that of the
+ * formulas except where a border is within about 1e-13 of the total; tokens
+ * whose e is below 2^-64 count as 0.  V <= 2^26, N < 2^23.  No workspace. */
+int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const float* u,
+               const ckl_sampling* how, int32_t* ids_out, float* logp_out, hipStream_t stream);
+
 /* Chunk planner of the fused call (pure host computation, needs no GPU).  The
  * sequence is cut into chunks of C rows so that the loss's own device memory
  * stays bounded independently of N ("A New Trick...", section "Does this
@@ -249,11 +315,12 @@ int ckl_debug_rows(const float* Z, const int32_t* idx, const float* tlogit, cons
                    void* G_out, float* kl_out, float* lse_out, hipStream_t stream);
 
 /* Measurement support.  While enabled, every kernel launch of a loss call
- * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk) is bracketed by HIP events on the call's
+ * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk), and all launches of one ckl_embed,
+ * ckl_embed_bwd or ckl_sample call together, are bracketed by HIP events on the call's
  * stream.  ckl_timing_query waits for the recorded events and returns the
  * summed milliseconds and launch count of one kernel kind: 0 logits GEMM,
  * 1 row pass, 2 dH GEMM, 3 dH split reduce, 4 dW GEMM, 5 other, 6 top-K
- * (ckl_topk).  Not for concurrent use from several threads. */
+ * (ckl_topk), 7 embedding, 8 sampling.  Not for concurrent use from several threads. */
 int ckl_timing_enable(int on);
 int ckl_timing_query(int kind, double* total_ms, int64_t* launches);
 
