@@ -17,7 +17,7 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 PASSES = {"fused": 0, "fwd": 1, "bwd": 2}
 TIMING_KINDS = {"logits": 0, "rows": 1, "dh": 2, "dh_reduce": 3, "dw": 4, "other": 5, "topk": 6, "embed": 7,
-                "sample": 8}
+                "sample": 8, "fp8": 9}
 
 _lib = None
 
@@ -72,6 +72,10 @@ def lib():
     L.ckl_embed_bwd_workspace.restype = ctypes.c_int
     L.ckl_sample.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, ctypes.POINTER(Sampling), vp, vp, vp]
     L.ckl_sample.restype = ctypes.c_int
+    L.ckl_quantize_fp8.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, vp, vp]
+    L.ckl_quantize_fp8.restype = ctypes.c_int
+    L.ckl_matmul_fp8.argtypes = [ctypes.c_int, vp, vp, vp, vp, i64, i64, i64, vp, vp]
+    L.ckl_matmul_fp8.restype = ctypes.c_int
     L.ckl_release_workspace.argtypes = []
     L.ckl_release_workspace.restype = None
     L.ckl_workspace_bytes_held.argtypes = []

@@ -14,8 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libckl.so")
-SOURCES = ["ckl_api.hip", "kernels_embed.hip", "kernels_gemm.hip", "kernels_logits.hip", "kernels_rows.hip",
-           "kernels_sample.hip", "kernels_topk.hip"]
+SOURCES = ["ckl_api.hip", "kernels_embed.hip", "kernels_fp8.hip", "kernels_gemm.hip", "kernels_logits.hip",
+           "kernels_rows.hip", "kernels_sample.hip", "kernels_topk.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -291,7 +291,7 @@ struct TraceRange {
 };
 
 // ------------------------------------------------------------------ timing
-enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_KINDS };
+enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_KINDS };
 struct TimingState {
   bool on = false;
   std::vector<std::pair<hipEvent_t, hipEvent_t>> pool;
@@ -687,6 +687,46 @@ int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_
   try {
     Timed t(T_SAMPLE, stream);
     CKL_TRY(launch_sample(to_dt(dtype), logits, N, V, row_stride, u, p, ids_out, logp_out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t block_rows, uint8_t* q_out,
+                     float* scales_out, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return CKL_EINVAL;
+  if (R < 0 || C <= 0 || (block_rows != 1 && block_rows != 128)) return CKL_EINVAL;
+  if (C % 16 != 0 || C > (int64_t)1 << 20 || R > (int64_t)1 << 26) return CKL_EUNSUPPORTED;
+  const int64_t blocks = (C + 127) / 128 * (block_rows == 1 ? (R + 15) / 16 : (R + 127) / 128);
+  if (blocks >= kMaxBlocks256) return CKL_EUNSUPPORTED;
+  if (R == 0) return CKL_OK;
+  if (!x || !q_out || !scales_out) return CKL_EINVAL;
+  if (!aligned(x, 16) || !aligned(q_out, 16) || !aligned(scales_out, 4)) return CKL_EINVAL;
+  try {
+    Timed t(T_FP8, stream);
+    CKL_TRY(launch_quantize_fp8(to_dt(dtype), x, R, C, block_rows == 1, q_out, scales_out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_matmul_fp8(int out_dtype, const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
+                   int64_t V, int64_t d, void* out, hipStream_t stream) {
+  if (!dtype_ok(out_dtype)) return CKL_EINVAL;
+  if (M < 0 || V <= 0 || d <= 0) return CKL_EINVAL;
+  if (d % 16 != 0 || d > (int64_t)1 << 20 || V > (int64_t)1 << 26 || M > (int64_t)1 << 26) return CKL_EUNSUPPORTED;
+  // tiles of any size the product takes, by the smallest
+  if ((V + 63) / 64 * ((M + 63) / 64) >= (int64_t)1 << 26) return CKL_EUNSUPPORTED;
+  if (M == 0) return CKL_OK;
+  if (!xq || !xs || !wq || !ws || !out) return CKL_EINVAL;
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(xs, 4) || !aligned(ws, 4) ||
+      !aligned(out, out_dtype == CKL_DTYPE_BF16 ? 2 : 4))
+    return CKL_EINVAL;
+  try {
+    Timed t(T_FP8, stream);
+    CKL_TRY(launch_matmul_fp8(to_dt(out_dtype), xq, xs, wq, ws, M, V, d, out, stream));
     return CKL_OK;
   } catch (...) {
     return CKL_EHIP;

@@ -114,6 +114,14 @@ struct SampleParams {
 hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t ld, const float* u,
                          const SampleParams& p, int32_t* ids, float* logp, hipStream_t s);
 
+// e4m3 values and their scales: per 1 x 128 block (rows; scales [ceil(C / 128), R])
+// or per 128 x 128 block (scales [ceil(R / 128), ceil(C / 128)]), see kernels_fp8.hip.
+hipError_t launch_quantize_fp8(Dtype dt, const void* x, int64_t R, int64_t C, bool rows, uint8_t* q, float* scales,
+                               hipStream_t s);
+// out [M, V] = the product of the rows xq (1 x 128 scales) with the weight wq (128 x 128 scales).
+hipError_t launch_matmul_fp8(Dtype out_dt, const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                             int64_t M, int64_t V, int64_t d, void* out, hipStream_t s);
+
 // Valid-token count n and scale 1/n (0 if n = 0) into scal (int64 n, float s).
 hipError_t launch_mask_count(const uint8_t* mask, int64_t N, void* scal, hipStream_t s);
 // Compaction of the chunk whose mask, H rows, ids and teacher logits start at

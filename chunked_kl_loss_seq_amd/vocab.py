@@ -1,5 +1,6 @@
 """Operators around the vocabulary table W [V, d], beside the loss at its head:
-the embedding lookup and its gradient, and sampling tokens from logits.
+the embedding lookup and its gradient, sampling tokens from logits, and the
+head's product with a weight held in 8 bits.
 
 Argument checks and marshalling only, as in ``binding``: every step runs in the
 library's HIP kernels on the current stream of the tensors' device, and CPU
@@ -10,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-from .binding import DTYPE_BF16, DTYPE_F32, Sampling, _check, _check_out, _ptr, _stream, lib
+from .binding import DTYPE_BF16, DTYPE_F32, Sampling, _check, _check_out, _ptr, _stream, lib, topk
 
 
 def _dtype(torch, t, name):
@@ -182,3 +183,99 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids_out=No
         _check(lib().ckl_sample(dt, _ptr(logits), N, V, logits.stride(0) if N > 1 else V, _ptr(u), ctypes.byref(how),
                                 _ptr(ids_out), _ptr(logp_out), _stream(torch, dev)), "ckl_sample")
     return ids_out, logp_out
+
+
+def quantize_fp8(x, block_rows=1):
+    """(q float8_e4m3fn [R, C], scales float32): x in 8 bits, an element being q times
+    the scale of its block.
+
+    ``block_rows`` = 1 (rows, activations): one scale per 1 x 128 block, scales
+    [ceil(C / 128), R]; 128 (a weight): one per 128 x 128 block, scales
+    [ceil(R / 128), ceil(C / 128)].  scale = amax / 448, q rounded to nearest
+    even; values that are not finite become NaN.  x is bfloat16 or float32,
+    contiguous, C a multiple of 16.
+    """
+    import torch
+
+    dev = _gpu(x, "x")
+    dt = _dtype(torch, x, "x")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [R, C] tensor")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    R, C = x.shape
+    kb = -(-C // 128)
+    q = torch.empty((R, C), dtype=torch.float8_e4m3fn, device=dev)
+    scales = torch.empty((kb, R) if block_rows == 1 else (-(-R // 128), kb), dtype=torch.float32, device=dev)
+    with _on(torch, dev):
+        _check(lib().ckl_quantize_fp8(dt, _ptr(x), R, C, block_rows, _ptr(q), _ptr(scales), _stream(torch, dev)),
+               "ckl_quantize_fp8")
+    return q, scales
+
+
+def _check_fp8(torch, q, scales, shape, name, dev):
+    if q.dtype != torch.float8_e4m3fn or q.dim() != 2 or not q.is_contiguous() or q.device != dev:
+        raise ValueError(f"{name}q must be a contiguous 2-D float8_e4m3fn tensor on {dev}")
+    _check_out(torch, scales, shape, torch.float32, dev, f"{name}s")
+
+
+def matmul_fp8(xq, xs, wq, ws, dtype=None, out=None):
+    """xq [M, d] times the transposed weight wq [V, d], both in 8 bits with the scales
+    ``quantize_fp8`` gives (rows, and a weight): [M, V] in ``dtype`` (bfloat16 if
+    None, or float32), summed in fp32 and rounded once.  No gradient."""
+    import torch
+
+    dev = _gpu(xq, "xq")
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError("xq must be [M, d] and wq [V, d]")
+    (M, d), V = xq.shape, wq.shape[0]
+    kb = -(-d // 128)
+    _check_fp8(torch, xq, xs, (kb, M), "x", dev)
+    _check_fp8(torch, wq, ws, (-(-V // 128), kb), "w", dev)
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be bfloat16 or float32")
+    _check_out(torch, out, (M, V), dtype, dev, "out")
+    if out is None:
+        out = torch.empty((M, V), dtype=dtype, device=dev)
+    dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
+    with _on(torch, dev):
+        _check(lib().ckl_matmul_fp8(dt, _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), M, V, d, _ptr(out),
+                                    _stream(torch, dev)), "ckl_matmul_fp8")
+    return out
+
+
+def logits_fp8(H, wq, ws, dtype=None, out=None):
+    """Logits [M, V] of hidden states H [M, d] (bfloat16 or float32) under a head held
+    in 8 bits (``wq``, ``ws`` = ``quantize_fp8(W, 128)``, once): H's rows are
+    quantised in the call, then ``matmul_fp8``."""
+    xq, xs = quantize_fp8(H)
+    return matmul_fp8(xq, xs, wq, ws, dtype=dtype, out=out)
+
+
+def teacher_topk(H, wq, ws, K, chunk=0):
+    """The teacher cache of hidden states H [N, d] under a head held in 8 bits: (ids
+    int32 [N, K], values float32 [N, K]) as ``topk`` of their bfloat16 logits.
+
+    Positions go in chunks (``chunk`` rows; 0: about 1 GiB of logits), so the
+    N x V logits are never held at once.
+    """
+    import torch
+
+    dev = _gpu(H, "H")
+    if H.dim() != 2 or wq.dim() != 2:
+        raise ValueError("H must be [N, d] and wq [V, d]")
+    N, V, K, chunk = H.shape[0], wq.shape[0], int(K), int(chunk)
+    if chunk < 0 or K < 1 or K > V:
+        raise ValueError("chunk must be at least 0 and K in 1 .. V")
+    if chunk == 0:
+        chunk = max(256, (1 << 30) // (2 * V) // 256 * 256)
+    ids = torch.empty((N, K), dtype=torch.int32, device=dev)
+    vals = torch.empty((N, K), dtype=torch.float32, device=dev)
+    logits = torch.empty((min(chunk, N), V), dtype=torch.bfloat16, device=dev)
+    for r in range(0, N, chunk):
+        n = min(chunk, N - r)
+        logits_fp8(H[r:r + n], wq, ws, out=logits[:n])
+        topk(logits[:n], K, ids_out=ids[r:r + n], vals_out=vals[r:r + n])
+    return ids, vals

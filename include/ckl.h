@@ -264,6 +264,33 @@ typedef struct ckl_sampling {
 int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const float* u,
                const ckl_sampling* how, int32_t* ids_out, float* logp_out, hipStream_t stream);
 
+/* Matrix product in 8-bit floating point (OCP e4m3) with an fp32 scale per
+ * block of 128, for a head whose weight is held in 8 bits (a teacher's logits
+ * for ckl_topk, a served student's for ckl_sample).  A value is q x its
+ * block's scale.
+ *   rows    [R, C] with block_rows = 1: scales [ceil(C / 128), R], one per
+ *           1 x 128 block, blocks of columns outermost
+ *   weight  [R, C] with block_rows = 128: scales [ceil(R / 128), ceil(C / 128)]
+ * ckl_quantize_fp8: scale = amax / 448 of the block's finite values (1 for a
+ * block of zeros, at least 2^-126), q = x / scale rounded to nearest even;
+ * values that are not finite become NaN, and only they.
+ *   dtype     ckl_dtype of x (16-byte aligned, as q_out)
+ *   C         a multiple of 16, at most 2^20; the last block of 128 columns
+ *             and of 128 rows may be short */
+int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t block_rows, uint8_t* q_out,
+                     float* scales_out, hipStream_t stream);
+
+/* out[m][v] = sum over blocks kb of xs[kb][m] ws[v / 128][kb]
+ *             (sum over k of block kb of xq[m][k] wq[v][k]),
+ * block sums and the sum over blocks in fp32, rounded once to out_dtype.
+ *   xq, xs    [M, d] and [ceil(d / 128), M], as ckl_quantize_fp8 writes rows
+ *   wq, ws    [V, d] and [ceil(V / 128), ceil(d / 128)], as it writes a weight
+ *   out       [M, V] in out_dtype (overwritten)
+ * xq and wq 16-byte aligned; d a multiple of 16, at most 2^20; V and M at most
+ * 2^26, and at most 2^26 tiles of 64 x 64.  No workspace, no gradient. */
+int ckl_matmul_fp8(int out_dtype, const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
+                   int64_t V, int64_t d, void* out, hipStream_t stream);
+
 /* Chunk planner of the fused call (pure host computation, needs no GPU).  The
  * sequence is cut into chunks of C rows so that the loss's own device memory
  * stays bounded independently of N ("A New Trick...", section "Does this
@@ -316,11 +343,12 @@ int ckl_debug_rows(const float* Z, const int32_t* idx, const float* tlogit, cons
 
 /* Measurement support.  While enabled, every kernel launch of a loss call
  * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk), and all launches of one ckl_embed,
- * ckl_embed_bwd or ckl_sample call together, are bracketed by HIP events on the call's
- * stream.  ckl_timing_query waits for the recorded events and returns the
+ * ckl_embed_bwd, ckl_sample, ckl_quantize_fp8 or ckl_matmul_fp8 call together, are
+ * bracketed by HIP events on the call's stream.  ckl_timing_query waits for the recorded events and returns the
  * summed milliseconds and launch count of one kernel kind: 0 logits GEMM,
  * 1 row pass, 2 dH GEMM, 3 dH split reduce, 4 dW GEMM, 5 other, 6 top-K
- * (ckl_topk), 7 embedding, 8 sampling.  Not for concurrent use from several threads. */
+ * (ckl_topk), 7 embedding, 8 sampling, 9 8-bit products and
+ * quantisers.  Not for concurrent use from several threads. */
 int ckl_timing_enable(int on);
 int ckl_timing_query(int kind, double* total_ms, int64_t* launches);
 

@@ -63,3 +63,33 @@ def test_sample_frequencies_are_the_probabilities():
 ])
 def test_sample_edges(x, u, want):
     assert O.sample_row(np.array(x), u)[0] == want
+
+
+def test_e4m3_values_and_rounding():
+    v = O.e4m3_values()
+    assert v[0] == 0 and v[1] == 2.0 ** -9 and v[8] == 2.0 ** -6 and v[56] == 1.0 and v[-1] == 448.0
+    assert np.all(np.diff(v) > 0)
+    np.testing.assert_array_equal(O.e4m3_codes(v), np.arange(127))
+    np.testing.assert_array_equal(O.e4m3_codes(-v[1:]), np.arange(1, 127) | 128)
+    # halfway to the even code, a hair beyond to the nearer one
+    assert O.e4m3_codes(np.array([1.0625, 1.1875, 1.0625 + 1e-9, 1.1875 - 1e-9])).tolist() == [56, 58, 57, 57]
+    assert O.e4m3_codes(np.array([2.0 ** -10, 3 * 2.0 ** -10, 448.00003, np.nan])).tolist() == [0, 2, 126, 127]
+
+
+def test_e4m3_against_torch():
+    torch = pytest.importorskip("torch")
+    x = np.random.default_rng(0).standard_normal(20000).astype(np.float32) * np.float32(60)
+    x = np.clip(np.concatenate([x, x * np.float32(1e-4)]), -448, 448)
+    np.testing.assert_array_equal(torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy(), O.e4m3_codes(x))
+
+
+def test_quantize_round_trip():
+    # each value comes back within half a step of its block's scale: 2^-4 of it, or 2^-10 scales
+    x = np.random.default_rng(1).standard_normal((200, 300)).astype(np.float32)
+    x[7] = 0
+    for rows in (1, 128):
+        codes, scales = O.quantize(x, rows)
+        back = O.dequantize(codes, scales, rows)
+        s = np.repeat(np.repeat((scales.T if rows == 1 else scales), rows, 0)[:200], 128, 1)[:, :300]
+        assert np.all(np.abs(back - x) <= np.maximum(np.abs(x) * 2.0 ** -4, s * 2.0 ** -10) * (1 + 1e-6))
+        assert np.max(np.abs(back)) >= 0.999 * np.max(np.abs(x))
