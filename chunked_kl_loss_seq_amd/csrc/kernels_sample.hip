@@ -35,13 +35,14 @@ namespace ckl {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 4096;
 constexpr int kPerThread = kBins / kThreads;
 constexpr int kCap = 2048;      // tokens held in LDS
 constexpr int kFastK = 512;     // largest k of the collected path
 constexpr int kTopBits = 13;    // key bits of the histogram of the threads' maxima
+constexpr int kFlight = 4;      // 16-byte loads of a thread in flight
 constexpr int kSub = 256;       // digits of a narrowing pass
 static_assert((1 << kTopBits) * 4 <= kBins * 8, "the maxima's histogram lives in the mass histogram");
 
@@ -81,38 +82,25 @@ struct Key<float> {
 __device__ inline uint64_t pack(uint32_t key, uint32_t id) { return ((uint64_t)key << 32) | (0xFFFFFFFFu - id); }
 __device__ inline uint32_t unpack_id(uint64_t c) { return 0xFFFFFFFFu - (uint32_t)c; }
 
-// A row as 16-byte chunks of its aligned memory: chunk c holds the elements
-// c kN - off .. + kN - 1, off = the elements between the aligned address and
-// the row's first one.  The first and the last chunk may reach outside the
-// row and are put together from element loads, the others are one load.
+// A row as its 16-byte aligned chunks, `nb` of them, with the fewer than kN
+// elements before the first one and after the last one apart.
 template <typename T>
 struct Row {
   static constexpr int kN = 16 / (int)sizeof(T);
   const T* x;
-  const u32x4_t* base;
+  const u32x4_t* body;
   int64_t V;
-  int off;
-  uint32_t chunks;
+  int head, tail;
+  uint32_t nb;
   __device__ inline Row(const T* row, int64_t v) : x(row), V(v) {
-    off = (int)(((uintptr_t)row & 15) / sizeof(T));
-    base = (const u32x4_t*)((uintptr_t)row & ~(uintptr_t)15);
-    chunks = (uint32_t)((v + off + kN - 1) / kN);
+    const int skip = (int)((0 - (uintptr_t)row) & 15) / (int)sizeof(T);
+    head = skip < v ? skip : (int)v;
+    nb = (uint32_t)((v - head) / kN);
+    tail = (int)(v - head - (int64_t)nb * kN);
+    body = (const u32x4_t*)(row + head);
   }
-  __device__ inline bool edge(uint32_t c) const {
-    return (c == 0 && off != 0) || (c == chunks - 1 && (V + off) % kN != 0);
-  }
-  // the chunk's values; outside the row -inf
-  __device__ inline void load(uint32_t c, float* f) const {
-    if (edge(c)) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const int64_t e = (int64_t)c * kN + i - off;
-        f[i] = (e >= 0 && e < V) ? (float)x[e] : -INFINITY;
-      }
-      return;
-    }
-    unpack(base[c], f);
-  }
+  __device__ inline int64_t body_id(uint32_t c) const { return head + (int64_t)c * kN; }
+  __device__ inline int64_t tail_id() const { return body_id(nb); }
   __device__ static inline void unpack(const u32x4_t& v, float* f) {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -129,35 +117,44 @@ struct Row {
       }
     }
   }
-  __device__ inline int64_t id(uint32_t c, int i) const { return (int64_t)c * kN + i - off; }
 };
 
-// Every value of the row as fn(value, id): the chunks of a thread in turn,
-// four loads in flight.
-template <typename T, typename F>
-__device__ inline void for_each(const Row<T>& row, F&& fn) {
-  constexpr int kN = Row<T>::kN;
-  constexpr int U = 4;
-  for (uint32_t c0 = threadIdx.x; c0 < row.chunks; c0 += U * kThreads) {
-    u32x4_t v[U];
+// Every chunk of the row as chunk(words, index), the chunks of a thread in
+// turn with kFlight loads in flight each (past the end the last chunk is loaded
+// again and left out: a load under a condition would wait for the one before),
+// and every element apart as one(element, id).
+template <int kFlight, typename T, typename C, typename O>
+__device__ inline void for_each_chunk(const Row<T>& row, C&& chunk, O&& one) {
+  const uint32_t tid = threadIdx.x;
+  for (uint32_t c0 = tid; c0 < row.nb; c0 += kFlight * kThreads) {
+    u32x4_t v[kFlight];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
+    for (int j = 0; j < kFlight; ++j) {
       const uint32_t c = c0 + j * kThreads;
-      if (c < row.chunks && !row.edge(c)) v[j] = row.base[c];
+      v[j] = row.body[c < row.nb ? c : row.nb - 1];
     }
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
+    for (int j = 0; j < kFlight; ++j) {
       const uint32_t c = c0 + j * kThreads;
-      if (c >= row.chunks) break;
-      float f[kN];
-      if (row.edge(c))
-        row.load(c, f);
-      else
-        Row<T>::unpack(v[j], f);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) fn(f[i], row.id(c, i));
+      if (c < row.nb) chunk(v[j], c);
     }
   }
+  if (tid < (uint32_t)row.head) one(row.x[tid], (int64_t)tid);
+  if (tid < (uint32_t)row.tail) one(row.x[row.tail_id() + tid], row.tail_id() + tid);
+}
+
+// Every value of the row as fn(value, id).
+template <typename T, typename F>
+__device__ inline void for_each(const Row<T>& row, F&& fn) {
+  for_each_chunk<kFlight>(
+      row,
+      [&](const u32x4_t& v, uint32_t c) {
+        float f[Row<T>::kN];
+        Row<T>::unpack(v, f);
+#pragma unroll
+        for (int i = 0; i < Row<T>::kN; ++i) fn(f[i], row.body_id(c) + i);
+      },
+      [&](T x, int64_t id) { fn((float)x, id); });
 }
 
 // The masses of one row.  y = -64 log2(e) of a logit; a bin is floor(y).
@@ -171,23 +168,33 @@ struct Scale {
   }
 };
 
-// 2^(-f / 64) for f in [0, 1): the exponential series, off by at most
-// (ln 2 / 64)^6 / 720 = 2.2e-15.
+// 2^(-f / 64) for f in [0, 1): the polynomial of degree 4 through the Chebyshev
+// points of [0, 1], its constant moved to 1 so that f = 0 is exact; off by at
+// most 5e-15.
 __device__ inline double pow_frac(double f) {
-  const double t = f * -0.010830424696249145;  // -ln 2 / 64
-  double r = 1.0 / 120.0;
-  r = __builtin_fma(r, t, 1.0 / 24.0);
-  r = __builtin_fma(r, t, 1.0 / 6.0);
-  r = __builtin_fma(r, t, 0.5);
-  r = __builtin_fma(r, t, 1.0);
-  return __builtin_fma(r, t, 1.0);
+  double r = 5.701897951327709e-10;
+  r = __builtin_fma(r, f, -2.1172866563406743e-07);
+  r = __builtin_fma(r, f, 5.864904858456656e-05);
+  r = __builtin_fma(r, f, -0.010830424696128419);
+  return __builtin_fma(r, f, 1.0);
 }
-__device__ inline double bin_top(int b) { return exp2(-(double)b / 64.0); }
+
+// Room for the block-wide reductions, and a table for mass_of.
+struct Red {
+  double d[kWaves];
+  uint32_t u[kWaves];
+  float f[kWaves];
+  double pow64[64];  // 2^(-j / 64)
+};
+__device__ inline void fill_pow64(Red& red) {
+  if (threadIdx.x < 64) red.pow64[threadIdx.x] = exp2(-(double)threadIdx.x / 64.0);
+}
+__device__ inline double bin_top(const Red& red, int b) { return ldexp(red.pow64[b & 63], -(b >> 6)); }
 // e of a logit whose y is below kBins, else 0
-__device__ inline double mass_of(double y) {
+__device__ inline double mass_of(const Red& red, double y) {
   if (!(y < (double)kBins)) return 0.0;
   const double b = floor(y);
-  return bin_top((int)b) * pow_frac(y - b);
+  return bin_top(red, (int)b) * pow_frac(y - b);
 }
 
 struct Shared {
@@ -196,68 +203,80 @@ struct Shared {
   uint64_t cand[kCap];        // collected (key, id)
   uint64_t sub_mass[kSub];    // a narrowing pass
   uint32_t sub_count[kSub];
-  double red_d[kWaves];
-  uint32_t red_u[kWaves];
-  float red_f[kWaves];
+  Red red;
   uint64_t edge_mass;         // mass of the tokens of min_p's bin that reach it
   uint32_t n_cand;
   uint32_t pick;
+  uint32_t nth[2];
   double pick_mass;           // mass above the chosen bin or digit
   uint32_t pick_count;        // tokens above it
   double got_mass;
 };
 
-__device__ inline float block_max(float v, Shared& sh) {
+__device__ inline float block_max(float v, Red& red) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh.red_f[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) red.f[threadIdx.x >> 6] = v;
   __syncthreads();
-  float m = sh.red_f[0];
+  float m = red.f[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.red_f[i]);
+  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, red.f[i]);
   return m;
 }
 
-// Sum of v over the threads before this one, and over all of them: one fixed
-// order, and a thread's sum plus its value is the next thread's sum exactly.
-__device__ inline double block_prefix(double v, Shared& sh, double* before) {
+// Inclusive sum over the lanes of a wave (lane order, one fixed order of
+// additions): four steps within rows of 16 lanes, two across them.
+template <int kCtrl, int kRows>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xF, false);
+}
+template <int kCtrl, int kRows>
+__device__ inline double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = dpp<kCtrl, kRows>((uint32_t)b), hi = dpp<kCtrl, kRows>((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <typename N>
+__device__ inline N wave_scan(N x) {
+  x += dpp<0x111, 0xF>(x);  // row_shr:1
+  x += dpp<0x112, 0xF>(x);
+  x += dpp<0x114, 0xF>(x);
+  x += dpp<0x118, 0xF>(x);
+  x += dpp<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+  x += dpp<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
+// Sum of v over the threads before this one (thread order), and over all of
+// them, in one fixed order.
+__device__ inline double block_prefix(double v, Red& red, double* before) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  double x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
+  const double x = wave_scan(v);
   __syncthreads();
-  if (lane == 63) sh.red_d[w] = x;
+  if (lane == 63) red.d[w] = x;
   __syncthreads();
   double base = 0.0, all = 0.0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     if (i == w) base = all;
-    all += sh.red_d[i];
+    all += red.d[i];
   }
   const double prev = __shfl_up(x, 1);
   *before = lane == 0 ? base : base + prev;
   return all;
 }
-__device__ inline uint32_t block_prefix(uint32_t v, Shared& sh, uint32_t* before) {
+__device__ inline uint32_t block_prefix(uint32_t v, Red& red, uint32_t* before) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  uint32_t x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
+  const uint32_t x = wave_scan(v);
   __syncthreads();
-  if (lane == 63) sh.red_u[w] = x;
+  if (lane == 63) red.u[w] = x;
   __syncthreads();
   uint32_t base = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     if (i == w) base = all;
-    all += sh.red_u[i];
+    all += red.u[i];
   }
   *before = base + x - v;
   return all;
@@ -313,16 +332,16 @@ __device__ inline bool reached(int kind, uint32_t count, double mass, uint32_t k
 template <typename T>
 __device__ inline int pick_in_list(Shared& sh, int n, const Scale& sc, int kind, uint32_t k, double target,
                                    double above, uint32_t above_n, double* mass) {
-  constexpr int kEach = kCap / kThreads;
+  constexpr int kEach = kCap / kThreads;  // tokens of a thread
   double e[kEach], mine = 0.0;
   const int b = threadIdx.x * kEach;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    e[i] = b + i < n ? mass_of(sc.y(Key<T>::value((uint32_t)(sh.cand[b + i] >> 32)))) : 0.0;
+    e[i] = b + i < n ? mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(sh.cand[b + i] >> 32)))) : 0.0;
     mine += e[i];
   }
   double before = 0.0;
-  block_prefix(mine, sh, &before);
+  block_prefix(mine, sh.red, &before);
   if (threadIdx.x == 0) sh.pick = 0xFFFFFFFFu;
   __syncthreads();
   double run = above + before;
@@ -346,6 +365,155 @@ __device__ inline int pick_in_list(Shared& sh, int n, const Scale& sc, int kind,
   return j;
 }
 
+// Which values of a 16-byte chunk equal l (bit i: value i).
+__device__ inline uint32_t equal_in(const u32x4_t& v, float l, float*) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = v[i];
+    m |= (uint32_t)(__builtin_bit_cast(float, w) == l) << i;
+  }
+  return m;
+}
+__device__ inline uint32_t equal_in(const u32x4_t& v, float l, __bf16*) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = v[i];
+    m |= (uint32_t)(__builtin_bit_cast(float, w << 16) == l) << (2 * i);
+    m |= (uint32_t)(__builtin_bit_cast(float, w & 0xFFFF0000u) == l) << (2 * i + 1);
+  }
+  return m;
+}
+// Whether any may: no more for fp32; for bf16 one test for pairs (l's bits in
+// both halves; 0 stands for either zero).
+__device__ inline bool may_equal(const u32x4_t& v, float l, float* t) { return equal_in(v, l, t) != 0; }
+__device__ inline bool may_equal(const u32x4_t& v, float l, __bf16*) {
+  const uint32_t h = __builtin_bit_cast(uint32_t, l) >> 16;
+  const uint32_t mask = l == 0.f ? 0x7FFF7FFFu : 0xFFFFFFFFu, want = l == 0.f ? 0u : h << 16 | h;
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 z = {0xFFFF, 0xFFFF};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = v[i];
+    z = __builtin_elementwise_min(z, __builtin_bit_cast(u16x2, (w & mask) ^ want));
+  }
+  return z[0] == 0 || z[1] == 0;
+}
+
+// The id of the r-th token (r >= 1) of logit l in id order, in every thread.
+// A wave reads 64 chunks at once; the equal logits of every such piece (or
+// group of pieces, in long rows) are counted until r are passed, then every
+// wave alike goes through the group that holds the r-th.  cnt: kGroups words of LDS, pick: two.
+constexpr int kGroups = 2 * kThreads;
+template <typename T>
+__device__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l, uint32_t r) {
+  constexpr int U = kFlight;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  // the r-th set bit of a mask of lanes
+  auto nth_lane = [](uint64_t m, uint32_t n) {
+    for (; n > 1; --n) m &= m - 1;
+    return __builtin_ctzll(m);
+  };
+  {
+    const uint64_t m = __ballot(lane < row.head && (float)row.x[lane < row.head ? lane : 0] == l);
+    const uint32_t n = (uint32_t)__popcll(m);
+    if (r <= n) return nth_lane(m, r);
+    r -= n;
+  }
+  if (row.nb > 0) {
+    const uint32_t pieces = (row.nb + 63) / 64;
+    int shift = 0;
+    while (((pieces - 1) >> shift) >= (uint32_t)kGroups) ++shift;
+    const uint32_t groups = ((pieces - 1) >> shift) + 1;
+    __syncthreads();
+    for (uint32_t g = groups + tid; g < (uint32_t)kGroups; g += kThreads) cnt[g] = 0;  // the last round's rest
+    if (tid == 0) pick[0] = 0;
+    // rounds of U groups a wave, in order: after each, stop if the r-th is past
+    uint32_t done = 0;
+    while (done < groups) {
+      const uint32_t g0 = done + w;
+      uint32_t n[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) n[j] = 0;
+      for (uint32_t s = 0; s < (1u << shift); ++s) {
+        u32x4_t v[U];
+        uint32_t c[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          c[j] = (((g0 + j * kWaves) << shift) + s) * 64 + lane;
+          v[j] = row.body[c[j] < row.nb ? c[j] : row.nb - 1];
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const bool may = c[j] < row.nb && may_equal(v[j], l, (T*)nullptr);
+          if (__ballot(may) == 0) continue;
+          const uint32_t m = may ? equal_in(v[j], l, (T*)nullptr) : 0;
+#pragma unroll
+          for (int i = 0; i < Row<T>::kN; ++i) n[j] += (uint32_t)__popcll(__ballot((m >> i) & 1u));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (lane == 0 && g0 + j * kWaves < groups) cnt[g0 + j * kWaves] = n[j];
+      uint32_t sum = 0;
+#pragma unroll
+      for (int j = 0; j < U; ++j) sum += n[j];
+      __syncthreads();  // pick[0] is clear (first round), or read by all (later ones)
+      if (lane == 0 && sum) atomicAdd(&pick[0], sum);
+      __syncthreads();
+      done += U * kWaves;
+      if (pick[0] >= r) break;
+    }
+    // groups not reached count as empty
+    const uint32_t a = 2 * tid < done ? cnt[2 * tid] : 0, b = 2 * tid + 1 < done ? cnt[2 * tid + 1] : 0;
+    uint32_t before = 0;
+    const uint32_t total = block_prefix(a + b, red, &before);
+    if (before < r && before + a + b >= r) {
+      const bool second = before + a < r;
+      pick[0] = 2 * tid + (second ? 1 : 0);
+      pick[1] = before + (second ? a : 0);
+    }
+    __syncthreads();
+    if (r <= total) {
+      const uint32_t g = pick[0];
+      uint32_t seen = pick[1];
+      for (uint32_t s = 0; s < (1u << shift); ++s) {
+        const uint32_t c = ((g << shift) + s) * 64 + lane;
+        uint32_t m = equal_in(row.body[c < row.nb ? c : row.nb - 1], l, (T*)nullptr);
+        if (c >= row.nb) m = 0;
+        const uint32_t mine = (uint32_t)__popc(m), upto = seen + wave_scan(mine);
+        const uint64_t here = __ballot(upto - mine < r && upto >= r);
+        if (here) {
+          for (uint32_t skip = r - 1 - (upto - mine); skip > 0 && m; --skip) m &= m - 1;
+          const int at = __builtin_ctzll(here);
+          return row.body_id(__shfl(c, at)) + __shfl(m ? __builtin_ctz(m) : 0, at);
+        }
+        seen = __shfl(upto, 63);
+      }
+    }
+    r -= total;
+  }
+  const uint64_t m = __ballot(lane < row.tail && (float)row.x[lane < row.tail ? row.tail_id() + lane : 0] == l);
+  return row.tail_id() + nth_lane(m, r);
+}
+
+// The smallest r in [1, n] for which above + r e reaches the target, n if none:
+// how many of n equal logits a border takes.
+__device__ inline uint32_t equal_taken(int kind, uint32_t n, uint32_t above_n, double above, double e, uint32_t k,
+                                       double target) {
+  if (kind == BY_COUNT) return k > above_n ? (k - above_n < n ? k - above_n : n) : 1;
+  uint32_t lo = 1, hi = n;
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (reached(kind, 0, above + (double)mid * e, 0, target))
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
 // Where a border lies: the mass of the prefix that ends there, and the last
 // token of that prefix.
 struct Found {
@@ -365,12 +533,12 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
   for (int i = 0; i < kPerThread; ++i) {
     const int b = tid * kPerThread + i;
     const uint64_t q = sh.mass[b];
-    m[i] = q ? (double)q / sc.fix * bin_top(b) : 0.0;
+    m[i] = q ? (double)q / sc.fix * bin_top(sh.red, b) : 0.0;
     mine += m[i];
     cmine += sh.count[b];
   }
-  block_prefix(mine, sh, &before);
-  if (kind == BY_COUNT) block_prefix(cmine, sh, &cbefore);
+  block_prefix(mine, sh.red, &before);
+  if (kind == BY_COUNT) block_prefix(cmine, sh.red, &cbefore);
   if (tid == 0) sh.pick = 0xFFFFFFFFu;
   __syncthreads();
   // the first bin at whose end the border is reached, else the last with mass
@@ -415,7 +583,7 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
   __syncthreads();
   double above = sh.pick_mass;
   uint32_t above_n = sh.pick_count;
-  const double top = bin_top(bin), y0 = (double)bin, y1 = (double)(bin + 1);
+  const double top = bin_top(sh.red, bin), y0 = (double)bin, y1 = (double)(bin + 1);
   // a float interval around the bin's logits: a cheap first test of each value
   // (c may be 0 or tiny: the interval is then the whole line)
   float lo = -INFINITY, hi = INFINITY;
@@ -441,7 +609,7 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
     for_each(row, [&](float l, int64_t id) {
       if (in_bin(l)) {
         const uint32_t key = Key<T>::of(l);
-        if ((key & prefix_mask) == prefix && id >= 0 && id < row.V) {
+        if ((key & prefix_mask) == prefix) {
           const uint32_t slot = atomicAdd(&sh.n_cand, 1u);
           if (slot < (uint32_t)kCap) sh.cand[slot] = pack(key, (uint32_t)id);
         }
@@ -468,7 +636,7 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
     for_each(row, [&](float l, int64_t id) {
       if (in_bin(l)) {
         const uint32_t key = Key<T>::of(l);
-        if ((key & prefix_mask) == prefix && id >= 0 && id < row.V) {
+        if ((key & prefix_mask) == prefix) {
           const double y = sc.y(l);
           const uint32_t dg = 255u - ((key >> digits_left) & 255u);
           atomicAdd((unsigned long long*)&sh.sub_mass[dg], (unsigned long long)(pow_frac(y - y0) * sc.fix + 0.5));
@@ -481,8 +649,8 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
     const uint32_t dc = tid < kSub ? sh.sub_count[tid] : 0;
     double db = 0.0;
     uint32_t cb = 0;
-    block_prefix(dm, sh, &db);
-    block_prefix(dc, sh, &cb);
+    block_prefix(dm, sh.red, &db);
+    block_prefix(dc, sh.red, &cb);
     if (tid == 0) {
       sh.pick = 0xFFFFFFFFu;
       sh.n_cand = 0;
@@ -507,39 +675,198 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
   // them (at least 1, at most n)
   const uint32_t n = sh.n_cand;
   const float l = Key<T>::value(prefix);
-  const double e = mass_of(sc.y(l));
-  uint32_t r = 1;
-  if (kind == BY_COUNT) {
-    r = k > above_n ? k - above_n : 1;
-  } else {
-    // the smallest r in [1, n] with above + r e >= (or >) target, n if none
-    uint32_t lo_r = 1, hi_r = n;
-    while (lo_r < hi_r) {
-      const uint32_t mid = lo_r + (hi_r - lo_r) / 2;
-      if (reached(kind, 0, above + (double)mid * e, 0, target))
-        hi_r = mid;
-      else
-        lo_r = mid + 1;
-    }
-    r = lo_r;
-  }
-  if (r > n) r = n;
+  const double e = mass_of(sh.red, sc.y(l));
+  const uint32_t r = equal_taken(kind, n, above_n, above, e, k, target);
   Found f{above + (double)r * e, l, -1};
   if (!want_id) return f;
-  // the r-th of them in id order
-  uint32_t seen = 0;
-  for (int64_t base = 0; base < row.V; base += kThreads) {
-    const int64_t id = base + tid;
-    const bool eq = id < row.V && Key<T>::of((float)row.x[id]) == prefix;
-    uint32_t rank = 0;
-    const uint32_t total = block_prefix(eq ? 1u : 0u, sh, &rank);
-    if (eq && seen + rank + 1 == r) sh.pick = (uint32_t)id;
-    seen += total;
-    if (seen >= r) break;  // uniform: every thread has the same total
-  }
-  __syncthreads();
-  f.id = (int64_t)sh.pick;
+  f.id = nth_equal(row, (uint32_t*)sh.cand, sh.red, sh.nth, l, r);
   return f;
+}
+
+// ---------------------------------------------------------------- bf16 rows
+// bf16 logits have few distinct values, so a row is its count of every value:
+// one pass with a 32-bit LDS add per logit, no exponential and no maximum
+// before it, and each border is exact from count x e of the values in order.
+// Counted one by one are the magnitudes in [2^-26, 2^8) of either sign; 0 and
+// smaller ones are one count, larger ones another, so that a logit's place is
+// eight packed 16-bit operations for two logits, without a branch.  Where
+// logits beyond +-256 matter, or nonzero ones below 2^-26 do (by 1e-13 of the
+// mass, or because a border falls among them), the row is left to the general
+// path (id kLeft).
+constexpr int32_t kLeft = -2;
+struct Counted {
+  static constexpr int kLo = (127 - 26) << 7, kHi = (127 + 8) << 7;  // magnitude bits
+  static constexpr int kW = kHi - kLo;
+  // counts of one sign: 0 = below 2^-26, 1 + (bits - kLo), kW + 1 = from 2^8 on
+  // (also infinities and NaN); the negative ones follow the positive ones
+  static constexpr int kSign = kW + 2;
+  static constexpr int kCounts = 2 * kSign;
+  // slots in the order of the logits: positive values, 0, negative values
+  static constexpr int kZero = kW;
+  static constexpr int kSlots = 2 * kW + 1;
+  static constexpr int kPer = (kSlots + kThreads - 1) / kThreads;  // slots of a thread
+  static_assert(kCounts * 4 < 65536, "byte offsets fit 16 bits");
+  __device__ static inline float value(int slot) {
+    if (slot == kZero) return 0.f;
+    const uint32_t b = slot < kZero ? (uint32_t)(kHi - 1 - slot) : 0x8000u | (uint32_t)(slot - kZero - 1 + kLo);
+    return __builtin_bit_cast(float, b << 16);
+  }
+  __device__ static inline uint32_t count(const uint32_t* cnt, int slot) {
+    if (slot >= kSlots) return 0;
+    return slot < kZero ? cnt[kW - slot] : slot == kZero ? cnt[0] + cnt[kSign] : cnt[kSign + slot - kZero];
+  }
+};
+struct CountShared {
+  uint32_t cnt[Counted::kCounts];
+  Red red;
+  uint32_t first;        // the first slot with a count
+  uint32_t pick, last;   // the thread a border falls to; the last one with mass
+  uint32_t nth[2];
+  double above;          // mass and tokens before that thread's slots
+  uint32_t above_n;
+};
+static_assert(kGroups <= Counted::kCounts, "the counts of groups take the counts' place");
+
+// Two logits (the halves of w) counted.
+__device__ inline void count_pair(uint32_t w, char* cnt) {
+  typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  const i16x2 lo = {(int16_t)(Counted::kLo - 1), (int16_t)(Counted::kLo - 1)}, zero = {0, 0};
+  const i16x2 top = {(int16_t)(Counted::kW + 1), (int16_t)(Counted::kW + 1)};
+  const i16x2 sign = {(int16_t)Counted::kSign, (int16_t)Counted::kSign}, fifteen = {15, 15};
+  i16x2 at = __builtin_bit_cast(i16x2, w & 0x7FFF7FFFu) - lo;
+  at = __builtin_elementwise_max(__builtin_elementwise_min(at, top), zero);
+  at += (__builtin_bit_cast(i16x2, w) >> fifteen) & sign;
+  const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, at) << (u16x2){2, 2});
+  atomicAdd((uint32_t*)(cnt + (b & 0xFFFFu)), 1u);
+  atomicAdd((uint32_t*)(cnt + (b >> 16)), 1u);
+}
+__device__ inline void count_one(uint32_t h, uint32_t* cnt) {
+  int at = (int)(h & 0x7FFFu) - (Counted::kLo - 1);
+  at = at < 0 ? 0 : at > Counted::kW + 1 ? Counted::kW + 1 : at;
+  atomicAdd(&cnt[at + (h & 0x8000u ? Counted::kSign : 0)], 1u);
+}
+
+__device__ inline void count_row(const Row<__bf16>& row, uint32_t* cnt) {
+  for_each_chunk<8>(
+      row,
+      [&](const u32x4_t& v, uint32_t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) count_pair(v[i], (char*)cnt);
+      },
+      [&](__bf16 x, int64_t) { count_one(__builtin_bit_cast(uint16_t, x), cnt); });
+}
+
+// Whether the row holds a nonzero logit below 2^-26 in magnitude.
+__device__ inline bool has_tiny(const Row<__bf16>& row) {
+  bool tiny = false;
+  for_each(row, [&](float l, int64_t) { tiny |= l != 0.f && fabsf(l) < 0x1p-26f; });
+  return __syncthreads_or(tiny);
+}
+
+struct Settings {
+  double T, p, min_p, u;
+  bool limit;
+  uint32_t k;
+};
+
+// From the counts in sh.cnt: the logit of the drawn token, which of the equal
+// ones it is (r >= 1; 0: nothing to draw), and its log-probability.  False:
+// the row is one for the general path.
+__device__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Settings& how, float* logit, uint32_t* nth,
+                             double* logp) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int kPer = Counted::kPer;
+  if (sh.cnt[Counted::kW + 1] != 0) return false;  // 256 and more, +inf or NaN
+  // the largest logit: the first slot with a count
+  uint32_t n[kPer], mine = 0, first = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = kPer - 1; i >= 0; --i) {
+    n[i] = Counted::count(sh.cnt, tid * kPer + i);
+    mine += n[i];
+    if (n[i]) first = (uint32_t)(tid * kPer + i);
+  }
+  const uint64_t any = __ballot(first != 0xFFFFFFFFu);
+  if (any && lane == __builtin_ctzll(any)) atomicMin(&sh.first, first);
+  __syncthreads();
+  first = sh.first;
+  const bool low = sh.cnt[Counted::kSign + Counted::kW + 1] != 0;  // -256 and less, -inf or NaN
+  if (first == 0xFFFFFFFFu) return false;
+  Scale sc;
+  sc.inf = false;
+  sc.mx = (double)Counted::value((int)first);
+  sc.c = 92.332482616893656877 / how.T;
+  sc.fix = 1.0;
+  if (low && sc.y(-256.f) < (double)kBins) return false;
+  double sum = 0.0, likely = 0.0, before = 0.0, dummy;
+  uint32_t cbefore = 0;
+  if (any) {  // else every slot of the wave is empty
+#pragma unroll 3
+    for (int i = 0; i < kPer; ++i) {
+      // slots above the largest logit are empty, and their e may overflow
+      const double e = n[i] ? mass_of(sh.red, sc.y(Counted::value(tid * kPer + i))) : 0.0;
+      sum += (double)n[i] * e;
+      if (e >= how.min_p) likely += (double)n[i] * e;
+    }
+  }
+  double S = block_prefix(sum, sh.red, &before);
+  if (how.limit) block_prefix(mine, sh.red, &cbefore);
+  const double s_min = how.min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
+  // nonzero logits below 2^-26 are taken as 0: off by 2^-26 / T of their mass
+  const uint32_t zeros = sh.cnt[0] + sh.cnt[Counted::kSign];
+  if (zeros && (double)zeros * mass_of(sh.red, sc.y(0.f)) * 0x1p-26 / how.T > 1e-13 * S && has_tiny(row)) return false;
+
+  // A border: the first thread at the end of whose slots it is reached (the
+  // last with mass if rounding leaves none), then among that thread's slots,
+  // one per lane, in every wave alike.
+  int slot = 0;
+  uint32_t r = 0;
+  double at_e = 0.0;
+  bool in_zero = false;
+  auto border = [&](int kind, double target) {
+    __syncthreads();
+    if (tid == 0) {
+      sh.pick = 0xFFFFFFFFu;
+      sh.last = 0;
+    }
+    __syncthreads();
+    const uint64_t hit = __ballot(sum > 0.0 && reached(kind, cbefore + mine, before + sum, how.k, target));
+    const uint64_t has = __ballot(sum > 0.0);
+    if (hit && lane == __builtin_ctzll(hit)) atomicMin(&sh.pick, (uint32_t)tid);
+    if (has && lane == 63 - __builtin_clzll(has)) atomicMax(&sh.last, (uint32_t)tid);
+    __syncthreads();
+    const uint32_t at = sh.pick != 0xFFFFFFFFu ? sh.pick : sh.last;
+    if ((uint32_t)tid == at) {
+      sh.above = before;
+      sh.above_n = cbefore;
+    }
+    __syncthreads();
+    const int s = (int)at * kPer + lane;
+    const uint32_t ns = lane < kPer ? Counted::count(sh.cnt, s) : 0;
+    const double e = ns ? mass_of(sh.red, sc.y(Counted::value(s))) : 0.0;
+    static_assert(kPer <= 16, "the slots of a thread lie in one row of lanes");
+    const double run = sh.above + wave_scan((double)ns * e);
+    const uint32_t crun = sh.above_n + wave_scan(ns);
+    const bool on = ns && e > 0.0;
+    const uint64_t there = __ballot(on && reached(kind, crun, run, how.k, target)), some = __ballot(on);
+    const int l = there ? __builtin_ctzll(there) : 63 - __builtin_clzll(some | 1ull);
+    const uint32_t nl = __shfl(ns, l), before_n = __shfl(crun, l) - nl;
+    at_e = __shfl(e, l);
+    const double above = l > 0 ? __shfl(run, l > 0 ? l - 1 : 0) : sh.above;
+    slot = (int)at * kPer + l;
+    in_zero |= slot == Counted::kZero;
+    r = equal_taken(kind, nl, before_n, above, at_e, how.k, target);
+    return above + (double)r * at_e;
+  };
+  if (how.limit) S = border(BY_COUNT, 0.0);
+  if (how.p < 1.0) S = fmin(S, border(BY_MASS, how.p * S));
+  S = fmin(S, s_min);
+  border(BY_MASS_OVER, how.u * S);
+  if (in_zero && has_tiny(row)) return false;
+  *logp = log(at_e / S);
+  *logit = Counted::value(slot);
+  *nth = r;
+  return true;
 }
 
 struct SampleArgs {
@@ -553,37 +880,72 @@ struct SampleArgs {
   float* logp;
 };
 
+// The row's settings; a temperature that is not above zero is greedy.
+__device__ inline Settings row_settings(const SampleArgs& a, int64_t r) {
+  Settings s;
+  s.T = a.p.temperatures ? (double)a.p.temperatures[r] : a.p.temperature;
+  int64_t k = a.p.top_ks ? (int64_t)a.p.top_ks[r] : a.p.top_k;
+  s.p = a.p.top_ps ? (double)a.p.top_ps[r] : a.p.top_p;
+  s.min_p = a.p.min_ps ? (double)a.p.min_ps[r] : a.p.min_p;
+  if (!(s.T > 0.0)) {
+    s.T = 1.0;
+    k = 1;
+  }
+  s.T = fmax(s.T, 1e-200);  // keeps 1 / T finite; only equal logits share the mass long before
+  s.limit = k > 0 && k < a.V;
+  s.k = (uint32_t)(s.limit ? k : a.V);
+  if (!(s.min_p > 0.0)) s.min_p = 0.0;
+  if (s.min_p > 1.0) s.min_p = 1.0;
+  s.u = (double)a.u[r];
+  if (!(s.u > 0.0)) s.u = 0.0;
+  const double u_max = 1.0 - 0x1p-24;  // the largest fp32 below 1
+  if (s.u > u_max) s.u = u_max;
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads, 8) count_kernel(SampleArgs a) {
+  __shared__ CountShared sh;
+  const int tid = threadIdx.x;
+  const int64_t r = blockIdx.x;
+  const Row<__bf16> row((const __bf16*)a.x + r * a.ld, a.V);
+  const Settings how = row_settings(a, r);
+  for (int i = tid; i < Counted::kCounts; i += kThreads) sh.cnt[i] = 0;
+  if (tid == 0) sh.first = 0xFFFFFFFFu;
+  fill_pow64(sh.red);
+  __syncthreads();
+  count_row(row, sh.cnt);
+  __syncthreads();
+  float logit = 0.f;
+  uint32_t nth = 0;
+  double logp = 0.0;
+  int64_t id = kLeft;
+  if (pick_counted(row, sh, how, &logit, &nth, &logp))
+    id = nth_equal(row, sh.cnt, sh.red, sh.nth, logit, nth);
+  if (tid == 0) {
+    a.ids[r] = (int32_t)id;
+    if (a.logp) a.logp[r] = (float)logp;
+  }
+}
+
+// The general path; of bf16 rows those that count_kernel left.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
+  if (sizeof(T) == 2 && a.ids[r] != kLeft) return;
   const Row<T> row((const T*)a.x + r * a.ld, a.V);
-  constexpr int kN = Row<T>::kN;
 
-  // the row's settings; a temperature that is not above zero is greedy
-  double T_ = a.p.temperatures ? (double)a.p.temperatures[r] : a.p.temperature;
-  int64_t k64 = a.p.top_ks ? (int64_t)a.p.top_ks[r] : a.p.top_k;
-  const double p = a.p.top_ps ? (double)a.p.top_ps[r] : a.p.top_p;
-  double min_p = a.p.min_ps ? (double)a.p.min_ps[r] : a.p.min_p;
-  if (!(T_ > 0.0)) {
-    T_ = 1.0;
-    k64 = 1;
-  }
-  T_ = fmax(T_, 1e-200);  // keeps 1 / T finite; only equal logits share the mass long before
-  const bool limit = k64 > 0 && k64 < a.V;
-  const uint32_t k = (uint32_t)(limit ? k64 : a.V);
-  if (!(min_p > 0.0)) min_p = 0.0;
-  if (min_p > 1.0) min_p = 1.0;
-  double u = (double)a.u[r];
-  if (!(u > 0.0)) u = 0.0;
-  const double u_max = 1.0 - 0x1p-24;  // the largest fp32 below 1
-  if (u > u_max) u = u_max;
+  const Settings how = row_settings(a, r);
+  const double p = how.p, min_p = how.min_p, u = how.u;
+  const bool limit = how.limit;
+  const uint32_t k = how.k;
+  fill_pow64(sh.red);  // read after the next barrier
 
-  // 1. the largest logit; each thread's largest, and those of its chunks
+  // 1. the largest logit, and each thread's
   float mv = -INFINITY;
   for_each(row, [&](float l, int64_t) { mv = fmaxf(mv, l); });
-  const float mx = block_max(mv, sh);
+  const float mx = block_max(mv, sh.red);
   if (mx == -INFINITY) {  // nothing to sample
     if (tid == 0) {
       a.ids[r] = -1;
@@ -594,11 +956,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   Scale sc;
   sc.inf = mx == INFINITY;
   sc.mx = (double)mx;
-  sc.c = 92.332482616893656877 / T_;  // 64 log2(e)
+  sc.c = 92.332482616893656877 / how.T;  // 64 log2(e)
   sc.fix = (double)(1ull << a.fix_bits);
 
   // 2a. few tokens: those that reach the k-th largest of the threads' maxima
-  if (k <= (uint32_t)kFastK) {
+  if (sizeof(T) == 4 && k <= (uint32_t)kFastK) {
     uint32_t* hist = (uint32_t*)sh.mass;
     constexpr int kHist = 1 << kTopBits, kShift = Key<T>::kBits - kTopBits, kPer = kHist / kThreads;
     for (int i = tid; i < kHist; i += kThreads) hist[i] = 0;
@@ -613,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     uint32_t mine = 0, above = 0;
 #pragma unroll
     for (int b = 0; b < kPer; ++b) mine += hist[kHist - 1 - (kPer * tid + b)];
-    block_prefix(mine, sh, &above);
+    block_prefix(mine, sh.red, &above);
     if (above < k && above + mine >= k) {
       uint32_t c = above;
       for (int b = 0; b < kPer; ++b) {
@@ -651,8 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
         // the prefix with e >= min_p: its length is a count of the list
         uint32_t c = 0, b = 0;
         for (int i = tid; i < n; i += kThreads)
-          c += mass_of(sc.y(Key<T>::value((uint32_t)(sh.cand[i] >> 32)))) >= min_p;
-        const uint32_t len = block_prefix(c, sh, &b);
+          c += mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(sh.cand[i] >> 32)))) >= min_p;
+        const uint32_t len = block_prefix(c, sh.red, &b);
         pick_in_list<T>(sh, n, sc, BY_COUNT, len > 0 ? len : 1, 0.0, 0.0, 0, &m);
         S = fmin(S, m);
       }
@@ -660,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
       if (tid == 0) {
         const uint64_t c = sh.cand[j];
         a.ids[r] = (int32_t)unpack_id(c);
-        if (a.logp) a.logp[r] = (float)log(mass_of(sc.y(Key<T>::value((uint32_t)(c >> 32)))) / S);
+        if (a.logp) a.logp[r] = (float)log(mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(c >> 32)))) / S);
       }
       return;
     }
@@ -698,13 +1060,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int b = tid * kPerThread + i;
-      const double m = sh.mass[b] ? (double)sh.mass[b] / sc.fix * bin_top(b) : 0.0;
+      const double m = sh.mass[b] ? (double)sh.mass[b] / sc.fix * bin_top(sh.red, b) : 0.0;
       all += m;
       if (b < bin_min) likely += m;
-      if (b == bin_min) likely += (double)sh.edge_mass / sc.fix * bin_top(b);
+      if (b == bin_min) likely += (double)sh.edge_mass / sc.fix * bin_top(sh.red, b);
     }
-    S = block_prefix(all, sh, &dummy);
-    s_min = min_p > 0.0 ? block_prefix(likely, sh, &dummy) : S;
+    S = block_prefix(all, sh.red, &dummy);
+    s_min = min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
   }
   if (limit) S = find_border(row, sh, sc, BY_COUNT, k, 0.0, false).mass;
   if (p < 1.0) S = fmin(S, find_border(row, sh, sc, BY_MASS, 0, p * S, false).mass);
@@ -712,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   const Found f = find_border(row, sh, sc, BY_MASS_OVER, 0, u * S, true);
   if (tid == 0) {
     a.ids[r] = (int32_t)f.id;
-    if (a.logp) a.logp[r] = (float)log(mass_of(sc.y(f.logit)) / S);
+    if (a.logp) a.logp[r] = (float)log(mass_of(sh.red, sc.y(f.logit)) / S);
   }
 }
 
@@ -731,9 +1093,12 @@ hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t 
   a.fix_bits = 62 - lg < 51 ? 62 - lg : 51;  // V masses of at most 2^fix_bits stay below 2^63
   a.ids = ids;
   a.logp = logp;
-  if (dt == DT_BF16)
+  if (dt == DT_BF16) {
+    hipLaunchKernelGGL(count_kernel, dim3((unsigned)N), dim3(kThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(sample_kernel<__bf16>, dim3((unsigned)N), dim3(kThreads), 0, s, a);
-  else
+  } else
     hipLaunchKernelGGL(sample_kernel<float>, dim3((unsigned)N), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
