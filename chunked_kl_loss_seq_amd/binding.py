@@ -70,8 +70,10 @@ def lib():
     L.ckl_embed_bwd.restype = ctypes.c_int
     L.ckl_embed_bwd_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(u64)]
     L.ckl_embed_bwd_workspace.restype = ctypes.c_int
-    L.ckl_sample.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, ctypes.POINTER(Sampling), vp, vp, vp]
+    L.ckl_sample.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, ctypes.POINTER(Sampling), vp, vp, vp, u64, vp]
     L.ckl_sample.restype = ctypes.c_int
+    L.ckl_sample_workspace.argtypes = [ctypes.c_int, i64, i64, ctypes.POINTER(u64)]
+    L.ckl_sample_workspace.restype = ctypes.c_int
     L.ckl_quantize_fp8.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, vp, vp]
     L.ckl_quantize_fp8.restype = ctypes.c_int
     L.ckl_matmul_fp8.argtypes = [ctypes.c_int, vp, vp, vp, vp, i64, i64, i64, vp, vp]

@@ -662,8 +662,16 @@ int ckl_embed_bwd(int dtype, const int32_t* ids, const void* dY, float scale, in
   }
 }
 
+int ckl_sample_workspace(int dtype, int64_t N, int64_t V, uint64_t* bytes_out) {
+  if (!dtype_ok(dtype) || !bytes_out || N < 0 || V <= 0) return CKL_EINVAL;
+  if (V > (int64_t)1 << 26 || N >= (int64_t)1 << 23) return CKL_EUNSUPPORTED;
+  *bytes_out = N > 0 ? sample_workspace(to_dt(dtype), N, V) : 0;
+  return CKL_OK;
+}
+
 int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const float* u,
-               const ckl_sampling* how, int32_t* ids_out, float* logp_out, hipStream_t stream) {
+               const ckl_sampling* how, int32_t* ids_out, float* logp_out, void* workspace,
+               uint64_t workspace_bytes, hipStream_t stream) {
   if (!dtype_ok(dtype)) return CKL_EINVAL;
   if (N < 0 || V <= 0 || row_stride < 0) return CKL_EINVAL;
   SampleParams p{1.0, 0, 1.0, 0.0, nullptr, nullptr, nullptr, nullptr};
@@ -684,9 +692,12 @@ int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_
   if (!aligned(logits, dtype == CKL_DTYPE_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(ids_out, 4) ||
       !aligned(logp_out, 4))
     return CKL_EINVAL;
+  const uint64_t need = sample_workspace(to_dt(dtype), N, V);
+  if (workspace && (!aligned(workspace, 256) || workspace_bytes < need)) return CKL_EINVAL;
   try {
     Timed t(T_SAMPLE, stream);
-    CKL_TRY(launch_sample(to_dt(dtype), logits, N, V, row_stride, u, p, ids_out, logp_out, stream));
+    CKL_TRY(launch_sample(to_dt(dtype), logits, N, V, row_stride, u, p, ids_out, logp_out, need ? workspace : nullptr,
+                          stream));
     return CKL_OK;
   } catch (...) {
     return CKL_EHIP;

@@ -858,10 +858,15 @@ __device__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Sett
     r = equal_taken(kind, nl, before_n, above, at_e, how.k, target);
     return above + (double)r * at_e;
   };
-  if (how.limit) S = border(BY_COUNT, 0.0);
-  if (how.p < 1.0) S = fmin(S, border(BY_MASS, how.p * S));
-  S = fmin(S, s_min);
-  border(BY_MASS_OVER, how.u * S);
+  // k, then p, then the draw: one copy of the code, run up to three times
+#pragma unroll 1
+  for (int kind = how.limit ? BY_COUNT : how.p < 1.0 ? BY_MASS : BY_MASS_OVER;;) {
+    if (kind == BY_MASS_OVER) S = fmin(S, s_min);
+    const double got = border(kind, kind == BY_MASS ? how.p * S : how.u * S);
+    if (kind == BY_MASS_OVER) break;
+    S = fmin(S, got);
+    kind = kind == BY_COUNT && how.p < 1.0 ? BY_MASS : BY_MASS_OVER;
+  }
   if (in_zero && has_tiny(row)) return false;
   *logp = log(at_e / S);
   *logit = Counted::value(slot);
@@ -878,7 +883,12 @@ struct SampleArgs {
   int fix_bits;
   int32_t* ids;
   float* logp;
+  // split rows (slices > 1): logits per slice, and the slices' counts
+  int slices;
+  int64_t slice_len;
+  uint16_t* tables;
 };
+constexpr int kSlicesMax = 16;
 
 // The row's settings; a temperature that is not above zero is greedy.
 __device__ inline Settings row_settings(const SampleArgs& a, int64_t r) {
@@ -903,14 +913,23 @@ __device__ inline Settings row_settings(const SampleArgs& a, int64_t r) {
   return s;
 }
 
+__device__ inline void clear_counts(CountShared& sh) {
+  for (int i = threadIdx.x; i < Counted::kCounts; i += kThreads) sh.cnt[i] = 0;
+  if (threadIdx.x == 0) sh.first = 0xFFFFFFFFu;
+}
+__device__ inline void put(const SampleArgs& a, int64_t r, int64_t id, double logp) {
+  if (threadIdx.x == 0) {
+    a.ids[r] = (int32_t)id;
+    if (a.logp) a.logp[r] = (float)logp;
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 8) count_kernel(SampleArgs a) {
   __shared__ CountShared sh;
-  const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
   const Row<__bf16> row((const __bf16*)a.x + r * a.ld, a.V);
   const Settings how = row_settings(a, r);
-  for (int i = tid; i < Counted::kCounts; i += kThreads) sh.cnt[i] = 0;
-  if (tid == 0) sh.first = 0xFFFFFFFFu;
+  clear_counts(sh);
   fill_pow64(sh.red);
   __syncthreads();
   count_row(row, sh.cnt);
@@ -919,12 +938,73 @@ __global__ void __launch_bounds__(kThreads, 8) count_kernel(SampleArgs a) {
   uint32_t nth = 0;
   double logp = 0.0;
   int64_t id = kLeft;
-  if (pick_counted(row, sh, how, &logit, &nth, &logp))
-    id = nth_equal(row, sh.cnt, sh.red, sh.nth, logit, nth);
-  if (tid == 0) {
-    a.ids[r] = (int32_t)id;
-    if (a.logp) a.logp[r] = (float)logp;
+  if (pick_counted(row, sh, how, &logit, &nth, &logp)) id = nth_equal(row, sh.cnt, sh.red, sh.nth, logit, nth);
+  put(a, r, id, logp);
+}
+
+// Few long rows: `slices` workgroups count a row's slices, so that more of the
+// chip reads it, and the finishing workgroup adds their counts (16 bits each)
+// and looks for the token in its slice alone.
+constexpr int64_t kSliceMax = 65535;  // logits: a count fits 16 bits
+constexpr int kTable = (Counted::kCounts + 7) / 8 * 8;  // counts of a slice in the workspace
+__device__ inline Row<__bf16> slice_of(const SampleArgs& a, int64_t r, int s) {
+  const int64_t b = (int64_t)s * a.slice_len, left = a.V - b;
+  return Row<__bf16>((const __bf16*)a.x + r * a.ld + b, left < a.slice_len ? left : a.slice_len);
+}
+__global__ void __launch_bounds__(kThreads, 8) count_slice_kernel(SampleArgs a) {
+  __shared__ CountShared sh;
+  const int64_t r = blockIdx.x / a.slices;
+  const int s = (int)(blockIdx.x - r * a.slices);
+  clear_counts(sh);
+  __syncthreads();
+  count_row(slice_of(a, r, s), sh.cnt);
+  __syncthreads();
+  uint32_t* dst = (uint32_t*)(a.tables + (int64_t)blockIdx.x * kTable);
+  for (int i = threadIdx.x; i < Counted::kCounts / 2; i += kThreads)
+    dst[i] = sh.cnt[2 * i] | sh.cnt[2 * i + 1] << 16;
+}
+static_assert(Counted::kCounts % 2 == 0, "counts are stored in pairs");
+
+__global__ void __launch_bounds__(kThreads, 8) count_finish_kernel(SampleArgs a) {
+  __shared__ CountShared sh;
+  __shared__ uint32_t there[kSlicesMax];
+  const int tid = threadIdx.x;
+  const int64_t r = blockIdx.x;
+  const Settings how = row_settings(a, r);
+  const uint16_t* tables = a.tables + r * a.slices * kTable;
+  fill_pow64(sh.red);
+  if (tid == 0) sh.first = 0xFFFFFFFFu;
+  for (int i = tid; i < Counted::kCounts / 2; i += kThreads) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll 4
+    for (int s = 0; s < a.slices; ++s) {
+      const uint32_t w = ((const uint32_t*)(tables + s * kTable))[i];
+      lo += w & 0xFFFFu;
+      hi += w >> 16;
+    }
+    sh.cnt[2 * i] = lo;
+    sh.cnt[2 * i + 1] = hi;
   }
+  __syncthreads();
+  float logit = 0.f;
+  uint32_t nth = 0;
+  double logp = 0.0;
+  int64_t id = kLeft;
+  const Row<__bf16> row((const __bf16*)a.x + r * a.ld, a.V);
+  if (pick_counted(row, sh, how, &logit, &nth, &logp)) {
+    // the slice that holds the nth such logit
+    if (tid < a.slices) {
+      const uint16_t* t = tables + tid * kTable;
+      const uint32_t h = __builtin_bit_cast(uint32_t, logit) >> 16;
+      const int at = (int)(h & 0x7FFFu) - (Counted::kLo - 1);
+      there[tid] = logit == 0.f ? (uint32_t)t[0] + t[Counted::kSign] : t[at + (h & 0x8000u ? Counted::kSign : 0)];
+    }
+    __syncthreads();
+    int s = 0;
+    while (s + 1 < a.slices && nth > there[s]) nth -= there[s++];
+    id = s * a.slice_len + nth_equal(slice_of(a, r, s), sh.cnt, sh.red, sh.nth, logit, nth);
+  }
+  put(a, r, id, logp);
 }
 
 // The general path; of bf16 rows those that count_kernel left.
@@ -1001,24 +1081,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     if (held <= (uint32_t)kCap) {
       sort_cand(sh, (int)held);
       const int n = (int)(held < k ? held : k);
+      // the mass of the first n, the shortest prefixes for p and min_p, the draw
       double S = 0.0, m = 0.0;
-      // mass of the first n; then the p and min_p borders within them
-      pick_in_list<T>(sh, n, sc, BY_COUNT, (uint32_t)n, 0.0, 0.0, 0, &S);
-      const double Sk = S;
-      if (p < 1.0) {
-        pick_in_list<T>(sh, n, sc, BY_MASS, 0, p * Sk, 0.0, 0, &m);
-        S = fmin(S, m);
+      int j = 0;
+#pragma unroll 1
+      for (int step = 0; step < 4; ++step) {
+        if ((step == 1 && !(p < 1.0)) || (step == 2 && !(min_p > 0.0))) continue;
+        uint32_t len = (uint32_t)n;
+        if (step == 2) {  // the prefix with e >= min_p: its length is a count of the list
+          uint32_t c = 0, b = 0;
+          for (int i = tid; i < n; i += kThreads)
+            c += mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(sh.cand[i] >> 32)))) >= min_p;
+          len = block_prefix(c, sh.red, &b);
+          if (len == 0) len = 1;
+        }
+        const int kind = step == 1 ? BY_MASS : step == 3 ? BY_MASS_OVER : BY_COUNT;
+        const double target = step == 1 ? p * S : u * S;
+        j = pick_in_list<T>(sh, n, sc, kind, len, target, 0.0, 0, &m);
+        // p is a share of the first k's mass, which step 0 left in S
+        S = step == 0 ? m : step == 3 ? S : fmin(S, m);
       }
-      if (min_p > 0.0) {
-        // the prefix with e >= min_p: its length is a count of the list
-        uint32_t c = 0, b = 0;
-        for (int i = tid; i < n; i += kThreads)
-          c += mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(sh.cand[i] >> 32)))) >= min_p;
-        const uint32_t len = block_prefix(c, sh.red, &b);
-        pick_in_list<T>(sh, n, sc, BY_COUNT, len > 0 ? len : 1, 0.0, 0.0, 0, &m);
-        S = fmin(S, m);
-      }
-      const int j = pick_in_list<T>(sh, n, sc, BY_MASS_OVER, 0, u * S, 0.0, 0, &m);
       if (tid == 0) {
         const uint64_t c = sh.cand[j];
         a.ids[r] = (int32_t)unpack_id(c);
@@ -1068,10 +1150,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     S = block_prefix(all, sh.red, &dummy);
     s_min = min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
   }
-  if (limit) S = find_border(row, sh, sc, BY_COUNT, k, 0.0, false).mass;
-  if (p < 1.0) S = fmin(S, find_border(row, sh, sc, BY_MASS, 0, p * S, false).mass);
-  S = fmin(S, s_min);
-  const Found f = find_border(row, sh, sc, BY_MASS_OVER, 0, u * S, true);
+  Found f;
+#pragma unroll 1
+  for (int kind = limit ? BY_COUNT : p < 1.0 ? BY_MASS : BY_MASS_OVER;;) {
+    if (kind == BY_MASS_OVER) S = fmin(S, s_min);
+    f = find_border(row, sh, sc, kind, k, kind == BY_MASS ? p * S : u * S, kind == BY_MASS_OVER);
+    if (kind == BY_MASS_OVER) break;
+    S = fmin(S, f.mass);
+    kind = kind == BY_COUNT && p < 1.0 ? BY_MASS : BY_MASS_OVER;
+  }
   if (tid == 0) {
     a.ids[r] = (int32_t)f.id;
     if (a.logp) a.logp[r] = (float)log(mass_of(sh.red, sc.y(f.logit)) / S);
@@ -1080,8 +1167,25 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 
 }  // namespace
 
+// Workgroups per bf16 row: more than one for few rows (less than a quarter of
+// the 256 compute units busy) of at least 2 x 16,384 logits.  One 201,088-logit
+// row takes 33 us by one workgroup.
+namespace {
+int slices_of(Dtype dt, int64_t N, int64_t V) {
+  if (dt != DT_BF16 || N > 64) return 1;
+  int64_t s = V / 16384;
+  if (s > 256 / N) s = 256 / N;
+  if (s > kSlicesMax) s = kSlicesMax;
+  return s < 2 || (V + s - 1) / s > kSliceMax - 64 ? 1 : (int)s;
+}
+}  // namespace
+uint64_t sample_workspace(Dtype dt, int64_t N, int64_t V) {
+  const int s = slices_of(dt, N, V);
+  return s > 1 ? (uint64_t)N * s * kTable * sizeof(uint16_t) : 0;
+}
+
 hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t ld, const float* u,
-                         const SampleParams& p, int32_t* ids, float* logp, hipStream_t s) {
+                         const SampleParams& p, int32_t* ids, float* logp, void* ws, hipStream_t s) {
   SampleArgs a{};
   a.x = x;
   a.ld = ld;
@@ -1094,9 +1198,19 @@ hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t 
   a.ids = ids;
   a.logp = logp;
   if (dt == DT_BF16) {
-    hipLaunchKernelGGL(count_kernel, dim3((unsigned)N), dim3(kThreads), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    a.slices = ws != nullptr ? slices_of(dt, N, V) : 1;
+    hipError_t e;
+    if (a.slices > 1) {
+      a.slice_len = ((V + a.slices - 1) / a.slices + 63) / 64 * 64;
+      a.slices = (int)((V + a.slice_len - 1) / a.slice_len);
+      a.tables = (uint16_t*)ws;
+      hipLaunchKernelGGL(count_slice_kernel, dim3((unsigned)(N * a.slices)), dim3(kThreads), 0, s, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      hipLaunchKernelGGL(count_finish_kernel, dim3((unsigned)N), dim3(kThreads), 0, s, a);
+    } else {
+      hipLaunchKernelGGL(count_kernel, dim3((unsigned)N), dim3(kThreads), 0, s, a);
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(sample_kernel<__bf16>, dim3((unsigned)N), dim3(kThreads), 0, s, a);
   } else
     hipLaunchKernelGGL(sample_kernel<float>, dim3((unsigned)N), dim3(kThreads), 0, s, a);

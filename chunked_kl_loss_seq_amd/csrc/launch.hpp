@@ -110,9 +110,12 @@ struct SampleParams {
   const float* top_ps;
   const float* min_ps;
 };
-// A token and its log-probability per row of x (rows ld elements apart), see kernels_sample.hip.
+// A token and its log-probability per row of x (rows ld elements apart), see
+// kernels_sample.hip; ws of sample_workspace bytes, or null (long rows of a
+// small batch are then not split).
+uint64_t sample_workspace(Dtype dt, int64_t N, int64_t V);
 hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t ld, const float* u,
-                         const SampleParams& p, int32_t* ids, float* logp, hipStream_t s);
+                         const SampleParams& p, int32_t* ids, float* logp, void* ws, hipStream_t s);
 
 // e4m3 values and their scales: per 1 x 128 block (rows; scales [ceil(C / 128), R])
 // or per 128 x 128 block (scales [ceil(R / 128), ceil(C / 128)]), see kernels_fp8.hip.

@@ -179,9 +179,12 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids_out=No
         ids_out = torch.empty((N,), dtype=torch.int32, device=dev)
     if logp_out is None:
         logp_out = torch.empty((N,), dtype=torch.float32, device=dev)
+    need = ctypes.c_uint64(0)
+    _check(lib().ckl_sample_workspace(dt, N, V, ctypes.byref(need)), "ckl_sample_workspace")
     with _on(torch, dev):
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
         _check(lib().ckl_sample(dt, _ptr(logits), N, V, logits.stride(0) if N > 1 else V, _ptr(u), ctypes.byref(how),
-                                _ptr(ids_out), _ptr(logp_out), _stream(torch, dev)), "ckl_sample")
+                                _ptr(ids_out), _ptr(logp_out), _ptr(ws), need.value, _stream(torch, dev)), "ckl_sample")
     return ids_out, logp_out
 
 

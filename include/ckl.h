@@ -260,9 +260,15 @@ typedef struct ckl_sampling {
  *   logp_out  fp32 [N] or NULL: log(e / S) of the drawn token (-inf for -1)
  * Masses and borders are computed in 64 bits, so the token is that of the
  * formulas except where a border is within about 1e-13 of the total; tokens
- * whose e is below 2^-64 count as 0.  V <= 2^26, N < 2^23.  No workspace. */
+ * whose e is below 2^-64 count as 0.  V <= 2^26, N < 2^23.
+ *   workspace NULL, or a device buffer of at least ckl_sample_workspace bytes
+ *             (0 for most shapes), 256-byte aligned, not shared by calls that
+ *             may overlap: with it, long rows of a small batch are split over
+ *             several workgroups.  The results are the same bits either way. */
 int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const float* u,
-               const ckl_sampling* how, int32_t* ids_out, float* logp_out, hipStream_t stream);
+               const ckl_sampling* how, int32_t* ids_out, float* logp_out, void* workspace,
+               uint64_t workspace_bytes, hipStream_t stream);
+int ckl_sample_workspace(int dtype, int64_t N, int64_t V, uint64_t* bytes_out);
 
 /* Matrix product in 8-bit floating point (OCP e4m3) with an fp32 scale per
  * block of 128, for a head whose weight is held in 8 bits (a teacher's logits

@@ -143,6 +143,19 @@ def test_equal_logits(ckl, V, how):
 
 
 @pytest.mark.parametrize("how", [{}, {"top_k": 4000}, {"top_p": 0.6}, {"top_k": 30000, "top_p": 0.9, "temperature": 0.8}])
+def test_tiny_and_large_logits(ckl, how):
+    # bf16 values the counted path leaves to the general one, or has to look at twice
+    g = torch.Generator().manual_seed(9)
+    u = uniforms(8)
+    base = torch.randn(8, 5000, generator=g).to("cuda:0")
+    for x in (base * 1e-9, base * 1e-9 * (base > 0), base * 200, base * 200 - 800, base * 3e37, -base.abs() * 1e3 - 300,
+              torch.where(base > 1, base * 1e-10, base), torch.where(base > 1, torch.zeros_like(base), base)):
+        check(ckl, x.to(torch.bfloat16), u, "tiny or large", **how)
+        check(ckl, x.to(torch.bfloat16), u, "tiny or large", **dict(how, temperature=100.0))
+    check(ckl, (base * 1e-9).to(torch.bfloat16), u, "tiny, resolved", **dict(how, temperature=1e-9))
+
+
+@pytest.mark.parametrize("how", [{}, {"top_k": 4000}, {"top_p": 0.6}, {"top_k": 30000, "top_p": 0.9, "temperature": 0.8}])
 def test_few_distinct_values(ckl, how):
     # one bin with far more tokens than fit, of several keys in it: narrowed by key digits
     g = torch.Generator().manual_seed(8)
@@ -152,6 +165,41 @@ def test_few_distinct_values(ckl, how):
     near = 1.0 + torch.randint(0, 300, (8, 60000), generator=g).float() * 2.0 ** -23
     check(ckl, near.to("cuda:0"), u, "neighbouring fp32 values", **how)
     check(ckl, (torch.rand(8, 60000, generator=g) * 1e-3).to("cuda:0"), u, "a narrow interval", **how)
+
+
+@pytest.mark.parametrize("N,V", [(1, 32768), (1, 50001), (3, 201088), (7, 140000), (17, 100003), (64, 70000), (1, 1000003), (1, 1100000)])
+def test_split_rows(ckl, N, V):
+    # long rows of a small batch are counted by several workgroups; borders,
+    # equal logits and the drawn one in any of the slices, also unaligned ones
+    big = rows(N, V + 3, "bf16")
+    for i, how in enumerate(({}, {"top_k": 40, "top_p": 0.9}, {"top_p": 0.8}, {"min_p": 0.02}, {"top_k": 3000})):
+        check(ckl, big[:, i % 4: V + i % 4], uniforms(N, i), "split", **how)
+    x = big[:, 1:V + 1]
+    x[:] = float("-inf")
+    x[:, V - 1] = 1.0
+    x[:, V // 3] = 1.0
+    assert set(check(ckl, x, uniforms(N), "two left").tolist()) <= {V // 3, V - 1}
+    x[:] = 0.25
+    check(ckl, x, uniforms(N), "all equal")
+    x[0] = float("-inf")
+    assert check(ckl, x, uniforms(N), "an empty row")[0] == -1
+
+
+def test_without_a_workspace_the_same_bits(ckl):
+    import ctypes
+
+    from chunked_kl_loss_seq_amd import binding as B
+
+    x, u = rows(2, 201088, "bf16"), uniforms(2)
+    want = ckl.sample(x, u, top_p=0.9, temperature=0.7)
+    how = B.Sampling(0.7, 0, 0.9, 0.0, None, None, None, None)
+    ids, logp = torch.empty(2, dtype=torch.int32, device="cuda:0"), torch.empty(2, device="cuda:0")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert B.lib().ckl_sample(0, x.data_ptr(), 2, 201088, 201088, u.data_ptr(), ctypes.byref(how), ids.data_ptr(),
+                              logp.data_ptr(), None, 0, stream) == 0
+    assert torch.equal(ids, want[0]) and torch.equal(logp, want[1])
+    assert B.lib().ckl_sample(0, x.data_ptr(), 2, 201088, 201088, u.data_ptr(), None, ids.data_ptr(), None, None, 0, stream) == 0
+    assert torch.equal(ids, ckl.sample(x, u)[0])
 
 
 def test_strided_and_unaligned_rows(ckl):

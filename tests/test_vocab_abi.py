@@ -65,10 +65,10 @@ def test_embed_bwd_workspace():
     assert workspace(262144, 2880, 201088)[1] < 262144 * 2880 * 2 // 4
 
 
-def sample(dt=0, x=G, N=4, V=10, ld=10, u=G, ids=G, logp=G, **how):
+def sample(dt=0, x=G, N=4, V=10, ld=10, u=G, ids=G, logp=G, work=None, bytes_=0, **how):
     s = B.Sampling(how.get("temperature", 1.0), how.get("top_k", 0), how.get("top_p", 1.0), how.get("min_p", 0.0),
                    how.get("Ts"), how.get("ks"), how.get("ps"), how.get("ms"))
-    return B.lib().ckl_sample(dt, x, N, V, ld, u, ctypes.byref(s), ids, logp, None)
+    return B.lib().ckl_sample(dt, x, N, V, ld, u, ctypes.byref(s), ids, logp, work, bytes_, None)
 
 
 @pytest.mark.parametrize("bad,want", [
@@ -77,11 +77,23 @@ def sample(dt=0, x=G, N=4, V=10, ld=10, u=G, ids=G, logp=G, **how):
     ({"ids": MIS}, EINVAL), ({"logp": MIS}, EINVAL), ({"Ts": MIS}, EINVAL), ({"ks": MIS}, EINVAL),
     ({"temperature": -0.5}, EINVAL), ({"temperature": float("nan")}, EINVAL), ({"top_k": -1}, EINVAL),
     ({"top_p": 1.01}, EINVAL), ({"top_p": -0.01}, EINVAL), ({"top_p": float("nan")}, EINVAL), ({"min_p": 1.5}, EINVAL),
-    ({"min_p": float("nan")}, EINVAL), ({"V": (1 << 26) + 1}, EUNSUPPORTED), ({"N": 1 << 23}, EUNSUPPORTED),
+    ({"min_p": float("nan")}, EINVAL), ({"V": 200000, "work": G + 128, "bytes_": 1 << 30}, EINVAL),
+    ({"V": 200000, "work": G, "bytes_": 100}, EINVAL), ({"V": (1 << 26) + 1}, EUNSUPPORTED), ({"N": 1 << 23}, EUNSUPPORTED),
     ({"N": 0, "x": None, "u": None, "ids": None, "logp": None}, OK),
 ])
 def test_sample(bad, want):
     assert sample(**bad) == want
+
+
+def test_sample_workspace():
+    b = ctypes.c_uint64(7)
+    f = B.lib().ckl_sample_workspace
+    assert f(0, 0, 10, ctypes.byref(b)) == OK and b.value == 0
+    assert f(0, 1, 201088, ctypes.byref(b)) == OK and 0 < b.value < 1 << 20
+    for dt, N, V in ((0, 1, 30000), (0, 1000, 201088), (1, 1, 201088), (0, 1, 1 << 26)):  # rows not split
+        assert f(dt, N, V, ctypes.byref(b)) == OK and b.value == 0
+    assert f(2, 1, 10, ctypes.byref(b)) == EINVAL and f(0, 1, 10, None) == EINVAL and f(0, -1, 10, ctypes.byref(b)) == EINVAL
+    assert f(0, 1, (1 << 26) + 1, ctypes.byref(b)) == EUNSUPPORTED
 
 
 def quantize(dt=0, x=G, R=4, C=16, rows=1, q=G, s=G):
