@@ -16,8 +16,8 @@
 // whatever their tokens, a run inside one tile is written at once, and a run
 // that crosses tiles leaves one partial row per tile, summed in tile order by
 // a second kernel.  Rows without a token are written as zeros by other
-// workgroups of the same launch (by a bit per token), so every byte of dW is
-// written once; those zeros bound the call for large vocabularies.
+// workgroups of the same launches, so every byte of dW is written once; those
+// zeros bound the call for large vocabularies.
 #include <hip/hip_runtime.h>
 
 #include "launch.hpp"
@@ -116,97 +116,10 @@ __device__ inline uint32_t key_of(const int32_t* ids, int64_t i, uint32_t V) {
   return id < V ? id : V;
 }
 
-// Bit v of `bits` is set where token v occurs.
-__global__ void __launch_bounds__(kThreads) clear_kernel(uint32_t* p, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < n) p[i] = 0;
-}
-__device__ inline void mark(uint32_t* bits, uint32_t key, uint32_t V) {
-  // the plain read spares a frequent token's word most of its atomics
-  if (bits != nullptr && key < V && ((bits[key >> 5] >> (key & 31)) & 1u) == 0) atomicOr(&bits[key >> 5], 1u << (key & 31));
-}
-
-// Few positions: a position's place is the number of positions before it in
-// (id, position) order, counted directly.  Four lanes share one position and
-// the list passes through LDS; one launch in place of the radix sort's six.
-constexpr int kRankMax = 8192;
-constexpr int kRankTile = 2048;
-__global__ void __launch_bounds__(kThreads) rank_kernel(const int32_t* __restrict__ ids, int N, uint32_t V,
-                                                        uint32_t* __restrict__ skey, uint32_t* __restrict__ spos,
-                                                        uint32_t* __restrict__ bits) {
-  __shared__ __attribute__((aligned(16))) uint32_t tile[kRankTile];
-  const int i = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2), part = threadIdx.x & 3;
-  const uint32_t key = i < N ? key_of(ids, i, V) : 0;
-  int place = 0;
-  for (int t0 = 0; t0 < N; t0 += kRankTile) {
-    const int n = min(kRankTile, N - t0);
-    __syncthreads();
-    for (int j = threadIdx.x; j < kRankTile; j += kThreads) tile[j] = j < n ? key_of(ids, t0 + j, V) : 0xFFFFFFFFu;
-    __syncthreads();
-    for (int j = 4 * part; j < n; j += 16) {
-      const u32x4_t k = *(const u32x4_t*)&tile[j];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t kq = k[q];
-        place += (kq < key || (kq == key && t0 + j + q < i)) ? 1 : 0;
-      }
-    }
-  }
-  place += __shfl_xor(place, 1);
-  place += __shfl_xor(place, 2);
-  if (i < N && part == 0) {
-    skey[place] = key;
-    spos[place] = (uint32_t)i;
-    mark(bits, key, V);
-  }
-}
-
-// Many positions: a stable radix sort of the keys, kDigit bits a pass (two
-// passes up to 2^18 - 1 tokens).  Per pass: a histogram per tile, an exclusive
-// scan of the counts in (digit, tile) order, and a scatter in which each wave
-// ranks its own stretch of the tile in order.
-constexpr int kDigit = 9;
-constexpr int kDigits = 1 << kDigit;
-constexpr int kSortTile = 2048;
-constexpr int kSortWaves = kThreads / 64;
-constexpr int kRounds = kSortTile / kThreads;  // 64-element rounds per wave
-
-// Element i of the pass: from the ids on the first pass (keys == null).
-__device__ inline uint32_t pass_key(const int32_t* ids, const uint32_t* keys, int64_t i, uint32_t V) {
-  return keys != nullptr ? keys[i] : key_of(ids, i, V);
-}
-
-__global__ void __launch_bounds__(kThreads) sort_hist_kernel(const int32_t* __restrict__ ids,
-                                                             const uint32_t* __restrict__ keys, int64_t N, uint32_t V,
-                                                             int shift, int tiles, uint32_t* __restrict__ hist,
-                                                             uint32_t* __restrict__ bits) {
-  __shared__ uint32_t h[kDigits];
-  for (int i = threadIdx.x; i < kDigits; i += kThreads) h[i] = 0;
-  __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kSortTile;
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = base + r * kThreads + threadIdx.x;
-    if (i < N) {
-      const uint32_t k = pass_key(ids, keys, i, V);
-      atomicAdd(&h[(k >> shift) & (kDigits - 1)], 1u);
-      if (keys == nullptr) mark(bits, k, V);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kDigits; i += kThreads) hist[(int64_t)i * tiles + blockIdx.x] = h[i];
-}
-
-// Exclusive scan of n counts in place, one workgroup.
-constexpr int kScanThreads = 1024;
-__global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(uint32_t* __restrict__ hist, int64_t n) {
-  __shared__ uint32_t wsum[kScanThreads / 64];
-  const int64_t per = (n + kScanThreads - 1) / kScanThreads;
-  const int64_t b = threadIdx.x * per, e = b + per < n ? b + per : n;
-  uint32_t mine = 0;
-  for (int64_t i = b; i < e; ++i) mine += hist[i];
+// Sum of v over the threads before this one in a workgroup of kThreads.
+__device__ inline uint32_t block_before(uint32_t v, uint32_t* wsum) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  uint32_t x = mine;
+  uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const uint32_t y = __shfl_up(x, o);
@@ -214,26 +127,123 @@ __global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(uint32_t* __res
   }
   if (lane == 63) wsum[w] = x;
   __syncthreads();
-  uint32_t run = x - mine;
+  uint32_t run = x - v;
   for (int i = 0; i < w; ++i) run += wsum[i];
-  for (int64_t i = b; i < e; ++i) {
-    const uint32_t c = hist[i];
-    hist[i] = run;
-    run += c;
+  return run;
+}
+
+// Few positions: a position's place is the number of positions before it in
+// (id, position) order, counted directly: one launch in place of the radix
+// sort's four.  16 lanes share one position and the list passes through LDS
+// (4,096 positions: 49 us with 4 lanes a position, which left most of the chip
+// idle).
+constexpr int kRankMax = 8192;
+constexpr int kRankTile = 4096;
+constexpr int kRankLanes = 16;
+__global__ void __launch_bounds__(kThreads) rank_kernel(const int32_t* __restrict__ ids, int N, uint32_t V,
+                                                        uint32_t* __restrict__ skey, uint32_t* __restrict__ spos) {
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kRankTile];
+  const int i = blockIdx.x * (kThreads / kRankLanes) + threadIdx.x / kRankLanes, part = threadIdx.x % kRankLanes;
+  const uint32_t key = i < N ? key_of(ids, i, V) : 0;
+  int place = 0;
+  for (int t0 = 0; t0 < N; t0 += kRankTile) {
+    const int n = min(kRankTile, N - t0), n4 = (n + 3) & ~3;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n4; j += kThreads) tile[j] = j < n ? key_of(ids, t0 + j, V) : 0xFFFFFFFFu;
+    __syncthreads();
+#pragma unroll 8
+    for (int j = 4 * part; j < n4; j += 4 * kRankLanes) {
+      const u32x4_t k = *(const u32x4_t*)&tile[j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t kq = k[q];
+        place += kq < key + (t0 + j + q < i ? 1u : 0u) ? 1 : 0;  // an earlier equal key counts
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < kRankLanes; o <<= 1) place += __shfl_xor(place, o);
+  if (i < N && part == 0) {
+    skey[place] = key;
+    spos[place] = (uint32_t)i;
   }
 }
 
+// Many positions: a stable radix sort of the keys, kDigit bits a pass (two
+// passes up to 2^18 - 1 tokens).  Per pass: a histogram per tile, and a scatter
+// in which each workgroup first adds up the tiles' histograms to its own
+// places (an exclusive scan in (digit, tile) order) and each wave ranks its
+// own stretch of the tile in order.  With more than kDirectTiles tiles those
+// sums would outgrow the sort, and a scan kernel between the two makes them.
+constexpr int kDigit = 9;
+constexpr int kDigits = 1 << kDigit;
+constexpr int kSortTile = 1024;
+constexpr int kSortWaves = kThreads / 64;
+constexpr int kRounds = kSortTile / kThreads;  // 64-element rounds per wave
+constexpr int64_t kDirectTiles = 256;
+
+// Element i of the pass: from the ids on the first pass (keys == null).
+__device__ inline uint32_t pass_key(const int32_t* ids, const uint32_t* keys, int64_t i, uint32_t V) {
+  return keys != nullptr ? keys[i] : key_of(ids, i, V);
+}
+
+// bits: null, or words to clear (a bit per token, set by the last scatter).
+__global__ void __launch_bounds__(kThreads) sort_hist_kernel(const int32_t* __restrict__ ids,
+                                                             const uint32_t* __restrict__ keys, int64_t N, uint32_t V,
+                                                             int shift, int tiles, uint32_t* __restrict__ hist,
+                                                             uint32_t* __restrict__ bits, int64_t words) {
+  __shared__ uint32_t h[kDigits];
+  for (int i = threadIdx.x; i < kDigits; i += kThreads) h[i] = 0;
+  if (bits != nullptr)
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (int64_t)tiles * kThreads) bits[i] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kSortTile;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = base + r * kThreads + threadIdx.x;
+    if (i < N) atomicAdd(&h[(pass_key(ids, keys, i, V) >> shift) & (kDigits - 1)], 1u);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kDigits; i += kThreads) hist[(int64_t)blockIdx.x * kDigits + i] = h[i];
+}
+
+// Exclusive scan of the histograms in (digit, tile) order in place, one
+// workgroup: thread t takes two digits, all tiles.
+static_assert(kDigits == 2 * kThreads, "two digits per thread");
+__global__ void __launch_bounds__(kThreads) sort_scan_kernel(uint32_t* __restrict__ hist, int64_t tiles) {
+  __shared__ uint32_t wsum[kThreads / 64];
+  uint2* h = (uint2*)hist;
+  uint32_t a = 0, b = 0;
+#pragma unroll 8
+  for (int64_t i = 0; i < tiles; ++i) {
+    const uint2 c = h[i * kThreads + threadIdx.x];
+    a += c.x;
+    b += c.y;
+  }
+  uint32_t ra = block_before(a + b, wsum), rb = ra + a;
+#pragma unroll 8
+  for (int64_t i = 0; i < tiles; ++i) {
+    const uint2 c = h[i * kThreads + threadIdx.x];
+    h[i * kThreads + threadIdx.x] = make_uint2(ra, rb);
+    ra += c.x;
+    rb += c.y;
+  }
+}
+
+// scanned: hist holds places (sort_scan_kernel) rather than counts.  bits: null,
+// or (last pass) where the tokens that occur are marked.
 __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* __restrict__ ids,
                                                                 const uint32_t* __restrict__ keys,
                                                                 const uint32_t* __restrict__ pos, int64_t N,
-                                                                uint32_t V, int shift, int tiles,
-                                                                const uint32_t* __restrict__ offs,
+                                                                uint32_t V, int shift, int tiles, bool scanned,
+                                                                const uint32_t* __restrict__ hist,
                                                                 uint32_t* __restrict__ keys_out,
-                                                                uint32_t* __restrict__ pos_out) {
+                                                                uint32_t* __restrict__ pos_out,
+                                                                uint32_t* __restrict__ bits) {
   __shared__ uint32_t cnt[kSortWaves][kDigits];
+  __shared__ uint32_t wsum[kSortWaves];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   for (int i = threadIdx.x; i < kSortWaves * kDigits; i += kThreads) (&cnt[0][0])[i] = 0;
-  __syncthreads();
   // wave w owns elements [64 kRounds w, 64 kRounds (w + 1)) of the tile, in order
   const int64_t base = (int64_t)blockIdx.x * kSortTile + (int64_t)w * 64 * kRounds;
   uint32_t key[kRounds], rank[kRounds];
@@ -241,6 +251,28 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
   for (int r = 0; r < kRounds; ++r) {
     const int64_t i = base + r * 64 + lane;
     key[r] = i < N ? pass_key(ids, keys, i, V) : 0xFFFFFFFFu;
+  }
+  // the places of this tile's digits 2 t and 2 t + 1
+  const uint2* h = (const uint2*)hist;
+  uint32_t pa, pb;
+  if (scanned) {
+    const uint2 c = h[(int64_t)blockIdx.x * kThreads + threadIdx.x];
+    pa = c.x;
+    pb = c.y;
+    __syncthreads();
+  } else {
+    uint32_t a = 0, b = 0, ea = 0, eb = 0;  // all tiles, earlier tiles
+#pragma unroll 8
+    for (int i = 0; i < tiles; ++i) {
+      const uint2 c = h[i * kThreads + threadIdx.x];
+      a += c.x;
+      b += c.y;
+      ea += i < (int)blockIdx.x ? c.x : 0;
+      eb += i < (int)blockIdx.x ? c.y : 0;
+    }
+    const uint32_t run = block_before(a + b, wsum);  // has a barrier: the counters are clear
+    pa = run + ea;
+    pb = run + a + eb;
   }
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
@@ -257,19 +289,20 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
     const uint32_t old = in ? cnt[w][dg] : 0;
     rank[r] = old + before;
     // one lane per digit moves the wave's counter on (LDS operations of one
-    // wave are in order; the barrier keeps the compiler from moving them)
+    // wave are in order; the barriers keep the compiler from moving them)
     __builtin_amdgcn_wave_barrier();
     if (in && before == 0) cnt[w][dg] = old + (uint32_t)__popcll(same);
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
-  // counts of the earlier waves, and the tile's place in the whole list
-  for (int d = threadIdx.x; d < kDigits; d += kThreads) {
-    uint32_t run = offs[(int64_t)d * tiles + blockIdx.x];
+  // counts of the earlier waves on top of the tile's places
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t run = q ? pb : pa;
 #pragma unroll
     for (int i = 0; i < kSortWaves; ++i) {
-      const uint32_t c = cnt[i][d];
-      cnt[i][d] = run;
+      const uint32_t c = cnt[i][2 * threadIdx.x + q];
+      cnt[i][2 * threadIdx.x + q] = run;
       run += c;
     }
   }
@@ -281,6 +314,9 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
       const uint32_t at = cnt[w][(key[r] >> shift) & (kDigits - 1)] + rank[r];
       keys_out[at] = key[r];
       pos_out[at] = pos != nullptr ? pos[i] : (uint32_t)i;
+      // the plain read spares a frequent token's word most of its atomics
+      if (bits != nullptr && key[r] < V && ((bits[key[r] >> 5] >> (key[r] & 31)) & 1u) == 0)
+        atomicOr(&bits[key[r] >> 5], 1u << (key[r] & 31));
     }
   }
 }
@@ -304,7 +340,11 @@ struct RunArgs {
   int accumulate;
   float* dW;
   float* part;
-  const uint32_t* bits;
+  const uint32_t* bits;  // a bit per token that occurs, or null: looked up in skey
+  int64_t sum_blocks;    // run_sum_kernel's workgroups that sum runs; its others write zeros
+  int64_t join_blocks;   // run_join_kernel's that join them; its others write zeros
+  int64_t zero_words;    // words of 32 tokens in all, and those of run_sum_kernel
+  int64_t zero_first;
 };
 
 // dst[0 .. kN) = scale acc, or += for accumulate; a partial row is stored as it is.
@@ -320,27 +360,56 @@ __device__ inline void store_row(float* dst, const float* acc, float scale, bool
 
 constexpr int kZeroRows = 32;  // table rows per zeroing workgroup: one word of bits
 
+// Whether token v occurs in the sorted keys (few positions).
+__device__ inline bool occurs(const uint32_t* skey, int64_t N, uint32_t v) {
+  int64_t lo = 0, hi = N;  // the first key >= v lies in [lo, hi]
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (skey[mid] < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo < N && skey[lo] == v;
+}
+
+// Zeros in the rows of absent tokens among the kZeroRows of block b (of n),
+// by all waves of the workgroup.  The blocks of one XCD (b % 8) take adjacent
+// words (1.4 % less time at 201,088 x 2,880 than words in block order).
+__device__ inline void zero_rows(const RunArgs& a, int64_t word0, int64_t n, int64_t b) {
+  const int64_t per = (n + 7) / 8, at = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || at >= n) return;
+  const int64_t word = word0 + at, v0 = word * kZeroRows;
+  const int lane = threadIdx.x & 63, waves = blockDim.x / 64;
+  uint32_t present;
+  if (a.bits != nullptr)
+    present = a.bits[word];
+  else
+    present = (uint32_t)__ballot(lane < kZeroRows && occurs(a.skey, a.N, (uint32_t)(v0 + lane)));
+  const int64_t cols4 = a.d / 4;
+  for (int r = threadIdx.x >> 6; r < kZeroRows; r += waves) {
+    if (v0 + r >= a.V || ((present >> r) & 1u)) continue;
+    f32x4_t* dst = (f32x4_t*)(a.dW + (v0 + r) * a.d);
+    for (int64_t c = lane; c < cols4; c += 64) dst[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+}
+// Blocks for n words: a whole number for each XCD.
+inline int64_t zero_blocks(int64_t n) { return (n + 7) / 8 * 8; }
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* __restrict__ dY, int64_t reduce_blocks,
-                                                           int groups) {
+__global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* __restrict__ dY, int groups) {
   constexpr int kN = Chunk<T>::kN;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if ((int64_t)blockIdx.x >= reduce_blocks) {
-    // rows of absent tokens
-    const int64_t word = (int64_t)blockIdx.x - reduce_blocks;
-    const uint32_t present = a.bits[word];
-    const int64_t v0 = word * kZeroRows;
-    const int64_t cols4 = a.d / 4;
-    for (int r = wave; r < kZeroRows; r += kThreads / 64) {
-      if (v0 + r >= a.V || ((present >> r) & 1u)) continue;
-      f32x4_t* dst = (f32x4_t*)(a.dW + (v0 + r) * a.d);
-      for (int64_t c = lane; c < cols4; c += 64) dst[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
+  // sums first: they wait for scattered reads, and the zeros' writes fill in
+  // (alternating the two instead took 6 % longer)
+  if ((int64_t)blockIdx.x >= a.sum_blocks) {
+    zero_rows(a, 0, a.zero_first, (int64_t)blockIdx.x - a.sum_blocks);
     return;
   }
-  const int64_t t = (int64_t)blockIdx.x / groups;
-  const int slice = (int)((int64_t)blockIdx.x - t * groups) * (kThreads / 64) + wave;
+  const int64_t sum_block = blockIdx.x;
+  const int64_t t = sum_block / groups;
+  const int slice = (int)(sum_block - t * groups) * (kThreads / 64) + wave;
   if (slice >= a.slices) return;
   const int c = slice * 64 + lane;
   const bool on = c < a.cpr;
@@ -395,14 +464,20 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* _
   flush(after == cur);
 }
 
-// Runs that cross tiles: the workgroup of the tile where such a run starts
-// sums its pieces.  Its waves take equal stretches of the tiles and wave 0
-// adds their sums in order.
+// Runs that cross tiles: the workgroup of the tile where such a run starts (one
+// per slice) sums its pieces.  Its waves take equal stretches of the tiles and
+// wave 0 adds their sums in order.  Most of these workgroups find no run and
+// the longest run takes 20 us, so a share of the zeros is left to this launch.
 constexpr int kJoinWaves = 8;
 template <int kN>
 __global__ void __launch_bounds__(kJoinWaves * 64) run_join_kernel(RunArgs a) {
   __shared__ float sums[kJoinWaves][64 * kN];
-  const int64_t t = blockIdx.x;
+  if ((int64_t)blockIdx.x >= a.join_blocks) {
+    zero_rows(a, a.zero_first, a.zero_words - a.zero_first, (int64_t)blockIdx.x - a.join_blocks);
+    return;
+  }
+  const int64_t t = blockIdx.x / a.slices;
+  const int slice = (int)(blockIdx.x - t * a.slices);
   const int64_t e = (t + 1) * a.tlen;
   if (e >= a.N) return;
   const uint32_t key = a.skey[e - 1];
@@ -421,35 +496,32 @@ __global__ void __launch_bounds__(kJoinWaves * 64) run_join_kernel(RunArgs a) {
   const int64_t pieces = lo - t + 1;  // piece 0 is tile t's second partial, piece i tile (t + i)'s first
   const int64_t per = (pieces + kJoinWaves - 1) / kJoinWaves;
   const int64_t p0 = w * per, p1 = p0 + per < pieces ? p0 + per : pieces;
-  for (int slice = blockIdx.y; slice < a.slices; slice += gridDim.y) {
-    const int c = slice * 64 + lane;
-    const bool on = c < a.cpr;
-    float acc[kN];
+  const int c = slice * 64 + lane;
+  const bool on = c < a.cpr;
+  float acc[kN];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) acc[i] = 0.f;
-    if (on) {
-#pragma unroll 4
-      for (int64_t p = p0; p < p1; ++p) {
-        const float* src = a.part + (p == 0 ? 2 * t + 1 : 2 * (t + p)) * a.d + (int64_t)c * kN;
+  for (int i = 0; i < kN; ++i) acc[i] = 0.f;
+  if (on) {
+#pragma unroll 8
+    for (int64_t p = p0; p < p1; ++p) {
+      const float* src = a.part + (p == 0 ? 2 * t + 1 : 2 * (t + p)) * a.d + (int64_t)c * kN;
 #pragma unroll
-        for (int q = 0; q < kN / 4; ++q) {
-          const f32x4_t v = *(const f32x4_t*)(src + 4 * q);
+      for (int q = 0; q < kN / 4; ++q) {
+        const f32x4_t v = *(const f32x4_t*)(src + 4 * q);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[4 * q + i] += v[i];
-        }
+        for (int i = 0; i < 4; ++i) acc[4 * q + i] += v[i];
       }
     }
-    __syncthreads();
+  }
 #pragma unroll
-    for (int i = 0; i < kN; ++i) sums[w][i * 64 + lane] = acc[i];
-    __syncthreads();
-    if (w == 0 && on) {
-      const int waves = (int)((pieces + per - 1) / per);
-      for (int j = 1; j < waves; ++j)
+  for (int i = 0; i < kN; ++i) sums[w][i * 64 + lane] = acc[i];
+  __syncthreads();
+  if (w == 0 && on) {
+    const int waves = (int)((pieces + per - 1) / per);
+    for (int j = 1; j < waves; ++j)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) acc[i] += sums[j][i * 64 + lane];
-      store_row<kN>(a.dW + (int64_t)key * a.d + (int64_t)c * kN, acc, a.scale, a.accumulate != 0);
-    }
+      for (int i = 0; i < kN; ++i) acc[i] += sums[j][i * 64 + lane];
+    store_row<kN>(a.dW + (int64_t)key * a.d + (int64_t)c * kN, acc, a.scale, a.accumulate != 0);
   }
 }
 
@@ -458,7 +530,7 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Sorted positions per tile: short tiles while there are few positions (more
 // waves in flight), long ones later (fewer partial rows).
-inline int tile_len(int64_t N) { return N <= 8192 ? 16 : N <= 65536 ? 32 : 64; }
+inline int tile_len(int64_t N) { return N <= 8192 ? 16 : N <= 16384 ? 32 : 64; }
 
 struct BwdLayout {
   int64_t tiles = 0, sort_tiles = 0;
@@ -491,18 +563,20 @@ BwdLayout bwd_layout(int64_t N, int64_t d, int64_t V) {
 }
 
 template <typename T>
-hipError_t launch_runs(RunArgs a, const void* dY, int64_t zero_blocks, hipStream_t s) {
+hipError_t launch_runs(RunArgs a, const void* dY, hipStream_t s) {
   constexpr int kN = Chunk<T>::kN;
   a.cpr = (int)(a.d / kN);
   a.slices = (int)cdiv(a.cpr, 64);
   const int groups = (int)cdiv(a.slices, kThreads / 64);
-  const int64_t reduce_blocks = a.tiles * groups;
-  hipLaunchKernelGGL(run_sum_kernel<T>, dim3((unsigned)(reduce_blocks + zero_blocks)), dim3(kThreads), 0, s, a,
-                     (const T*)dY, reduce_blocks, groups);
+  a.sum_blocks = a.tiles * groups;
+  a.join_blocks = (a.tiles - 1) * a.slices;
+  a.zero_first = a.join_blocks > 0 ? a.zero_words - a.zero_words / 4 : a.zero_words;
+  hipLaunchKernelGGL(run_sum_kernel<T>, dim3((unsigned)(a.sum_blocks + zero_blocks(a.zero_first))), dim3(kThreads), 0,
+                     s, a, (const T*)dY, groups);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.tiles < 2) return e;
-  hipLaunchKernelGGL(run_join_kernel<kN>, dim3((unsigned)(a.tiles - 1), (unsigned)a.slices), dim3(kJoinWaves * 64), 0,
-                     s, a);
+  if (e != hipSuccess || a.join_blocks == 0) return e;
+  hipLaunchKernelGGL(run_join_kernel<kN>, dim3((unsigned)(a.join_blocks + zero_blocks(a.zero_words - a.zero_first))),
+                     dim3(kJoinWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -528,7 +602,10 @@ uint64_t embed_bwd_workspace(int64_t N, int64_t d, int64_t V) { return N > 0 ? b
 int64_t embed_bwd_blocks(Dtype dt, int64_t N, int64_t d, int64_t V) {
   const int64_t slices = cdiv(d / (dt == DT_BF16 ? 8 : 4), 64);
   const int64_t tiles = cdiv(N, tile_len(N));
-  return tiles * cdiv(slices, kThreads / 64) + cdiv(V, kZeroRows);
+  const int64_t words = cdiv(V, kZeroRows) + 8;
+  const int64_t sum = tiles * cdiv(slices, kThreads / 64) + words;
+  const int64_t join = ((tiles - 1) * slices + words) * (kJoinWaves * 64 / kThreads);  // of twice the threads
+  return sum > join ? sum : join;
 }
 
 hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,
@@ -537,38 +614,37 @@ hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float 
   char* base = (char*)ws;
   uint32_t* skey = (uint32_t*)(base + L.key0);
   uint32_t* spos = (uint32_t*)(base + L.pos0);
-  // an accumulating call leaves the other rows alone and needs no bits
-  uint32_t* bits = accumulate ? nullptr : (uint32_t*)(base + L.bits);
+  uint32_t* bits = nullptr;
   hipError_t e = hipSuccess;
 #define EMBED_TRY()                            \
   if ((e = hipGetLastError()) != hipSuccess) return e
-  if (bits != nullptr) {
-    const int64_t words = cdiv(V, 32);
-    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)cdiv(words, kThreads)), dim3(kThreads), 0, s, bits, words);
-    EMBED_TRY();
-  }
   if (L.passes == 0) {
-    hipLaunchKernelGGL(rank_kernel, dim3((unsigned)cdiv(N, kThreads / 4)), dim3(kThreads), 0, s, ids, (int)N,
-                       (uint32_t)V, skey, spos, bits);
+    hipLaunchKernelGGL(rank_kernel, dim3((unsigned)cdiv(N, kThreads / kRankLanes)), dim3(kThreads), 0, s, ids, (int)N,
+                       (uint32_t)V, skey, spos);
     EMBED_TRY();
   } else {
+    // an accumulating call leaves the other rows alone and needs no bits
+    if (!accumulate) bits = (uint32_t*)(base + L.bits);
     uint32_t* key1 = (uint32_t*)(base + L.key1);
     uint32_t* pos1 = (uint32_t*)(base + L.pos1);
     uint32_t* hist = (uint32_t*)(base + L.hist);
     const uint32_t *kin = nullptr, *pin = nullptr;  // the first pass reads the ids
     const dim3 grid((unsigned)L.sort_tiles);
     const int st = (int)L.sort_tiles;
+    const bool scan = L.sort_tiles > kDirectTiles;
     for (int p = 0; p < L.passes; ++p) {
       // the last pass writes skey / spos
       uint32_t* kout = (L.passes - p) % 2 ? skey : key1;
       uint32_t* pout = (L.passes - p) % 2 ? spos : pos1;
       hipLaunchKernelGGL(sort_hist_kernel, grid, dim3(kThreads), 0, s, ids, kin, N, (uint32_t)V, p * kDigit, st, hist,
-                         bits);
+                         p == 0 ? bits : nullptr, cdiv(V, 32));
       EMBED_TRY();
-      hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, hist, (int64_t)st * kDigits);
-      EMBED_TRY();
+      if (scan) {
+        hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kThreads), 0, s, hist, L.sort_tiles);
+        EMBED_TRY();
+      }
       hipLaunchKernelGGL(sort_scatter_kernel, grid, dim3(kThreads), 0, s, ids, kin, pin, N, (uint32_t)V, p * kDigit, st,
-                         hist, kout, pout);
+                         scan, hist, kout, pout, p == L.passes - 1 ? bits : nullptr);
       EMBED_TRY();
       kin = kout;
       pin = pout;
@@ -588,8 +664,8 @@ hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float 
   a.dW = dW;
   a.part = (float*)(base + L.part);
   a.bits = bits;
-  const int64_t zero_blocks = bits != nullptr ? cdiv(V, kZeroRows) : 0;
-  return dt == DT_BF16 ? launch_runs<__bf16>(a, dY, zero_blocks, s) : launch_runs<float>(a, dY, zero_blocks, s);
+  a.zero_words = accumulate ? 0 : cdiv(V, kZeroRows);
+  return dt == DT_BF16 ? launch_runs<__bf16>(a, dY, s) : launch_runs<float>(a, dY, s);
 }
 
 }  // namespace ckl

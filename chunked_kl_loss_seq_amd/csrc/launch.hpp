@@ -97,7 +97,7 @@ hipError_t launch_embed(Dtype dt, const int32_t* ids, const void* W, float scale
 uint64_t embed_bwd_workspace(int64_t N, int64_t d, int64_t V);
 hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,
                             bool accumulate, float* dW, void* ws, hipStream_t s);
-// Workgroups of its largest launch.
+// Workgroups of its largest launch, in units of 256 threads.
 int64_t embed_bwd_blocks(Dtype dt, int64_t N, int64_t d, int64_t V);
 
 // Settings of a sampling call: one value for all rows, or a device array [N].
