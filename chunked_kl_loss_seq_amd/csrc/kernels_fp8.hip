@@ -283,12 +283,53 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Args p) {
 // BM ids x BN tokens, WM x (BN / 64) waves of (BM / WM) x 64.  The ring's stage
 // holds the tile's 128-byte rows of both operands (16-byte chunks XOR-swizzled
 // by the row) and the BN token scales of the block.
-// buffer_load_dword ... lds: as dma16, 4 bytes per lane.
+// Lane l's 16 (or 4) bytes at byte voff + soff of the resource go to LDS byte
+// lds_addr + 16 l (4 l); see dma16 for why these are written out.
+__device__ inline void dma16_at(const i32x4& rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
+               "s"(soff), "s"(lds_addr)
+               : "memory", "m0");
+}
 __device__ inline void dma4(const i32x4& rsrc, uint32_t voff, uint32_t lds_addr) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
                "s"(lds_addr)
                : "memory", "m0");
 }
+
+// Copies R rows x 128 bytes (one block of k) of an operand into LDS, laid out
+// as KTile.  One instruction of a wave fills 8 rows; a wave's next one lies
+// NW x 8 rows on, a multiple of the swizzle's period, so one lane offset serves
+// all and the rows' distance goes into the scalar offset.  Rows past the
+// operand lie past the resource's end, k past d only on the last block: both
+// read as zeros.
+template <int R, int NW>
+struct BlockDMA {
+  static constexpr int kBytes = R * kBlk;
+  static constexpr int kNI = kBytes / 1024 / NW;
+  static_assert(kBytes % (1024 * NW) == 0, "whole loads per wave");
+  static_assert((NW * 8) % 16 == 0 || kNI == 1, "the swizzle repeats every 16 rows");
+  uint64_t org;      // row 0 of the tile, k = 0
+  uint32_t voff, step, rows;
+  __device__ inline void init(const uint8_t* ptr, int64_t row0, int64_t ext, int64_t d, int wave, int lane) {
+    org = uniform64((uint64_t)ptr + (uint64_t)(row0 * d));
+    rows = (uint32_t)(ext - row0 < R ? ext - row0 : R);
+    const int row = wave * 8 + (lane >> 3);
+    voff = (uint32_t)row * (uint32_t)d + (uint32_t)(chunk(wave, lane) * 16);
+    step = (uint32_t)(NW * 8) * (uint32_t)d;
+  }
+  __device__ static inline int chunk(int wave, int lane) {
+    const int row = wave * 8 + (lane >> 3);
+    return (lane & 7) ^ ((row >> 1) & 7);
+  }
+  __device__ inline void issue(int64_t k0, int64_t d, uint32_t lds, int wave, int lane) const {
+    i32x4 rs = make_rsrc((const void*)(org + (uint64_t)k0));
+    rs.z = (int32_t)(rows * (uint32_t)d - (uint32_t)k0);
+    uint32_t v = voff;
+    if (d - k0 < kBlk && chunk(wave, lane) * 16 >= (int)(d - k0)) v = kOOB;
+#pragma unroll
+    for (int i = 0; i < kNI; ++i) dma16_at(rs, v, (uint32_t)i * step, lds + (uint32_t)((i * NW + wave) * 1024));
+  }
+};
 
 // 16 rows x 128 k: lane l gets row row0 + l % 16, 16-byte chunks l / 16 and 4 + l / 16.
 template <int R>
@@ -315,10 +356,8 @@ struct Frag8<float> {
 template <typename TO, int BM, int BN, int WM>
 __global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2))) fp8_tile_kernel(Fp8Args p, GemmParams g) {
   constexpr int WN = BN / 64, NW = WM * WN, WTM = BM / WM, FM = WTM / 16, FN = 4;
-  // the copies count in pairs of 8-bit values (d is even): 128-byte rows of 64 pairs
-  typedef SlabDMA<__bf16, BM, NW, true, kBlk> DA;
-  typedef SlabDMA<__bf16, BN, NW, true, kBlk> DB;
-  static_assert(DA::kEven && DB::kEven, "whole loads per wave");
+  typedef BlockDMA<BM, NW> DA;
+  typedef BlockDMA<BN, NW> DB;
   static_assert(WTM <= 128 && 128 % WTM == 0, "a wave's ids share one block of 128");
   constexpr int STAGE = DA::kBytes + DB::kBytes + BN * 4;
   constexpr int STORE = sizeof(TO) == 2 ? NW * 64 * WTM * 2 : 0;  // the epilogue's staging, in the ring's place
@@ -332,33 +371,29 @@ __global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2))
   const int64_t m0 = (int64_t)tc.tm * BM, n0 = (int64_t)tc.tn * BN;
   DA da;
   DB db;
-  da.init(g.a, m0, wave, lane);
-  db.init(g.b, n0, wave, lane);
-  const uint64_t a_org = uniform64((uint64_t)p.wq + (uint64_t)(m0 * p.d));
-  const uint64_t b_org = uniform64((uint64_t)p.xq + (uint64_t)(n0 * p.d));
+  da.init(p.wq, m0, p.V, p.d, wave, lane);
+  db.init(p.xq, n0, p.M, p.d, wave, lane);
   const uint64_t s_org = uniform64((uint64_t)p.xs + (uint64_t)n0 * 4);
-  // this lane's token scale of a block: wave w < WN copies those of tokens 64 w ..
-  const uint32_t s_off = n0 + wave * 64 + lane < p.M ? (uint32_t)(wave * 256 + lane * 4) : kOOB;
+  const uint32_t tokens = (uint32_t)(p.M - n0 < BN ? p.M - n0 : BN);
   auto issue = [&](int kb, int st) {
     const uint32_t at = lds0 + (uint32_t)(st * STAGE);
-    const uint64_t ka = a_org + (uint64_t)kb * kBlk, kbb = b_org + (uint64_t)kb * kBlk;
-    const int64_t left = p.d - (int64_t)kb * kBlk;
-    if (left >= kBlk) {
-      da.issue_full(ka, at, wave, at);
-      db.issue_full(kbb, at + DA::kBytes, wave, at);
-    } else {
-      da.issue_tail(ka, at, wave, lane, at, (int)(left / 2));
-      db.issue_tail(kbb, at + DA::kBytes, wave, lane, at, (int)(left / 2));
+    const int64_t k0 = (int64_t)kb * kBlk;
+    if (wave < WN) {  // wave w: the scales of tokens 64 w ..
+      i32x4 rs = make_rsrc((const void*)(s_org + (uint64_t)kb * (uint64_t)p.M * 4));
+      rs.z = (int32_t)(tokens * 4);
+      dma4(rs, (uint32_t)tid * 4u, at + DA::kBytes + DB::kBytes + (uint32_t)wave * 256u);
     }
-    if (wave < WN)
-      dma4(make_rsrc((const void*)(s_org + (uint64_t)kb * (uint64_t)p.M * 4)), s_off,
-           at + DA::kBytes + DB::kBytes + (uint32_t)wave * 256u);
+    da.issue(k0, p.d, at, wave, lane);
+    db.issue(k0, p.d, at + DA::kBytes, wave, lane);
   };
-  // the wave's weight scales (one per block of k); ids past V are not stored
+  // The wave's weight scales, one per block of k: lane l holds block
+  // 64 (kb / 64) + l, so that a block costs one v_readlane and no load's wait.
+  // Ids past V are not stored and take the last scales.
   const int64_t vb_max = (p.V - 1) / kBlk;
   int64_t vb = (m0 + wm * WTM) / kBlk;
   if (vb > vb_max) vb = vb_max;
   const float* wscale = p.ws + vb * p.kb;
+  float wsv = 0.f;
 
   f32x4 acc[FM][FN];
 #pragma unroll
@@ -367,14 +402,17 @@ __global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2))
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int c = lane & 15, q = lane >> 4;
   issue(0, 0);
-  float sw = wscale[0];
   for (int kb = 0; kb < p.kb; ++kb) {
     const int st = kb & 1;
     // block kb has landed, and every wave has left the other stage
     wait_vmcnt<0>();
     __syncthreads();
+    if ((kb & 63) == 0) {
+      wsv = wscale[kb + lane < p.kb ? kb + lane : p.kb - 1];
+      asm volatile("" : "+v"(wsv));  // waited for here: behind the copies, the wait would cover them too
+    }
     if (kb + 1 < p.kb) issue(kb + 1, st ^ 1);
-    const float sw_next = wscale[kb + 1 < p.kb ? kb + 1 : kb];
+    const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv), kb & 63));
     const char* sa = smem + st * STAGE;
     const char* sb = sa + DA::kBytes;
     const float* sc = (const float*)(sb + DB::kBytes) + wn * 64 + c;
@@ -385,17 +423,42 @@ __global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2))
       b[j] = Frag8<TO>::of(load_frag8<BN>(sb, wn * 64 + 16 * j, lane));
       s[j] = sc[16 * j] * sw;
     }
+    // Row i's products run while row i - 1's are scaled and added, so that no
+    // vector instruction waits for the matrix instruction before it, and row
+    // i + 1's fragment loads.  The fences keep the scheduler from loading all
+    // fragments at once, which spills.
+    typename Frag8<TO>::type a = Frag8<TO>::of(load_frag8<BM>(sa, wm * WTM, lane));
+    f32x4 t[2][FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const typename Frag8<TO>::type a = Frag8<TO>::of(load_frag8<BM>(sa, wm * WTM + 16 * i, lane));
+    for (int i = 0; i <= FM; ++i) {
+      i32x8 an;
+      if (i + 1 < FM) an = load_frag8<BM>(sa, wm * WTM + 16 * (i + 1), lane);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const f32x4 t = block_product(a, b[j]);
+        if (i < FM) t[i & 1][j] = block_product(a, b[j]);
+        if (i > 0)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(t[r], s[j], acc[i][j][r]);
+          for (int r = 0; r < 4; ++r)
+            acc[i - 1][j][r] = __builtin_fmaf(t[(i - 1) & 1][j][r], s[j], acc[i - 1][j][r]);
       }
+      // the sums are wanted here, not moved to the end of the block of k
+      if (i > 0)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i - 1][j]));
+      if (i + 1 < FM) a = Frag8<TO>::of(an);
+      if constexpr (sizeof(TO) == 2) {
+        // one product, then the four additions of an earlier one
+        if (i > 0 && i < FM) {
+          if (i + 1 < FM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    sw = sw_next;
   }
 
   // Lane (c, q), slot r of block (i, j) holds id mw + 16 i + 4 q + r of token nw + 16 j + c.
@@ -460,8 +523,6 @@ __global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2))
 template <typename TO, int BM, int BN, int WM>
 hipError_t launch_tiles(const Fp8Args& p, hipStream_t s) {
   GemmParams g{};
-  g.a = Operand{p.wq, p.d / 2, p.V, p.d / 2, 0};  // in pairs of values
-  g.b = Operand{p.xq, p.d / 2, p.M, p.d / 2, 0};
   g.tiles_m = cdiv64(p.V, BM);
   g.tiles_n = cdiv64(p.M, BN);
   g.splits = 1;

@@ -11,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-from .binding import DTYPE_BF16, DTYPE_F32, Sampling, _check, _check_out, _ptr, _stream, lib, topk
+from .binding import DTYPE_BF16, DTYPE_F32, Sampling, _check, _check_out, _ptr, lib, topk
 
 
 def _dtype(torch, t, name):
@@ -33,6 +33,13 @@ def _on(torch, device):
     if torch.cuda.current_device() == device.index:
         return contextlib.nullcontext()
     return torch.cuda.device(device)
+
+
+def _stream(torch, device):
+    """The current stream's handle.  torch's own short way to it spares a call on a
+    few rows 2 of its 10 us; without it, through the Stream object."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _check_ids(torch, ids, device):
