@@ -533,19 +533,48 @@ hipError_t launch_tiles(const Fp8Args& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The product by the tile that is expected to end first: a tile takes `alone`
+// microseconds per block of k where it has a compute unit to itself, and the
+// 256 units together finish 256 tiles per `full` microseconds of each block
+// where there are many (bf16 results; fp32 results take about 1.6 times as long
+// for every tile).  Measured, in us (256 x 256, 128 x 128, 128 x 64, 64 x 64):
+//   2,048 x 201,088 x 2,880: 1,277 1,499 - -    300 x 100,000 x 512: 44 35 35 44
+//   128 x 201,088 x 2,880: 224 163 - -          1,000 x 5,000 x 1,024: 20 14 14 15
+//   256 x 32,000 x 2,048: 33 23 29 34           40 x 5,000 x 4,096: 49 23 18 15
+struct TileCost {
+  int bm, bn;
+  double alone, full;
+};
+constexpr TileCost kTileCosts[] = {{256, 256, 1.5, 2.26}, {128, 128, 0.90, 0.66}, {128, 64, 0.57, 0.44}, {64, 64, 0.48, 0.28}};
+
 template <typename TO>
 hipError_t launch_product(const Fp8Args& p, hipStream_t s) {
-  if (p.M <= kFewRows) {
+  // Few rows and fewer 64 x 64 tiles than compute units: the k blocks are split
+  // over waves instead (8 x 10,000 x 4,096: 15 us, by tiles 19; with 500 tiles,
+  // 4 x 32,000 x 2,048, 17 and 13).
+  if (p.M <= kFewRows && p.V < 64 * 256) {
     hipLaunchKernelGGL(fp8_few_kernel<TO>, dim3((unsigned)((p.V + kFewIds - 1) / kFewIds)), dim3(kFewWaves * 64), 0, s,
                        p);
     return hipGetLastError();
   }
-  // the largest tile that still leaves a tile per compute unit
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.V + bm - 1) / bm) * ((p.M + bn - 1) / bn); };
-  if (p.M > 128 && tiles(256, 256) >= 256) return launch_tiles<TO, 256, 256, 2>(p, s);
-  if (p.M > 64 && tiles(256, 128) >= 256) return launch_tiles<TO, 256, 128, 4>(p, s);
-  if (tiles(128, 64) >= 256) return launch_tiles<TO, 128, 64, 4>(p, s);
-  return launch_tiles<TO, 64, 64, 4>(p, s);
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    const TileCost& c = kTileCosts[i];
+    const int64_t tiles = ((p.V + c.bm - 1) / c.bm) * ((p.M + c.bn - 1) / c.bn);
+    const double us = (double)((tiles + 255) / 256) * c.full;
+    const double cost = us > c.alone ? us : c.alone;
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  switch (best) {
+    case 0: return launch_tiles<TO, 256, 256, 2>(p, s);
+    case 1: return launch_tiles<TO, 128, 128, 2>(p, s);
+    case 2: return launch_tiles<TO, 128, 64, 4>(p, s);
+    default: return launch_tiles<TO, 64, 64, 4>(p, s);
+  }
 }
 
 }  // namespace
