@@ -26,12 +26,16 @@
 // columns: a lane holds one token and four consecutive ids, so its scale is
 // one register and its results are adjacent in memory.
 //
-//   * M <= 16 (decode): bound by reading the weight.  Weight rows go straight
-//     from memory to registers, no LDS; four waves share 32 rows, each taking
-//     a quarter of the k blocks, and add their sums through LDS.
-//   * more rows: tiles staged through a two-stage LDS ring by LDS DMA, one
-//     barrier per block of k, the tile size chosen so that there are enough
-//     tiles to fill the chip.
+//   * M <= 16 and a short weight: too few tiles to fill the chip.  Weight rows
+//     go straight from memory to registers, no LDS; four waves share 32 rows,
+//     each taking a quarter of the k blocks, and add their sums through LDS.
+//   * else tiles staged through a two-stage LDS ring by LDS DMA, one barrier
+//     per block of k, of the size that is expected to end first.  Up to about
+//     128 rows this is bound by reading the weight (1 x 201,088 x 2,880: 114 us,
+//     5.1 TB/s), beyond by the board's power: 2,048 x 201,088 x 2,880 takes
+//     1,277 us (1,860 TFLOP/s) with the matrix cores busy 39 % of the cycles at
+//     1.77 GHz; loading the next block's fragments across the barrier made them
+//     busy 48 % of the cycles, at 1.56 GHz, in the same time.
 #include "gemm_core.hpp"
 #include "launch.hpp"
 
