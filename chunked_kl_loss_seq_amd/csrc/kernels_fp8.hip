@@ -26,13 +26,14 @@
 // columns: a lane holds one token and four consecutive ids, so its scale is
 // one register and its results are adjacent in memory.
 //
-//   * M <= 16 and a short weight: too few tiles to fill the chip.  Weight rows
+//   * M <= 16 and a short weight (too few tiles to fill the chip), or M <= 2 and a
+//     very long one.  Weight rows
 //     go straight from memory to registers, no LDS; four waves share 32 rows,
 //     each taking a quarter of the k blocks, and add their sums through LDS.
 //   * else tiles staged through a two-stage LDS ring by LDS DMA, one barrier
 //     per block of k, of the size that is expected to end first.  Up to about
-//     128 rows this is bound by reading the weight (1 x 201,088 x 2,880: 114 us,
-//     5.1 TB/s), beyond by the board's power: 2,048 x 201,088 x 2,880 takes
+//     128 rows this is bound by reading the weight (16 x 201,088 x 2,880: 121 us,
+//     4.8 TB/s), beyond by the board's power: 2,048 x 201,088 x 2,880 takes
 //     1,277 us (1,860 TFLOP/s) with the matrix cores busy 39 % of the cycles at
 //     1.77 GHz; loading the next block's fragments across the barrier made them
 //     busy 48 % of the cycles, at 1.56 GHz, in the same time.
@@ -555,8 +556,10 @@ template <typename TO>
 hipError_t launch_product(const Fp8Args& p, hipStream_t s) {
   // Few rows and fewer 64 x 64 tiles than compute units: the k blocks are split
   // over waves instead (8 x 10,000 x 4,096: 15 us, by tiles 19; with 500 tiles,
-  // 4 x 32,000 x 2,048, 17 and 13).
-  if (p.M <= kFewRows && p.V < 64 * 256) {
+  // 4 x 32,000 x 2,048, 17 and 13).  Also one or two rows of a weight beyond the
+  // 256 MB last-level cache, which come straight from memory: 1 x 201,088 x
+  // 2,880 105 us (5.5 TB/s), by tiles 113.
+  if (p.M <= kFewRows && (p.V < 64 * 256 || (p.M <= 2 && p.V * p.d > (int64_t)256 << 20))) {
     hipLaunchKernelGGL(fp8_few_kernel<TO>, dim3((unsigned)((p.V + kFewIds - 1) / kFewIds)), dim3(kFewWaves * 64), 0, s,
                        p);
     return hipGetLastError();

@@ -29,6 +29,8 @@
 //     its rank in id order.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "launch.hpp"
 
 namespace ckl {
@@ -157,20 +159,58 @@ __device__ inline void for_each(const Row<T>& row, F&& fn) {
       [&](T x, int64_t id) { fn((float)x, id); });
 }
 
-// The masses of one row.  y = -64 log2(e) of a logit; a bin is floor(y).
+// The masses of one row.  y = -64 log2(e) of a logit, in fp64; its bin is the
+// whole part of the same in fp32 (monotone in the logit and within 1e-3 of y,
+// at a fifth of the cost), so that y - bin lies in [-1e-3, 1 + 1e-3].
 struct Scale {
-  double mx, c, fix;  // c = 64 log2(e) / T; fix = 2^shift of the integer masses
-  bool inf;           // the largest logit is +inf: equal ones weigh 1, all others nothing
+  double mx, c;        // c = 64 log2(e) / T
+  double fix, inv_fix; // 2^shift of the integer masses, and its inverse
+  float mxf, cf;
+  bool inf;            // the largest logit is +inf: equal ones weigh 1, all others nothing
+  bool wide;           // c or the logits' differences may leave fp32's range
+  __device__ inline void set(float m, double T, int fix_bits) {
+    inf = m == INFINITY;
+    mx = (double)m;
+    c = 92.332482616893656877 / T;
+    fix = (double)(1ull << fix_bits);
+    inv_fix = 1.0 / fix;
+    mxf = m;
+    cf = (float)c;
+    wide = !(c > 1e-30 && c < 1e30);
+  }
   __device__ inline double y(float l) const {
     if (inf) return l == INFINITY ? 0.0 : (double)INFINITY;
     // -inf (and NaN, by the comparison below being false) weighs nothing
     return l > -INFINITY ? (mx - (double)l) * c : (double)INFINITY;
   }
+  // a logit's place among the bins; kBins and more, or NaN, where it has none
+  // (-inf and NaN never have one).  kPlain: neither inf nor wide.
+  template <bool kPlain>
+  __device__ inline float place(float l) const {
+    if constexpr (kPlain) return (mxf - l) * cf;
+    if (inf) return l == INFINITY ? 0.f : INFINITY;
+    return (float)((mx - (double)l) * c);
+  }
+  // y - bin of a logit in that bin
+  template <bool kPlain>
+  __device__ inline double frac(float l, int bin) const {
+    if (!kPlain && inf) return 0.0;
+    return __builtin_fma(mx - (double)l, c, -(double)bin);
+  }
+  // fn(true_type) for plain rows, fn(false_type) for the others: the choice is
+  // made once per pass over the row
+  template <typename F>
+  __device__ inline void either(F&& fn) const {
+    if (!inf && !wide)
+      fn(std::true_type{});
+    else
+      fn(std::false_type{});
+  }
 };
 
-// 2^(-f / 64) for f in [0, 1): the polynomial of degree 4 through the Chebyshev
-// points of [0, 1], its constant moved to 1 so that f = 0 is exact; off by at
-// most 5e-15.
+// 2^(-f / 64) for f in [-1e-3, 1 + 1e-3]: the polynomial of degree 4 through the
+// Chebyshev points of [0, 1], its constant moved to 1 so that f = 0 is exact;
+// off by at most 5e-15.
 __device__ inline double pow_frac(double f) {
   double r = 5.701897951327709e-10;
   r = __builtin_fma(r, f, -2.1172866563406743e-07);
@@ -198,13 +238,13 @@ __device__ inline double mass_of(const Red& red, double y) {
 }
 
 struct Shared {
-  uint64_t mass[kBins];       // integer masses relative to each bin's upper edge
+  uint64_t mass[kBins];       // integer masses relative to each bin's upper edge, then (fp64) masses
   uint32_t count[kBins];      // tokens per bin (kept while k limits)
   uint64_t cand[kCap];        // collected (key, id)
   uint64_t sub_mass[kSub];    // a narrowing pass
   uint32_t sub_count[kSub];
   Red red;
-  uint64_t edge_mass;         // mass of the tokens of min_p's bin that reach it
+  uint64_t edge_mass[3];      // mass of the tokens of min_p's bin and of its neighbours that reach it
   uint32_t n_cand;
   uint32_t pick;
   uint32_t nth[2];
@@ -291,6 +331,7 @@ __device__ inline void sort_cand(Shared& sh, int n) {
     int place = 0;
     if ((int)threadIdx.x < n) {
       c = a[threadIdx.x];
+#pragma unroll 8
       for (int i = 0; i < n; ++i) place += a[i] > c;
     }
     __syncthreads();
@@ -317,6 +358,17 @@ __device__ inline void sort_cand(Shared& sh, int n) {
       __syncthreads();
     }
   }
+}
+
+// *slot = the least v of the threads with `hit`, v growing with the thread: one
+// atomic per wave (one per thread would pass through the LDS one by one).
+__device__ inline void min_of_hits(bool hit, uint32_t v, uint32_t* slot) {
+  const uint64_t m = __ballot(hit);
+  if (hit && (threadIdx.x & 63) == __builtin_ctzll(m)) atomicMin(slot, v);
+}
+__device__ inline void max_of_hits(bool hit, uint32_t v, uint32_t* slot) {
+  const uint64_t m = __ballot(hit);
+  if (hit && (threadIdx.x & 63) == 63 - __builtin_clzll(m)) atomicMax(slot, v);
 }
 
 enum Border : int { BY_COUNT = 0, BY_MASS = 1, BY_MASS_OVER = 2 };  // the k-th token; mass >= target; mass > target
@@ -351,7 +403,7 @@ __device__ inline int pick_in_list(Shared& sh, int n, const Scale& sc, int kind,
     run += e[i];
     if (at < 0 && b + i < n && reached(kind, above_n + (uint32_t)(b + i + 1), run, k, target)) at = b + i;
   }
-  if (at >= 0) atomicMin(&sh.pick, (uint32_t)at);
+  min_of_hits(at >= 0, (uint32_t)at, &sh.pick);
   __syncthreads();
   const int j = sh.pick < (uint32_t)n ? (int)sh.pick : n - 1;
   run = above + before;
@@ -407,7 +459,7 @@ __device__ inline bool may_equal(const u32x4_t& v, float l, __bf16*) {
 // wave alike goes through the group that holds the r-th.  cnt: kGroups words of LDS, pick: two.
 constexpr int kGroups = 2 * kThreads;
 template <typename T>
-__device__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l, uint32_t r) {
+__device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l, uint32_t r) {
   constexpr int U = kFlight;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   // the r-th set bit of a mask of lanes
@@ -522,23 +574,13 @@ struct Found {
   int64_t id;
 };
 
+// before, cbefore: mass and (for BY_COUNT) tokens of the bins of earlier threads.
 template <typename T>
-__device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int kind, uint32_t k, double target,
-                             bool want_id) {
+__device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int kind, uint32_t k, double target,
+                             double before, uint32_t cbefore, bool want_id) {
   const int tid = threadIdx.x;
   // 1. the bin: thread t holds the bins [kPerThread t, kPerThread (t + 1))
-  double m[kPerThread], mine = 0.0, before = 0.0;
-  uint32_t cmine = 0, cbefore = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
-    const uint64_t q = sh.mass[b];
-    m[i] = q ? (double)q / sc.fix * bin_top(sh.red, b) : 0.0;
-    mine += m[i];
-    cmine += sh.count[b];
-  }
-  block_prefix(mine, sh.red, &before);
-  if (kind == BY_COUNT) block_prefix(cmine, sh.red, &cbefore);
+  const double* mass = (const double*)sh.mass;
   if (tid == 0) sh.pick = 0xFFFFFFFFu;
   __syncthreads();
   // the first bin at whose end the border is reached, else the last with mass
@@ -548,20 +590,20 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int b = tid * kPerThread + i;
-    run += m[i];
+    run += mass[b];
     crun += kind == BY_COUNT ? sh.count[b] : 0;
-    if (sh.mass[b] != 0) {
+    if (mass[b] != 0.0) {
       last = b;
       if (at < 0 && reached(kind, crun, run, k, target)) at = b;
     }
   }
-  if (at >= 0) atomicMin(&sh.pick, (uint32_t)at);
+  min_of_hits(at >= 0, (uint32_t)at, &sh.pick);
   __syncthreads();
   if (sh.pick == 0xFFFFFFFFu) {
     __syncthreads();
     if (tid == 0) sh.n_cand = 0;
     __syncthreads();
-    if (last >= 0) atomicMax(&sh.n_cand, (uint32_t)last);
+    max_of_hits(last >= 0, (uint32_t)last, &sh.n_cand);
     __syncthreads();
     if (tid == 0) sh.pick = sh.n_cand;
     __syncthreads();
@@ -573,7 +615,7 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       if (tid * kPerThread + i < bin) {
-        r += m[i];
+        r += mass[tid * kPerThread + i];
         c += kind == BY_COUNT ? sh.count[tid * kPerThread + i] : 0;
       }
     }
@@ -583,22 +625,8 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
   __syncthreads();
   double above = sh.pick_mass;
   uint32_t above_n = sh.pick_count;
-  const double top = bin_top(sh.red, bin), y0 = (double)bin, y1 = (double)(bin + 1);
-  // a float interval around the bin's logits: a cheap first test of each value
-  // (c may be 0 or tiny: the interval is then the whole line)
-  float lo = -INFINITY, hi = INFINITY;
-  if (!sc.inf && sc.c > 0.0) {
-    const double a = sc.mx - y1 / sc.c, b = sc.mx - y0 / sc.c;
-    const double slack = 1e-9 * fabs(sc.mx) + 1e-30;  // far above the rounding of a, b and y
-    lo = (float)(a - 1e-5 * fabs(a) - slack);
-    hi = (float)(b + 1e-5 * fabs(b) + slack);
-  }
-  auto in_bin = [&](float l) {
-    if (!(l >= lo && l <= hi)) return false;
-    const double y = sc.y(l);
-    return y >= y0 && y < y1;
-  };
-
+  const double top = bin_top(sh.red, bin);
+  const float p0 = (float)bin, p1 = (float)(bin + 1);
   // 2. the bin's tokens, narrowed by key digits until they fit
   uint32_t prefix = 0, prefix_mask = 0;
   int digits_left = Key<T>::kBits;
@@ -606,14 +634,17 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
     __syncthreads();
     if (tid == 0) sh.n_cand = 0;
     __syncthreads();
+    sc.either([&](auto plain) {
     for_each(row, [&](float l, int64_t id) {
-      if (in_bin(l)) {
+      const float place = sc.template place<plain.value>(l);
+      if (place >= p0 && place < p1) {
         const uint32_t key = Key<T>::of(l);
         if ((key & prefix_mask) == prefix) {
           const uint32_t slot = atomicAdd(&sh.n_cand, 1u);
           if (slot < (uint32_t)kCap) sh.cand[slot] = pack(key, (uint32_t)id);
         }
       }
+    });
     });
     __syncthreads();
     const uint32_t n = sh.n_cand;
@@ -633,19 +664,22 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
       sh.sub_count[i] = 0;
     }
     __syncthreads();
-    for_each(row, [&](float l, int64_t id) {
-      if (in_bin(l)) {
+    sc.either([&](auto plain) {
+    for_each(row, [&](float l, int64_t) {
+      const float place = sc.template place<plain.value>(l);
+      if (place >= p0 && place < p1) {
         const uint32_t key = Key<T>::of(l);
         if ((key & prefix_mask) == prefix) {
-          const double y = sc.y(l);
           const uint32_t dg = 255u - ((key >> digits_left) & 255u);
-          atomicAdd((unsigned long long*)&sh.sub_mass[dg], (unsigned long long)(pow_frac(y - y0) * sc.fix + 0.5));
+          atomicAdd((unsigned long long*)&sh.sub_mass[dg],
+                    (unsigned long long)(pow_frac(sc.template frac<plain.value>(l, bin)) * sc.fix + 0.5));
           atomicAdd(&sh.sub_count[dg], 1u);
         }
       }
     });
+    });
     __syncthreads();
-    const double dm = tid < kSub && sh.sub_count[tid] ? (double)sh.sub_mass[tid] / sc.fix * top : 0.0;
+    const double dm = tid < kSub && sh.sub_count[tid] ? (double)sh.sub_mass[tid] * sc.inv_fix * top : 0.0;
     const uint32_t dc = tid < kSub ? sh.sub_count[tid] : 0;
     double db = 0.0;
     uint32_t cb = 0;
@@ -656,8 +690,8 @@ __device__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int
       sh.n_cand = 0;
     }
     __syncthreads();
-    if (dc && reached(kind, above_n + cb + dc, above + db + dm, k, target)) atomicMin(&sh.pick, (uint32_t)tid);
-    if (dc) atomicMax(&sh.n_cand, (uint32_t)tid);
+    min_of_hits(dc && reached(kind, above_n + cb + dc, above + db + dm, k, target), (uint32_t)tid, &sh.pick);
+    max_of_hits(dc != 0, (uint32_t)tid, &sh.n_cand);
     __syncthreads();
     const uint32_t dg = sh.pick == 0xFFFFFFFFu ? sh.n_cand : sh.pick;
     if ((uint32_t)tid == dg) {
@@ -773,7 +807,7 @@ struct Settings {
 // From the counts in sh.cnt: the logit of the drawn token, which of the equal
 // ones it is (r >= 1; 0: nothing to draw), and its log-probability.  False:
 // the row is one for the general path.
-__device__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Settings& how, float* logit, uint32_t* nth,
+__device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Settings& how, float* logit, uint32_t* nth,
                              double* logp) {
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int kPer = Counted::kPer;
@@ -793,10 +827,7 @@ __device__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Sett
   const bool low = sh.cnt[Counted::kSign + Counted::kW + 1] != 0;  // -256 and less, -inf or NaN
   if (first == 0xFFFFFFFFu) return false;
   Scale sc;
-  sc.inf = false;
-  sc.mx = (double)Counted::value((int)first);
-  sc.c = 92.332482616893656877 / how.T;
-  sc.fix = 1.0;
+  sc.set(Counted::value((int)first), how.T, 0);
   if (low && sc.y(-256.f) < (double)kBins) return false;
   double sum = 0.0, likely = 0.0, before = 0.0, dummy;
   uint32_t cbefore = 0;
@@ -830,10 +861,8 @@ __device__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Sett
       sh.last = 0;
     }
     __syncthreads();
-    const uint64_t hit = __ballot(sum > 0.0 && reached(kind, cbefore + mine, before + sum, how.k, target));
-    const uint64_t has = __ballot(sum > 0.0);
-    if (hit && lane == __builtin_ctzll(hit)) atomicMin(&sh.pick, (uint32_t)tid);
-    if (has && lane == 63 - __builtin_clzll(has)) atomicMax(&sh.last, (uint32_t)tid);
+    min_of_hits(sum > 0.0 && reached(kind, cbefore + mine, before + sum, how.k, target), (uint32_t)tid, &sh.pick);
+    max_of_hits(sum > 0.0, (uint32_t)tid, &sh.last);
     __syncthreads();
     const uint32_t at = sh.pick != 0xFFFFFFFFu ? sh.pick : sh.last;
     if ((uint32_t)tid == at) {
@@ -1034,10 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     return;
   }
   Scale sc;
-  sc.inf = mx == INFINITY;
-  sc.mx = (double)mx;
-  sc.c = 92.332482616893656877 / how.T;  // 64 log2(e)
-  sc.fix = (double)(1ull << a.fix_bits);
+  sc.set(mx, how.T, a.fix_bits);
 
   // 2a. few tokens: those that reach the k-th largest of the threads' maxima
   if (sizeof(T) == 4 && k <= (uint32_t)kFastK) {
@@ -1116,45 +1142,58 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     sh.mass[i] = 0;
     sh.count[i] = 0;
   }
-  if (tid == 0) sh.edge_mass = 0;
+  if (tid < 3) sh.edge_mass[tid] = 0;
   __syncthreads();
-  // min_p's border: y <= y_min; its bin's share is summed on the side
+  // min_p's border: y <= y_min; the share of its bin and of the two beside it
+  // (a bin is only within 1e-3 of y) is summed on the side
   const double y_min = min_p > 0.0 ? -64.0 * log2(min_p) : (double)INFINITY;
-  const int bin_min = y_min < (double)kBins ? (int)y_min : kBins;
+  const int bin_min = y_min < (double)kBins ? (int)y_min : 2 * kBins;
+  sc.either([&](auto plain) {
   for_each(row, [&](float l, int64_t) {
-    const double y = sc.y(l);
-    if (y < (double)kBins) {
-      const double b = floor(y);
-      const int bin = (int)b;
+    const float place = sc.template place<plain.value>(l);
+    if (place < (float)kBins) {
+      const int bin = (int)place;
       // round to an integer by adding 2^52: the low bits of the sum are it
-      const double q = __builtin_fma(pow_frac(y - b), sc.fix, 0x1p52);
+      const double q = __builtin_fma(pow_frac(sc.template frac<plain.value>(l, bin)), sc.fix, 0x1p52);
       const unsigned long long qi = (unsigned long long)__builtin_bit_cast(uint64_t, q) & 0xFFFFFFFFFFFFFull;
       atomicAdd((unsigned long long*)&sh.mass[bin], qi);
       if (limit) atomicAdd(&sh.count[bin], 1u);
-      if (bin == bin_min && y <= y_min) atomicAdd((unsigned long long*)&sh.edge_mass, qi);
+      const uint32_t near = (uint32_t)(bin - bin_min + 1);
+      if (near < 3u && sc.y(l) <= y_min) atomicAdd((unsigned long long*)&sh.edge_mass[near], qi);
     }
   });
+  });
   __syncthreads();
-  // masses of the whole row and of the tokens that reach min_p
-  double S = 0.0, s_min = 0.0;
+  // masses of the bins, of the whole row and of the tokens that reach min_p
+  double S = 0.0, s_min = 0.0, before = 0.0;
+  uint32_t cbefore = 0;
   {
     double all = 0.0, likely = 0.0, dummy;
+    uint32_t tokens = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int b = tid * kPerThread + i;
-      const double m = sh.mass[b] ? (double)sh.mass[b] / sc.fix * bin_top(sh.red, b) : 0.0;
+      const double unit = sc.inv_fix * bin_top(sh.red, b);
+      const double m = (double)sh.mass[b] * unit;
+      ((double*)sh.mass)[b] = m;
       all += m;
-      if (b < bin_min) likely += m;
-      if (b == bin_min) likely += (double)sh.edge_mass / sc.fix * bin_top(sh.red, b);
+      tokens += sh.count[b];
+      const uint32_t near = (uint32_t)(b - bin_min + 1);
+      if (near < 3u)
+        likely += (double)sh.edge_mass[near] * unit;
+      else if (b < bin_min)
+        likely += m;
     }
-    S = block_prefix(all, sh.red, &dummy);
+    S = block_prefix(all, sh.red, &before);
+    if (limit) block_prefix(tokens, sh.red, &cbefore);
     s_min = min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
   }
   Found f;
 #pragma unroll 1
   for (int kind = limit ? BY_COUNT : p < 1.0 ? BY_MASS : BY_MASS_OVER;;) {
     if (kind == BY_MASS_OVER) S = fmin(S, s_min);
-    f = find_border(row, sh, sc, kind, k, kind == BY_MASS ? p * S : u * S, kind == BY_MASS_OVER);
+    f = find_border(row, sh, sc, kind, k, kind == BY_MASS ? p * S : u * S, before, cbefore,
+                    kind == BY_MASS_OVER);
     if (kind == BY_MASS_OVER) break;
     S = fmin(S, f.mass);
     kind = kind == BY_COUNT && p < 1.0 ? BY_MASS : BY_MASS_OVER;
