@@ -912,7 +912,9 @@ struct SampleArgs {
   int fix_bits;
   int32_t* ids;
   float* logp;
+  // direct: no counting kernel runs first
   // split rows (slices > 1): logits per slice, and the slices' counts
+  bool direct;
   int slices;
   int64_t slice_len;
   uint16_t* tables;
@@ -1036,13 +1038,13 @@ __global__ void __launch_bounds__(kThreads, 8) count_finish_kernel(SampleArgs a)
   put(a, r, id, logp);
 }
 
-// The general path; of bf16 rows those that count_kernel left.
+// The general path: every row (direct), or those that the counting kernels left.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
-  if (sizeof(T) == 2 && a.ids[r] != kLeft) return;
+  if (!a.direct && a.ids[r] != kLeft) return;
   const Row<T> row((const T*)a.x + r * a.ld, a.V);
 
   const Settings how = row_settings(a, r);
@@ -1066,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   sc.set(mx, how.T, a.fix_bits);
 
   // 2a. few tokens: those that reach the k-th largest of the threads' maxima
-  if (sizeof(T) == 4 && k <= (uint32_t)kFastK) {
+  if (a.direct && k <= (uint32_t)kFastK) {
     uint32_t* hist = (uint32_t*)sh.mass;
     constexpr int kHist = 1 << kTopBits, kShift = Key<T>::kBits - kTopBits, kPer = kHist / kThreads;
     for (int i = tid; i < kHist; i += kThreads) hist[i] = 0;
@@ -1206,6 +1208,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 
 }  // namespace
 
+// Whether bf16 rows go to the general path at once.
+namespace {
+bool direct_bf16(int64_t V, const SampleParams& p) {
+  const bool few = !p.top_ks && !p.temperatures && ((p.top_k > 0 && p.top_k <= kFastK) || p.temperature == 0.0);
+  return V <= 4096 || few;
+}
+}  // namespace
+
 // Workgroups per bf16 row: more than one for few rows (less than a quarter of
 // the 256 compute units busy) of at least 2 x 16,384 logits.  One 201,088-logit
 // row takes 33 us by one workgroup.
@@ -1236,7 +1246,8 @@ hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t 
   a.fix_bits = 62 - lg < 51 ? 62 - lg : 51;  // V masses of at most 2^fix_bits stay below 2^63
   a.ids = ids;
   a.logp = logp;
-  if (dt == DT_BF16) {
+  a.direct = dt != DT_BF16 || direct_bf16(V, p);
+  if (!a.direct) {
     a.slices = ws != nullptr ? slices_of(dt, N, V) : 1;
     hipError_t e;
     if (a.slices > 1) {
@@ -1250,8 +1261,10 @@ hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t 
       hipLaunchKernelGGL(count_kernel, dim3((unsigned)N), dim3(kThreads), 0, s, a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (dt == DT_BF16)
     hipLaunchKernelGGL(sample_kernel<__bf16>, dim3((unsigned)N), dim3(kThreads), 0, s, a);
-  } else
+  else
     hipLaunchKernelGGL(sample_kernel<float>, dim3((unsigned)N), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
