@@ -13,12 +13,19 @@
 // about 1e-14 of the total: exponentials in fp64, sums in 64-bit integers (in
 // any order the same) and fp64.
 //
-// One workgroup per row, bound by reading the row:
-//  1. the largest logit of the row, with each thread's chunk maxima kept;
-//  2a. 1 <= k <= 512: the k-th largest of the threads' maxima is a bound that
-//     at least k tokens reach; only the chunks that reach it are read again,
-//     the tokens found are sorted in LDS and everything else happens there;
-//  2b. otherwise a histogram of the row's mass over 4096 bins, 1/64 octave of
+// The floor is reading a row once.  One workgroup of 1024 threads takes a row:
+//  1. bf16 rows (count_kernel): a count of every value, one LDS add per logit,
+//     from which all borders follow; then the row is read again from its start
+//     up to the drawn token, which is the n-th logit of its value.  N <= 64
+//     rows of 32,768 logits and more are counted by several workgroups each
+//     (count_slice_kernel, count_finish_kernel).
+//  2. The general path (sample_kernel): fp32 rows, bf16 rows that counting
+//     leaves (logits beyond +-256 that matter, and the like), and bf16 rows of
+//     which few tokens are wanted (direct_bf16).  First the largest logit, then
+//   a. 1 <= k <= 512: the k-th largest of the threads' maxima is a bound that
+//     at least k tokens reach; the tokens that do are collected, sorted in LDS,
+//     and everything else happens there;
+//   b. otherwise a histogram of the row's mass over 4096 bins, 1/64 octave of
 //     e each (64 octaves: what lies below weighs less than 2^-64 a token).
 //     Within a bin the masses e / (upper edge) lie in (2^-1/64, 1], so a short
 //     polynomial gives them and 64-bit integers sum them with one relative
@@ -27,6 +34,17 @@
 //     there is narrowed by 8 bits of the key at a time first, and where only
 //     equal logits are left the border is a count, and the token is found by
 //     its rank in id order.
+//
+// Measured (MI355X):
+//  1,024 x 201,088 bf16, no limit: 149 us, 2.8 TB/s of the logits.  Counting is
+//    bound by the LDS (an add per logit: 117 us without the second read, against
+//    75 us for the bytes); by the histogram of 2b the same took 890 us.
+//  512 x 128,256 bf16, top-p: 59 us, 2.2 TB/s (two rounds of workgroups).
+//  64 x 32,000 bf16, top-k 50: 13 us by 2a (20 us by counting); fp32 top-p 29 us.
+//  1 x 201,088 bf16, top-k 50: 22 us by 2a, 28 us by counting in slices, 33 us
+//    by one counting workgroup: latency, a row is read by few compute units.
+//  1,024 x 201,088 fp32, no limit: 459 us, 1.8 TB/s, bound by the 64-bit LDS
+//    adds of 2b and the fp64 polynomial.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -459,7 +477,8 @@ __device__ inline bool may_equal(const u32x4_t& v, float l, __bf16*) {
 // wave alike goes through the group that holds the r-th.  cnt: kGroups words of LDS, pick: two.
 constexpr int kGroups = 2 * kThreads;
 template <typename T>
-__device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l, uint32_t r) {
+__device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l,
+                                             uint32_t r) {
   constexpr int U = kFlight;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   // the r-th set bit of a mask of lanes
@@ -576,8 +595,8 @@ struct Found {
 
 // before, cbefore: mass and (for BY_COUNT) tokens of the bins of earlier threads.
 template <typename T>
-__device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int kind, uint32_t k, double target,
-                             double before, uint32_t cbefore, bool want_id) {
+__device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, const Scale& sc, int kind, uint32_t k,
+                                             double target, double before, uint32_t cbefore, bool want_id) {
   const int tid = threadIdx.x;
   // 1. the bin: thread t holds the bins [kPerThread t, kPerThread (t + 1))
   const double* mass = (const double*)sh.mass;
@@ -635,16 +654,16 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
     if (tid == 0) sh.n_cand = 0;
     __syncthreads();
     sc.either([&](auto plain) {
-    for_each(row, [&](float l, int64_t id) {
-      const float place = sc.template place<plain.value>(l);
-      if (place >= p0 && place < p1) {
-        const uint32_t key = Key<T>::of(l);
-        if ((key & prefix_mask) == prefix) {
-          const uint32_t slot = atomicAdd(&sh.n_cand, 1u);
-          if (slot < (uint32_t)kCap) sh.cand[slot] = pack(key, (uint32_t)id);
+      for_each(row, [&](float l, int64_t id) {
+        const float place = sc.template place<plain.value>(l);
+        if (place >= p0 && place < p1) {
+          const uint32_t key = Key<T>::of(l);
+          if ((key & prefix_mask) == prefix) {
+            const uint32_t slot = atomicAdd(&sh.n_cand, 1u);
+            if (slot < (uint32_t)kCap) sh.cand[slot] = pack(key, (uint32_t)id);
+          }
         }
-      }
-    });
+      });
     });
     __syncthreads();
     const uint32_t n = sh.n_cand;
@@ -665,18 +684,18 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
     }
     __syncthreads();
     sc.either([&](auto plain) {
-    for_each(row, [&](float l, int64_t) {
-      const float place = sc.template place<plain.value>(l);
-      if (place >= p0 && place < p1) {
-        const uint32_t key = Key<T>::of(l);
-        if ((key & prefix_mask) == prefix) {
-          const uint32_t dg = 255u - ((key >> digits_left) & 255u);
-          atomicAdd((unsigned long long*)&sh.sub_mass[dg],
-                    (unsigned long long)(pow_frac(sc.template frac<plain.value>(l, bin)) * sc.fix + 0.5));
-          atomicAdd(&sh.sub_count[dg], 1u);
+      for_each(row, [&](float l, int64_t) {
+        const float place = sc.template place<plain.value>(l);
+        if (place >= p0 && place < p1) {
+          const uint32_t key = Key<T>::of(l);
+          if ((key & prefix_mask) == prefix) {
+            const uint32_t dg = 255u - ((key >> digits_left) & 255u);
+            atomicAdd((unsigned long long*)&sh.sub_mass[dg],
+                      (unsigned long long)(pow_frac(sc.template frac<plain.value>(l, bin)) * sc.fix + 0.5));
+            atomicAdd(&sh.sub_count[dg], 1u);
+          }
         }
-      }
-    });
+      });
     });
     __syncthreads();
     const double dm = tid < kSub && sh.sub_count[tid] ? (double)sh.sub_mass[tid] * sc.inv_fix * top : 0.0;
@@ -807,8 +826,8 @@ struct Settings {
 // From the counts in sh.cnt: the logit of the drawn token, which of the equal
 // ones it is (r >= 1; 0: nothing to draw), and its log-probability.  False:
 // the row is one for the general path.
-__device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Settings& how, float* logit, uint32_t* nth,
-                             double* logp) {
+__device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Settings& how,
+                                             float* logit, uint32_t* nth, double* logp) {
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int kPer = Counted::kPer;
   if (sh.cnt[Counted::kW + 1] != 0) return false;  // 256 and more, +inf or NaN
@@ -1151,19 +1170,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   const double y_min = min_p > 0.0 ? -64.0 * log2(min_p) : (double)INFINITY;
   const int bin_min = y_min < (double)kBins ? (int)y_min : 2 * kBins;
   sc.either([&](auto plain) {
-  for_each(row, [&](float l, int64_t) {
-    const float place = sc.template place<plain.value>(l);
-    if (place < (float)kBins) {
-      const int bin = (int)place;
-      // round to an integer by adding 2^52: the low bits of the sum are it
-      const double q = __builtin_fma(pow_frac(sc.template frac<plain.value>(l, bin)), sc.fix, 0x1p52);
-      const unsigned long long qi = (unsigned long long)__builtin_bit_cast(uint64_t, q) & 0xFFFFFFFFFFFFFull;
-      atomicAdd((unsigned long long*)&sh.mass[bin], qi);
-      if (limit) atomicAdd(&sh.count[bin], 1u);
-      const uint32_t near = (uint32_t)(bin - bin_min + 1);
-      if (near < 3u && sc.y(l) <= y_min) atomicAdd((unsigned long long*)&sh.edge_mass[near], qi);
-    }
-  });
+    for_each(row, [&](float l, int64_t) {
+      const float place = sc.template place<plain.value>(l);
+      if (place < (float)kBins) {
+        const int bin = (int)place;
+        // round to an integer by adding 2^52: the low bits of the sum are it
+        const double q = __builtin_fma(pow_frac(sc.template frac<plain.value>(l, bin)), sc.fix, 0x1p52);
+        const unsigned long long qi = (unsigned long long)__builtin_bit_cast(uint64_t, q) & 0xFFFFFFFFFFFFFull;
+        atomicAdd((unsigned long long*)&sh.mass[bin], qi);
+        if (limit) atomicAdd(&sh.count[bin], 1u);
+        const uint32_t near = (uint32_t)(bin - bin_min + 1);
+        if (near < 3u && sc.y(l) <= y_min) atomicAdd((unsigned long long*)&sh.edge_mass[near], qi);
+      }
+    });
   });
   __syncthreads();
   // masses of the bins, of the whole row and of the tokens that reach min_p
@@ -1208,18 +1227,21 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 
 }  // namespace
 
-// Whether bf16 rows go to the general path at once.
 namespace {
+// Whether bf16 rows go to the general path at once.  Counting clears and scans
+// about 8,700 counts a row, which short rows do not repay, and where every row
+// takes at most kFastK tokens the collected path reads the row at least as
+// fast: with k = 50 a row of 201,088 logits 22 us against 28, 64 x 32,000 13
+// against 20 (1,024 x 201,088: 157 against 147, the price of a simple rule).
+// A limit of each row's own cannot be read here.
 bool direct_bf16(int64_t V, const SampleParams& p) {
   const bool few = !p.top_ks && !p.temperatures && ((p.top_k > 0 && p.top_k <= kFastK) || p.temperature == 0.0);
   return V <= 4096 || few;
 }
-}  // namespace
 
-// Workgroups per bf16 row: more than one for few rows (less than a quarter of
-// the 256 compute units busy) of at least 2 x 16,384 logits.  One 201,088-logit
-// row takes 33 us by one workgroup.
-namespace {
+// Workgroups per bf16 row: more than one for few rows (at most a quarter of
+// the 256 compute units busy) of at least 2 x 16,384 logits.  One row of
+// 201,088 logits takes 28 us so, 33 us by one workgroup.
 int slices_of(Dtype dt, int64_t N, int64_t V) {
   if (dt != DT_BF16 || N > 64) return 1;
   int64_t s = V / 16384;
