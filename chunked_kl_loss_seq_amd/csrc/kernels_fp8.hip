@@ -288,13 +288,8 @@ __global__ void __launch_bounds__(kFewWaves * 64) fp8_few_kernel(Fp8Args p) {
 // BM ids x BN tokens, WM x (BN / 64) waves of (BM / WM) x 64.  The ring's stage
 // holds the tile's 128-byte rows of both operands (16-byte chunks XOR-swizzled
 // by the row) and the BN token scales of the block.
-// Lane l's 16 (or 4) bytes at byte voff + soff of the resource go to LDS byte
-// lds_addr + 16 l (4 l); see dma16 for why these are written out.
-__device__ inline void dma16_at(const i32x4& rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
-               "s"(soff), "s"(lds_addr)
-               : "memory", "m0");
-}
+// Lane l's 4 bytes at byte voff of the resource go to LDS byte lds_addr + 4 l;
+// see dma16 for why this is written out.
 __device__ inline void dma4(const i32x4& rsrc, uint32_t voff, uint32_t lds_addr) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc),
                "s"(lds_addr)
@@ -304,9 +299,10 @@ __device__ inline void dma4(const i32x4& rsrc, uint32_t voff, uint32_t lds_addr)
 // Copies R rows x 128 bytes (one block of k) of an operand into LDS, laid out
 // as KTile.  One instruction of a wave fills 8 rows; a wave's next one lies
 // NW x 8 rows on, a multiple of the swizzle's period, so one lane offset serves
-// all and the rows' distance goes into the scalar offset.  Rows past the
-// operand lie past the resource's end, k past d only on the last block: both
-// read as zeros.
+// all and the rows' distance is added to it (not put into the instruction's
+// scalar offset, which the range check need not cover).  Rows past the operand
+// lie past the resource's end, k past d only on the last block: both read as
+// zeros.
 template <int R, int NW>
 struct BlockDMA {
   static constexpr int kBytes = R * kBlk;
@@ -332,7 +328,7 @@ struct BlockDMA {
     uint32_t v = voff;
     if (d - k0 < kBlk && chunk(wave, lane) * 16 >= (int)(d - k0)) v = kOOB;
 #pragma unroll
-    for (int i = 0; i < kNI; ++i) dma16_at(rs, v, (uint32_t)i * step, lds + (uint32_t)((i * NW + wave) * 1024));
+    for (int i = 0; i < kNI; ++i) dma16(rs, v + (uint32_t)i * step, lds + (uint32_t)((i * NW + wave) * 1024));
   }
 };
 
