@@ -513,6 +513,8 @@ int run_impl(Pass pass, Dtype dt, const void* H, const void* W, const int32_t* i
 inline bool dtype_ok(int dtype) { return dtype == CKL_DTYPE_BF16 || dtype == CKL_DTYPE_F32; }
 // Workgroups of 256 threads in one launch dimension, at most (exclusive).
 constexpr int64_t kMaxBlocks256 = (int64_t)1 << 24;
+// Rows of a sampling call, at most (exclusive): a workgroup of 1024 threads each.
+constexpr int64_t kMaxSampleRows = (int64_t)1 << 22;
 
 int embed_shape(int64_t N, int64_t d, int64_t V) {
   if (N < 0 || d <= 0 || V <= 0) return CKL_EINVAL;
@@ -664,7 +666,7 @@ int ckl_embed_bwd(int dtype, const int32_t* ids, const void* dY, float scale, in
 
 int ckl_sample_workspace(int dtype, int64_t N, int64_t V, uint64_t* bytes_out) {
   if (!dtype_ok(dtype) || !bytes_out || N < 0 || V <= 0) return CKL_EINVAL;
-  if (V > (int64_t)1 << 26 || N >= (int64_t)1 << 23) return CKL_EUNSUPPORTED;
+  if (V > (int64_t)1 << 26 || N >= kMaxSampleRows) return CKL_EUNSUPPORTED;
   *bytes_out = N > 0 ? sample_workspace(to_dt(dtype), N, V) : 0;
   return CKL_OK;
 }
@@ -686,7 +688,7 @@ int ckl_sample(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_
     if (!aligned(p.temperatures, 4) || !aligned(p.top_ks, 4) || !aligned(p.top_ps, 4) || !aligned(p.min_ps, 4))
       return CKL_EINVAL;
   }
-  if (V > (int64_t)1 << 26 || N >= (int64_t)1 << 23) return CKL_EUNSUPPORTED;
+  if (V > (int64_t)1 << 26 || N >= kMaxSampleRows) return CKL_EUNSUPPORTED;
   if (N == 0) return CKL_OK;
   if (!logits || !u || !ids_out) return CKL_EINVAL;
   if (!aligned(logits, dtype == CKL_DTYPE_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(ids_out, 4) ||

@@ -260,7 +260,7 @@ typedef struct ckl_sampling {
  *   logp_out  fp32 [N] or NULL: log(e / S) of the drawn token (-inf for -1)
  * Masses and borders are computed in 64 bits, so the token is that of the
  * formulas except where a border is within about 1e-13 of the total; tokens
- * whose e is below 2^-64 count as 0.  V <= 2^26, N < 2^23.
+ * whose e is below 2^-64 count as 0.  V <= 2^26, N < 2^22.
  *   workspace NULL, or a device buffer of at least ckl_sample_workspace bytes
  *             (0 for most shapes), 256-byte aligned, not shared by calls that
  *             may overlap: with it, long rows of a small batch are split over

@@ -85,6 +85,14 @@ def test_sample(bad, want):
     assert sample(**bad) == want
 
 
+def test_sample_rows_fit_one_launch():
+    # a workgroup of 1,024 threads per row, fewer than 2^32 threads a launch
+    b = ctypes.c_uint64(0)
+    assert sample(N=1 << 22) == EUNSUPPORTED
+    assert B.lib().ckl_sample_workspace(0, 1 << 22, 10, ctypes.byref(b)) == EUNSUPPORTED
+    assert B.lib().ckl_sample_workspace(0, (1 << 22) - 1, 10, ctypes.byref(b)) == OK
+
+
 def test_sample_workspace():
     b = ctypes.c_uint64(7)
     f = B.lib().ckl_sample_workspace
