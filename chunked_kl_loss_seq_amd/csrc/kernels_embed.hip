@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* _
   if (slice >= a.slices) return;
   const int c = slice * 64 + lane;
   const bool on = c < a.cpr;
+  const int cl = on ? c : a.cpr - 1;
   const int64_t b = t * a.tlen, e = b + a.tlen < a.N ? b + a.tlen : a.N;
   const uint32_t before = b > 0 ? a.skey[b - 1] : 0xFFFFFFFFu;
   const uint32_t after = e < a.N ? a.skey[e] : 0xFFFFFFFFu;
@@ -433,7 +434,10 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* _
     else
       store_row<kN>(a.dW + (int64_t)cur * a.d + (int64_t)c * kN, acc, a.scale, a.accumulate != 0);
   };
-  constexpr int U = 8;  // rows in flight
+  // Rows in flight, loaded without conditions (lanes past the row take its last
+  // chunk, positions without a token their own row, and neither is used): under
+  // conditions each load waited, 4,096 x 2,048 of 32,000 70 us instead of 60.
+  constexpr int U = 8;
   for (int64_t i0 = b; i0 < e; i0 += U) {
     u32x4_t v[U];
     uint32_t k[U];
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* _
       const int64_t i = i0 + j < e ? i0 + j : e - 1;
       k[j] = __builtin_amdgcn_readfirstlane(a.skey[i]);
       const uint32_t p = __builtin_amdgcn_readfirstlane(a.spos[i]);
-      if (on && k[j] < a.V) v[j] = src[(int64_t)p * a.cpr + c];
+      v[j] = src[(int64_t)p * a.cpr + cl];
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
