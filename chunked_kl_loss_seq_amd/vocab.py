@@ -104,6 +104,14 @@ def embed_bwd(ids, dY, V, scale=1.0, dW=None, accumulate=False):
     return dW
 
 
+def _not_capturing(torch, step):
+    """autograd accumulates a leaf's gradient on the stream where its accumulator was
+    made, which an eager graph of the same leaf may have left outside the capture:
+    that would end the process, so it is refused first."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"embedding's {step} cannot be captured with a gradient: capture embed and embed_bwd")
+
+
 class _Embedding:
     """torch.autograd.Function wrapper, created lazily so importing needs no torch."""
 
@@ -125,6 +133,7 @@ class _Embedding:
                 @staticmethod
                 @torch.autograd.function.once_differentiable
                 def backward(ctx, g):
+                    _not_capturing(torch, "backward")
                     (ids,) = ctx.saved_tensors
                     dW = embed_bwd(ids, g.contiguous(), ctx.V, ctx.scale)
                     return None, dW.to(ctx.w_dtype), None
@@ -134,7 +143,15 @@ class _Embedding:
 
 
 def embedding(ids, W, scale=1.0):
-    """``embed`` as a differentiable torch function of W (gradient: ``embed_bwd``)."""
+    """``embed`` as a differentiable torch function of W (gradient: ``embed_bwd``).
+
+    A stream capture takes it only where no gradient is asked for; a captured
+    training step calls ``embed`` and ``embed_bwd``.
+    """
+    import torch
+
+    if W.requires_grad and torch.is_grad_enabled():
+        _not_capturing(torch, "forward")
     return _Embedding.get().apply(ids, W, float(scale))
 
 
@@ -269,7 +286,8 @@ def teacher_topk(H, wq, ws, K, chunk=0):
     int32 [N, K], values float32 [N, K]) as ``topk`` of their bfloat16 logits.
 
     Positions go in chunks (``chunk`` rows; 0: about 1 GiB of logits), so the
-    N x V logits are never held at once.
+    N x V logits are never held at once.  As for ``topk``, NaN logits (a hidden
+    row that is not finite) are outside its inputs.
     """
     import torch
 
@@ -284,8 +302,9 @@ def teacher_topk(H, wq, ws, K, chunk=0):
     ids = torch.empty((N, K), dtype=torch.int32, device=dev)
     vals = torch.empty((N, K), dtype=torch.float32, device=dev)
     logits = torch.empty((min(chunk, N), V), dtype=torch.bfloat16, device=dev)
-    for r in range(0, N, chunk):
-        n = min(chunk, N - r)
-        logits_fp8(H[r:r + n], wq, ws, out=logits[:n])
-        topk(logits[:n], K, ids_out=ids[r:r + n], vals_out=vals[r:r + n])
+    with _on(torch, dev):
+        for r in range(0, N, chunk):
+            n = min(chunk, N - r)
+            logits_fp8(H[r:r + n], wq, ws, out=logits[:n])
+            topk(logits[:n], K, ids_out=ids[r:r + n], vals_out=vals[r:r + n])
     return ids, vals

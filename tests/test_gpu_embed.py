@@ -248,6 +248,35 @@ def test_captured_and_replayed(ckl):
             assert torch.equal(out, ckl.embed(ids, W, 2.0)) and torch.equal(dW, ckl.embed_bwd(ids, dY, 3000, 2.0))
 
 
+def test_embedding_under_capture(ckl, monkeypatch):
+    # an eager graph of the same leaf may live: a captured call that needs its
+    # gradient is refused before anything is recorded; without one it replays
+    rng = np.random.default_rng(8)
+    ids = dev(tokens(rng, 50, 100, "uniform"))
+    W = dev(rng.standard_normal((100, 16)).astype(np.float32)).requires_grad_(True)
+    eager = ckl.embedding(ids, W, 2.0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with torch.no_grad():
+            out = ckl.embedding(ids, W, 2.0)
+        with pytest.raises(RuntimeError, match="capture embed and embed_bwd"):
+            ckl.embedding(ids, W)
+    for _ in range(3):
+        ids.copy_(torch.roll(ids, 3))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ckl.embed(ids, W.detach(), 2.0))
+    # the backward's own check (reported as capturing, nothing is captured)
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="capture embed and embed_bwd"):
+            eager.sum().backward()
+    assert W.grad is None
+    ckl.embedding(ids, W, 2.0).sum().backward()
+    assert torch.equal(W.grad, ckl.embed_bwd(ids, torch.ones(50, 16, device="cuda:0"), 100, 2.0))
+
+
 def test_refusals(ckl):
     W = torch.zeros(10, 16, device="cuda:0")
     ids = torch.zeros(4, dtype=torch.int32, device="cuda:0")
