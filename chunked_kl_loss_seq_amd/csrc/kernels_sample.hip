@@ -248,11 +248,18 @@ __device__ inline void fill_pow64(Red& red) {
   if (threadIdx.x < 64) red.pow64[threadIdx.x] = exp2(-(double)threadIdx.x / 64.0);
 }
 __device__ inline double bin_top(const Red& red, int b) { return ldexp(red.pow64[b & 63], -(b >> 6)); }
-// e of a logit whose y is below kBins, else 0
+// e of a logit whose y is below kBins, else 0; here 2^(-f / 64) is its Taylor
+// polynomial of degree 6 (off by 4e-18), as a product of such values follows
 __device__ inline double mass_of(const Red& red, double y) {
   if (!(y < (double)kBins)) return 0.0;
-  const double b = floor(y);
-  return bin_top(red, (int)b) * pow_frac(y - b);
+  const double b = floor(y), f = (y - b) * -0.01083042469624914;  // ln 2 / 64
+  double r = 1.0 / 720;
+  r = __builtin_fma(r, f, 1.0 / 120);
+  r = __builtin_fma(r, f, 1.0 / 24);
+  r = __builtin_fma(r, f, 1.0 / 6);
+  r = __builtin_fma(r, f, 0.5);
+  r = __builtin_fma(r, f, 1.0);
+  return bin_top(red, (int)b) * __builtin_fma(r, f, 1.0);
 }
 
 struct Shared {
@@ -471,14 +478,15 @@ __device__ inline bool may_equal(const u32x4_t& v, float l, __bf16*) {
   return z[0] == 0 || z[1] == 0;
 }
 
-// The id of the r-th token (r >= 1) of logit l in id order, in every thread.
-// A wave reads 64 chunks at once; the equal logits of every such piece (or
-// group of pieces, in long rows) are counted until r are passed, then every
-// wave alike goes through the group that holds the r-th.  cnt: kGroups words of LDS, pick: two.
+// The id of the r-th token (1 <= r <= n) of the n of logit l in id order, in
+// every thread.  A wave reads 64 chunks at once; the equal logits of every such
+// piece (or group of pieces, in long rows) are counted from the row's nearer
+// end (by r among n) until the r-th is passed, then every wave alike goes
+// through the group that holds it.  cnt: kGroups words of LDS, pick: two.
 constexpr int kGroups = 2 * kThreads;
 template <typename T>
 __device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l,
-                                             uint32_t r) {
+                                             uint32_t r, uint32_t n) {
   constexpr int U = kFlight;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   // the r-th set bit of a mask of lanes
@@ -486,87 +494,88 @@ __device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, R
     for (; n > 1; --n) m &= m - 1;
     return __builtin_ctzll(m);
   };
-  {
-    const uint64_t m = __ballot(lane < row.head && (float)row.x[lane < row.head ? lane : 0] == l);
-    const uint32_t n = (uint32_t)__popcll(m);
-    if (r <= n) return nth_lane(m, r);
-    r -= n;
-  }
-  if (row.nb > 0) {
-    const uint32_t pieces = (row.nb + 63) / 64;
-    int shift = 0;
-    while (((pieces - 1) >> shift) >= (uint32_t)kGroups) ++shift;
-    const uint32_t groups = ((pieces - 1) >> shift) + 1;
-    __syncthreads();
-    for (uint32_t g = groups + tid; g < (uint32_t)kGroups; g += kThreads) cnt[g] = 0;  // the last round's rest
-    if (tid == 0) pick[0] = 0;
-    // rounds of U groups a wave, in order: after each, stop if the r-th is past
-    uint32_t done = 0;
-    while (done < groups) {
-      const uint32_t g0 = done + w;
-      uint32_t n[U];
+  const uint64_t head = __ballot(lane < row.head && (float)row.x[lane < row.head ? lane : 0] == l);
+  const uint64_t tail = __ballot(lane < row.tail && (float)row.x[lane < row.tail ? row.tail_id() + lane : 0] == l);
+  const uint32_t nh = (uint32_t)__popcll(head), in_body = n - nh - (uint32_t)__popcll(tail);
+  if (r <= nh) return nth_lane(head, r);
+  r -= nh;
+  if (r > in_body) return row.tail_id() + nth_lane(tail, r - in_body);
+  if (row.nb == 0) return -1;
+  const uint32_t pieces = (row.nb + 63) / 64;
+  int shift = 0;
+  while (((pieces - 1) >> shift) >= (uint32_t)kGroups) ++shift;
+  const uint32_t groups = ((pieces - 1) >> shift) + 1;
+  const bool back = r > in_body - r + 1;  // groups in falling order: the r-th is the (in_body - r + 1)-th
+  if (back) r = in_body - r + 1;
+  __syncthreads();
+  for (uint32_t g = groups + tid; g < (uint32_t)kGroups; g += kThreads) cnt[g] = 0;  // the last round's rest
+  if (tid == 0) pick[0] = 0;
+  // rounds of U groups a wave, in order: after each, stop if the r-th is past
+  uint32_t done = 0;
+  while (done < groups) {
+    const uint32_t o0 = done + w;
+    uint32_t found[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) n[j] = 0;
-      for (uint32_t s = 0; s < (1u << shift); ++s) {
-        u32x4_t v[U];
-        uint32_t c[U];
+    for (int j = 0; j < U; ++j) found[j] = 0;
+    for (uint32_t s = 0; s < (1u << shift); ++s) {
+      u32x4_t v[U];
+      uint32_t c[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          c[j] = (((g0 + j * kWaves) << shift) + s) * 64 + lane;
-          v[j] = row.body[c[j] < row.nb ? c[j] : row.nb - 1];
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const bool may = c[j] < row.nb && may_equal(v[j], l, (T*)nullptr);
-          if (__ballot(may) == 0) continue;
-          const uint32_t m = may ? equal_in(v[j], l, (T*)nullptr) : 0;
-#pragma unroll
-          for (int i = 0; i < Row<T>::kN; ++i) n[j] += (uint32_t)__popcll(__ballot((m >> i) & 1u));
-        }
+      for (int j = 0; j < U; ++j) {
+        const uint32_t o = o0 + j * kWaves;
+        const uint32_t g = o >= groups ? groups : back ? groups - 1 - o : o;
+        c[j] = ((g << shift) + s) * 64 + lane;
+        v[j] = row.body[c[j] < row.nb ? c[j] : row.nb - 1];
       }
 #pragma unroll
-      for (int j = 0; j < U; ++j)
-        if (lane == 0 && g0 + j * kWaves < groups) cnt[g0 + j * kWaves] = n[j];
-      uint32_t sum = 0;
+      for (int j = 0; j < U; ++j) {
+        const bool may = c[j] < row.nb && may_equal(v[j], l, (T*)nullptr);
+        if (__ballot(may) == 0) continue;
+        const uint32_t m = may ? equal_in(v[j], l, (T*)nullptr) : 0;
 #pragma unroll
-      for (int j = 0; j < U; ++j) sum += n[j];
-      __syncthreads();  // pick[0] is clear (first round), or read by all (later ones)
-      if (lane == 0 && sum) atomicAdd(&pick[0], sum);
-      __syncthreads();
-      done += U * kWaves;
-      if (pick[0] >= r) break;
-    }
-    // groups not reached count as empty
-    const uint32_t a = 2 * tid < done ? cnt[2 * tid] : 0, b = 2 * tid + 1 < done ? cnt[2 * tid + 1] : 0;
-    uint32_t before = 0;
-    const uint32_t total = block_prefix(a + b, red, &before);
-    if (before < r && before + a + b >= r) {
-      const bool second = before + a < r;
-      pick[0] = 2 * tid + (second ? 1 : 0);
-      pick[1] = before + (second ? a : 0);
-    }
-    __syncthreads();
-    if (r <= total) {
-      const uint32_t g = pick[0];
-      uint32_t seen = pick[1];
-      for (uint32_t s = 0; s < (1u << shift); ++s) {
-        const uint32_t c = ((g << shift) + s) * 64 + lane;
-        uint32_t m = equal_in(row.body[c < row.nb ? c : row.nb - 1], l, (T*)nullptr);
-        if (c >= row.nb) m = 0;
-        const uint32_t mine = (uint32_t)__popc(m), upto = seen + wave_scan(mine);
-        const uint64_t here = __ballot(upto - mine < r && upto >= r);
-        if (here) {
-          for (uint32_t skip = r - 1 - (upto - mine); skip > 0 && m; --skip) m &= m - 1;
-          const int at = __builtin_ctzll(here);
-          return row.body_id(__shfl(c, at)) + __shfl(m ? __builtin_ctz(m) : 0, at);
-        }
-        seen = __shfl(upto, 63);
+        for (int i = 0; i < Row<T>::kN; ++i) found[j] += (uint32_t)__popcll(__ballot((m >> i) & 1u));
       }
     }
-    r -= total;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (lane == 0 && o0 + j * kWaves < groups) cnt[o0 + j * kWaves] = found[j];
+    uint32_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < U; ++j) sum += found[j];
+    __syncthreads();  // pick[0] is clear (first round), or read by all (later ones)
+    if (lane == 0 && sum) atomicAdd(&pick[0], sum);
+    __syncthreads();
+    done += U * kWaves;
+    if (pick[0] >= r) break;
   }
-  const uint64_t m = __ballot(lane < row.tail && (float)row.x[lane < row.tail ? row.tail_id() + lane : 0] == l);
-  return row.tail_id() + nth_lane(m, r);
+  // groups not reached count as empty
+  const uint32_t a = 2 * tid < done ? cnt[2 * tid] : 0, b = 2 * tid + 1 < done ? cnt[2 * tid + 1] : 0;
+  uint32_t before = 0;
+  block_prefix(a + b, red, &before);
+  if (before < r && before + a + b >= r) {
+    const bool second = before + a < r;
+    const uint32_t o = 2 * tid + (second ? 1 : 0), in = r - before - (second ? a : 0);
+    pick[0] = back ? groups - 1 - o : o;
+    pick[1] = back ? (second ? b : a) - in + 1 : in;
+  }
+  __syncthreads();
+  const uint32_t g = pick[0];
+  r = pick[1];
+  uint32_t seen = 0;
+  for (uint32_t s = 0; s < (1u << shift); ++s) {
+    const uint32_t c = ((g << shift) + s) * 64 + lane;
+    uint32_t m = equal_in(row.body[c < row.nb ? c : row.nb - 1], l, (T*)nullptr);
+    if (c >= row.nb) m = 0;
+    const uint32_t mine = (uint32_t)__popc(m), upto = seen + wave_scan(mine);
+    const uint64_t here = __ballot(upto - mine < r && upto >= r);
+    if (here) {
+      for (uint32_t skip = r - 1 - (upto - mine); skip > 0 && m; --skip) m &= m - 1;
+      const int at = __builtin_ctzll(here);
+      return row.body_id(__shfl(c, at)) + __shfl(m ? __builtin_ctz(m) : 0, at);
+    }
+    seen = __shfl(upto, 63);
+  }
+  return -1;  // not reached: the row holds n such logits
 }
 
 // The smallest r in [1, n] for which above + r e reaches the target, n if none:
@@ -575,6 +584,13 @@ __device__ inline uint32_t equal_taken(int kind, uint32_t n, uint32_t above_n, d
                                        double target) {
   if (kind == BY_COUNT) return k > above_n ? (k - above_n < n ? k - above_n : n) : 1;
   uint32_t lo = 1, hi = n;
+  // the quotient, where the sums' rounding leaves it within one, spares most steps
+  const double g = (target - above) / e;
+  if (g > 2.0 && g < (double)n - 2.0) {
+    const uint32_t a = (uint32_t)g - 1;
+    if (!reached(kind, 0, above + (double)a * e, 0, target)) lo = a + 1;
+    if (reached(kind, 0, above + (double)(a + 3) * e, 0, target)) hi = a + 3;
+  }
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo) / 2;
     if (reached(kind, 0, above + (double)mid * e, 0, target))
@@ -732,7 +748,7 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
   const uint32_t r = equal_taken(kind, n, above_n, above, e, k, target);
   Found f{above + (double)r * e, l, -1};
   if (!want_id) return f;
-  f.id = nth_equal(row, (uint32_t*)sh.cand, sh.red, sh.nth, l, r);
+  f.id = nth_equal(row, (uint32_t*)sh.cand, sh.red, sh.nth, l, r, n);
   return f;
 }
 
@@ -740,48 +756,87 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
 // bf16 logits have few distinct values, so a row is its count of every value:
 // one pass with a 32-bit LDS add per logit, no exponential and no maximum
 // before it, and each border is exact from count x e of the values in order.
-// Counted one by one are the magnitudes in [2^-26, 2^8) of either sign; 0 and
+// Counted one by one are the magnitudes in [2^-24, 2^8) of either sign; 0 and
 // smaller ones are one count, larger ones another, so that a logit's place is
 // eight packed 16-bit operations for two logits, without a branch.  Where
-// logits beyond +-256 matter, or nonzero ones below 2^-26 do (by 1e-13 of the
+// logits beyond +-256 matter, or nonzero ones below 2^-24 do (by 1e-13 of the
 // mass, or because a border falls among them), the row is left to the general
 // path (id kLeft).
+//
+// The counting itself keeps up with the memory (1,024 rows of 201,088: 80 us,
+// 5.2 TB/s; without the LDS adds 77), so what follows it is kept short: a
+// thread takes 8 adjacent values of one octave, equally spaced, whose e are a
+// geometric series (two exponentials for eight), and one wave alone looks into
+// the thread that a border falls to.
 constexpr int32_t kLeft = -2;
 struct Counted {
-  static constexpr int kLo = (127 - 26) << 7, kHi = (127 + 8) << 7;  // magnitude bits
+  static constexpr int kLo = (127 - 24) << 7, kHi = (127 + 8) << 7;  // magnitude bits
   static constexpr int kW = kHi - kLo;
-  // counts of one sign: 0 = below 2^-26, 1 + (bits - kLo), kW + 1 = from 2^8 on
+  static constexpr int kPer = 8;  // values of a thread: the positive ones from the largest down, then the negative ones
+  static_assert(2 * kW == kPer * kThreads && 128 % kPer == 0, "a thread's values lie in one octave");
+  // counts of one sign: 0 = below 2^-24, 1 + (bits - kLo), kW + 1 = from 2^8 on
   // (also infinities and NaN); the negative ones follow the positive ones
-  static constexpr int kSign = kW + 2;
+  static constexpr int kSign = kW + 4;
   static constexpr int kCounts = 2 * kSign;
-  // slots in the order of the logits: positive values, 0, negative values
-  static constexpr int kZero = kW;
-  static constexpr int kSlots = 2 * kW + 1;
-  static constexpr int kPer = (kSlots + kThreads - 1) / kThreads;  // slots of a thread
+  static constexpr int kZeroThread = kThreads / 2 - 1;  // 0 comes after this thread's values, as place kPer
   static_assert(kCounts * 4 < 65536, "byte offsets fit 16 bits");
-  __device__ static inline float value(int slot) {
-    if (slot == kZero) return 0.f;
-    const uint32_t b = slot < kZero ? (uint32_t)(kHi - 1 - slot) : 0x8000u | (uint32_t)(slot - kZero - 1 + kLo);
+  // place i of thread t
+  __device__ static inline float value(int t, int i) {
+    if (i >= kPer) return 0.f;
+    const int s = t * kPer + i;
+    const uint32_t b = s < kW ? (uint32_t)(kHi - 1 - s) : 0x8000u | (uint32_t)(s - kW + kLo);
     return __builtin_bit_cast(float, b << 16);
   }
-  __device__ static inline uint32_t count(const uint32_t* cnt, int slot) {
-    if (slot >= kSlots) return 0;
-    return slot < kZero ? cnt[kW - slot] : slot == kZero ? cnt[0] + cnt[kSign] : cnt[kSign + slot - kZero];
+  __device__ static inline uint32_t word(const uint32_t* cnt, int t, int i) {
+    const int s = t * kPer + i;
+    return i < kPer ? s < kW ? cnt[kW - s] : cnt[kSign + 1 + s - kW] : cnt[0];
   }
 };
+// A row's settings; in LDS, where they take no registers through the passes.
+struct Settings {
+  double T, p, min_p, u;
+  bool limit;
+  uint32_t k;
+};
 struct CountShared {
-  uint32_t cnt[Counted::kCounts];
+  Settings how;
+  u32x4_t words[(Counted::kCounts + 7) / 4];
   Red red;
-  uint32_t first;        // the first slot with a count
-  uint32_t pick, last;   // the thread a border falls to; the last one with mass
+  uint32_t first;    // the first place with a count
+  uint32_t last;     // the last thread with mass
+  uint32_t pick[3];  // the thread a border falls to
+  double got[3];     // the mass up to and with the border's token, its own mass,
+  double got_e[3];
+  uint32_t got_at[3], got_r[3], got_n[3];  // its place, which of the equal ones it is, and how many there are
+  uint32_t got_parts[3];
   uint32_t nth[2];
-  double above;          // mass and tokens before that thread's slots
-  uint32_t above_n;
+  // the counts, so that a thread's values are whole 16-byte words
+  __device__ inline uint32_t* cnt() { return (uint32_t*)words + 3; }
 };
 static_assert(kGroups <= Counted::kCounts, "the counts of groups take the counts' place");
 
+// Rows of fewer than 2^18 logits: a count takes the low 18 bits of its word, and
+// above them two fields of 7 bits count its logits in the row's first and in
+// its second third, which later tells the third that holds the n-th of fewer
+// than 128 equal logits (with more of them the fields overflow, harmlessly).
+constexpr int kPartShift = 18, kPartBits = 7;
+struct Thirds {
+  bool on;
+  uint32_t b1, b2;  // the second and the last third's first chunks
+  __device__ inline Thirds(const Row<__bf16>& row, bool use) {
+    b1 = row.nb / 3 / kThreads * kThreads;  // a round of chunks lies in one third
+    b2 = 2 * b1;
+    on = use && b1 > 0;
+  }
+  __device__ inline uint32_t mask() const { return on ? (1u << kPartShift) - 1 : 0xFFFFFFFFu; }
+  __device__ inline uint32_t step(uint32_t c) const {
+    const uint32_t s = c < b1 ? 1u + (1u << kPartShift) : c < b2 ? 1u + (1u << (kPartShift + kPartBits)) : 1u;
+    return on ? s : 1u;
+  }
+};
+
 // Two logits (the halves of w) counted.
-__device__ inline void count_pair(uint32_t w, char* cnt) {
+__device__ inline void count_pair(uint32_t w, char* cnt, uint32_t step) {
   typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   const i16x2 lo = {(int16_t)(Counted::kLo - 1), (int16_t)(Counted::kLo - 1)}, zero = {0, 0};
@@ -791,23 +846,26 @@ __device__ inline void count_pair(uint32_t w, char* cnt) {
   at = __builtin_elementwise_max(__builtin_elementwise_min(at, top), zero);
   at += (__builtin_bit_cast(i16x2, w) >> fifteen) & sign;
   const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, at) << (u16x2){2, 2});
-  atomicAdd((uint32_t*)(cnt + (b & 0xFFFFu)), 1u);
-  atomicAdd((uint32_t*)(cnt + (b >> 16)), 1u);
+  atomicAdd((uint32_t*)(cnt + (b & 0xFFFFu)), step);
+  atomicAdd((uint32_t*)(cnt + (b >> 16)), step);
 }
-__device__ inline void count_one(uint32_t h, uint32_t* cnt) {
+__device__ inline void count_one(uint32_t h, uint32_t* cnt, uint32_t step) {
   int at = (int)(h & 0x7FFFu) - (Counted::kLo - 1);
   at = at < 0 ? 0 : at > Counted::kW + 1 ? Counted::kW + 1 : at;
-  atomicAdd(&cnt[at + (h & 0x8000u ? Counted::kSign : 0)], 1u);
+  atomicAdd(&cnt[at + (h & 0x8000u ? Counted::kSign : 0)], step);
 }
 
-__device__ inline void count_row(const Row<__bf16>& row, uint32_t* cnt) {
+__device__ inline void count_row(const Row<__bf16>& row, uint32_t* cnt, const Thirds& parts) {
   for_each_chunk<8>(
       row,
-      [&](const u32x4_t& v, uint32_t) {
+      [&](const u32x4_t& v, uint32_t c) {
+        const uint32_t step = parts.step(c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) count_pair(v[i], (char*)cnt);
+        for (int i = 0; i < 4; ++i) count_pair(v[i], (char*)cnt, step);
       },
-      [&](__bf16 x, int64_t) { count_one(__builtin_bit_cast(uint16_t, x), cnt); });
+      [&](__bf16 x, int64_t id) {
+        count_one(__builtin_bit_cast(uint16_t, x), cnt, parts.step(id < row.head ? 0 : row.nb));
+      });
 }
 
 // Whether the row holds a nonzero logit below 2^-26 in magnitude.
@@ -817,108 +875,139 @@ __device__ inline bool has_tiny(const Row<__bf16>& row) {
   return __syncthreads_or(tiny);
 }
 
-struct Settings {
-  double T, p, min_p, u;
-  bool limit;
-  uint32_t k;
+// A drawn token: the r-th (r >= 1) of the row's n logits of this value, its
+// mass e and the mass S it was drawn from.
+struct Drawn {
+  float logit;
+  uint32_t r, n, parts;  // parts: the fields of n's thirds
+  double e, S;
 };
 
-// From the counts in sh.cnt: the logit of the drawn token, which of the equal
-// ones it is (r >= 1; 0: nothing to draw), and its log-probability.  False:
-// the row is one for the general path.
-__device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, const Settings& how,
-                                             float* logit, uint32_t* nth, double* logp) {
+// The draw from the counts in sh.  False: the row is one for the general path.
+__device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, uint32_t mask, Drawn* out) {
+  const Settings& how = sh.how;
   const int tid = threadIdx.x, lane = tid & 63;
-  constexpr int kPer = Counted::kPer;
-  if (sh.cnt[Counted::kW + 1] != 0) return false;  // 256 and more, +inf or NaN
-  // the largest logit: the first slot with a count
-  uint32_t n[kPer], mine = 0, first = 0xFFFFFFFFu;
+  constexpr int kPer = Counted::kPer, kPlaces = kPer + 1;
+  const uint32_t* cnt = sh.cnt();
+  if (tid == 0) {
+    sh.first = 0xFFFFFFFFu;
+    sh.last = 0;
+    for (int i = 0; i < 3; ++i) sh.pick[i] = 0xFFFFFFFFu;
+  }
+  if ((cnt[Counted::kW + 1] & mask) != 0) return false;  // 256 and more, +inf or NaN
+  const bool low = (cnt[Counted::kSign + Counted::kW + 1] & mask) != 0;  // -256 and less, -inf or NaN
+  const uint32_t zeros = (cnt[0] & mask) + (cnt[Counted::kSign] & mask);
+  uint32_t n[kPer], mine = tid == Counted::kZeroThread ? zeros : 0;
+  {
+    const int s = tid * kPer;
+    const bool neg = s >= Counted::kW;
+    const int at = neg ? Counted::kSign + 1 + s - Counted::kW : Counted::kW - s - kPer + 1;
+    const u32x4_t a = ((const u32x4_t*)(cnt + at))[0], b = ((const u32x4_t*)(cnt + at))[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n[i] = (neg ? a[i] : b[3 - i]) & mask;
+      n[4 + i] = (neg ? b[i] : a[3 - i]) & mask;
+    }
+  }
+  int first = kPer;
 #pragma unroll
   for (int i = kPer - 1; i >= 0; --i) {
-    n[i] = Counted::count(sh.cnt, tid * kPer + i);
     mine += n[i];
-    if (n[i]) first = (uint32_t)(tid * kPer + i);
+    if (n[i]) first = i;
   }
-  const uint64_t any = __ballot(first != 0xFFFFFFFFu);
-  if (any && lane == __builtin_ctzll(any)) atomicMin(&sh.first, first);
   __syncthreads();
-  first = sh.first;
-  const bool low = sh.cnt[Counted::kSign + Counted::kW + 1] != 0;  // -256 and less, -inf or NaN
-  if (first == 0xFFFFFFFFu) return false;
+  const uint64_t any = __ballot(mine != 0);
+  min_of_hits(mine != 0, (uint32_t)(tid * kPlaces + first), &sh.first);
+  __syncthreads();
+  const uint32_t top = sh.first;
+  if (top == 0xFFFFFFFFu) return false;
   Scale sc;
-  sc.set(Counted::value((int)first), how.T, 0);
+  sc.set(Counted::value((int)(top / kPlaces), (int)(top % kPlaces)), how.T, 0);
   if (low && sc.y(-256.f) < (double)kBins) return false;
+  const double e0 = mass_of(sh.red, sc.y(0.f));  // of 0, where the row has it
   double sum = 0.0, likely = 0.0, before = 0.0, dummy;
   uint32_t cbefore = 0;
-  if (any) {  // else every slot of the wave is empty
-#pragma unroll 3
+  if (any) {  // else every place of the wave is empty
+    // from the thread's first value that occurs (those above it may lie above
+    // the largest logit, where e would overflow), each e is q of the one before
+    const float v = Counted::value(tid, first);
+    const uint32_t octave = __builtin_bit_cast(uint32_t, v) & 0x7F800000u;
+    const float step = __builtin_bit_cast(float, octave - (7u << 23));
+    double y = sc.y(v);
+    const double dy = first < kPer ? (double)step * sc.c : 0.0, q = mass_of(sh.red, dy);
+    double e = mine ? mass_of(sh.red, y) : 0.0;
+#pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      // slots above the largest logit are empty, and their e may overflow
-      const double e = n[i] ? mass_of(sh.red, sc.y(Counted::value(tid * kPer + i))) : 0.0;
-      sum += (double)n[i] * e;
-      if (e >= how.min_p) likely += (double)n[i] * e;
+      const double m = (double)n[i] * e;
+      sum += m;
+      if (e >= how.min_p) likely += m;
+      if (i >= first) {
+        y += dy;
+        e = y < (double)kBins ? e * q : 0.0;
+      }
+    }
+    if (tid == Counted::kZeroThread && zeros) {
+      sum += (double)zeros * e0;
+      if (e0 >= how.min_p) likely += (double)zeros * e0;
     }
   }
   double S = block_prefix(sum, sh.red, &before);
   if (how.limit) block_prefix(mine, sh.red, &cbefore);
   const double s_min = how.min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
-  // nonzero logits below 2^-26 are taken as 0: off by 2^-26 / T of their mass
-  const uint32_t zeros = sh.cnt[0] + sh.cnt[Counted::kSign];
-  if (zeros && (double)zeros * mass_of(sh.red, sc.y(0.f)) * 0x1p-26 / how.T > 1e-13 * S && has_tiny(row)) return false;
+  // nonzero logits below 2^-24 are taken as 0: off by 2^-24 / T of their mass
+  bool tiny_counts = zeros && (double)zeros * e0 * 0x1p-24 / how.T > 1e-13 * S;
 
-  // A border: the first thread at the end of whose slots it is reached (the
-  // last with mass if rounding leaves none), then among that thread's slots,
-  // one per lane, in every wave alike.
-  int slot = 0;
-  uint32_t r = 0;
-  double at_e = 0.0;
-  bool in_zero = false;
-  auto border = [&](int kind, double target) {
-    __syncthreads();
-    if (tid == 0) {
-      sh.pick = 0xFFFFFFFFu;
-      sh.last = 0;
-    }
-    __syncthreads();
-    min_of_hits(sum > 0.0 && reached(kind, cbefore + mine, before + sum, how.k, target), (uint32_t)tid, &sh.pick);
-    max_of_hits(sum > 0.0, (uint32_t)tid, &sh.last);
-    __syncthreads();
-    const uint32_t at = sh.pick != 0xFFFFFFFFu ? sh.pick : sh.last;
-    if ((uint32_t)tid == at) {
-      sh.above = before;
-      sh.above_n = cbefore;
-    }
-    __syncthreads();
-    const int s = (int)at * kPer + lane;
-    const uint32_t ns = lane < kPer ? Counted::count(sh.cnt, s) : 0;
-    const double e = ns ? mass_of(sh.red, sc.y(Counted::value(s))) : 0.0;
-    static_assert(kPer <= 16, "the slots of a thread lie in one row of lanes");
-    const double run = sh.above + wave_scan((double)ns * e);
-    const uint32_t crun = sh.above_n + wave_scan(ns);
-    const bool on = ns && e > 0.0;
-    const uint64_t there = __ballot(on && reached(kind, crun, run, how.k, target)), some = __ballot(on);
-    const int l = there ? __builtin_ctzll(there) : 63 - __builtin_clzll(some | 1ull);
-    const uint32_t nl = __shfl(ns, l), before_n = __shfl(crun, l) - nl;
-    at_e = __shfl(e, l);
-    const double above = l > 0 ? __shfl(run, l > 0 ? l - 1 : 0) : sh.above;
-    slot = (int)at * kPer + l;
-    in_zero |= slot == Counted::kZero;
-    r = equal_taken(kind, nl, before_n, above, at_e, how.k, target);
-    return above + (double)r * at_e;
-  };
-  // k, then p, then the draw: one copy of the code, run up to three times
+  // Borders: k, then p, then the draw.  Each falls to the first thread at the
+  // end of whose values it is reached (the last with mass if rounding leaves
+  // none); that thread's wave takes its places one per lane.
+  max_of_hits(sum > 0.0, (uint32_t)tid, &sh.last);
 #pragma unroll 1
   for (int kind = how.limit ? BY_COUNT : how.p < 1.0 ? BY_MASS : BY_MASS_OVER;;) {
     if (kind == BY_MASS_OVER) S = fmin(S, s_min);
-    const double got = border(kind, kind == BY_MASS ? how.p * S : how.u * S);
+    const double target = kind == BY_MASS ? how.p * S : how.u * S;
+    min_of_hits(sum > 0.0 && reached(kind, cbefore + mine, before + sum, how.k, target), (uint32_t)tid, &sh.pick[kind]);
+    __syncthreads();
+    const uint32_t hit = sh.pick[kind], at = hit != 0xFFFFFFFFu ? hit : sh.last;
+    if (at >> 6 == (uint32_t)tid >> 6) {
+      const double above0 = __shfl(before, (int)(at & 63));
+      const uint32_t above_n0 = __shfl(cbefore, (int)(at & 63));
+      const bool zero = lane == kPer && at == Counted::kZeroThread;
+      uint32_t word = lane < kPer || zero ? Counted::word(cnt, (int)at, lane) : 0, ns = word & mask;
+      word >>= kPartShift;
+      if (zero) {
+        ns = zeros;
+        word += cnt[Counted::kSign] >> kPartShift;
+      }
+      const double e = ns ? mass_of(sh.red, sc.y(Counted::value((int)at, lane))) : 0.0;
+      static_assert(kPlaces <= 16, "the places of a thread lie in one row of lanes");
+      const double run = above0 + wave_scan((double)ns * e);
+      const uint32_t crun = above_n0 + wave_scan(ns);
+      const uint64_t there = __ballot(ns && e > 0.0 && reached(kind, crun, run, how.k, target));
+      const uint64_t some = __ballot(ns && e > 0.0);
+      const int l = there ? __builtin_ctzll(there) : 63 - __builtin_clzll(some | 1ull);
+      const uint32_t nl = __shfl(ns, l), before_n = __shfl(crun, l) - nl;
+      const double el = __shfl(e, l), above = l > 0 ? __shfl(run, l > 0 ? l - 1 : 0) : above0;
+      const uint32_t r = nl ? equal_taken(kind, nl, before_n, above, el, how.k, target) : 0;
+      if (lane == 0) {
+        sh.got[kind] = above + (double)r * el;
+        sh.got_e[kind] = el;
+        sh.got_at[kind] = at * kPlaces + (uint32_t)l;
+        sh.got_r[kind] = r;
+        sh.got_n[kind] = nl;
+      }
+      if (lane == l) sh.got_parts[kind] = word;
+    }
+    __syncthreads();
+    tiny_counts |= sh.got_at[kind] % kPlaces == kPer;
+    if (sh.got_r[kind] == 0) return false;  // nothing with mass there
     if (kind == BY_MASS_OVER) break;
-    S = fmin(S, got);
+    S = fmin(S, sh.got[kind]);
     kind = kind == BY_COUNT && how.p < 1.0 ? BY_MASS : BY_MASS_OVER;
   }
-  if (in_zero && has_tiny(row)) return false;
-  *logp = log(at_e / S);
-  *logit = Counted::value(slot);
-  *nth = r;
+  if (tiny_counts && has_tiny(row)) return false;
+  const uint32_t at = sh.got_at[BY_MASS_OVER];
+  *out = Drawn{Counted::value((int)(at / kPlaces), (int)(at % kPlaces)), sh.got_r[BY_MASS_OVER], sh.got_n[BY_MASS_OVER],
+               sh.got_parts[BY_MASS_OVER], sh.got_e[BY_MASS_OVER], S};
   return true;
 }
 
@@ -964,13 +1053,13 @@ __device__ inline Settings row_settings(const SampleArgs& a, int64_t r) {
 }
 
 __device__ inline void clear_counts(CountShared& sh) {
-  for (int i = threadIdx.x; i < Counted::kCounts; i += kThreads) sh.cnt[i] = 0;
-  if (threadIdx.x == 0) sh.first = 0xFFFFFFFFu;
+  for (int i = threadIdx.x; i < (int)(sizeof(sh.words) / 16); i += kThreads) sh.words[i] = u32x4_t{0, 0, 0, 0};
 }
-__device__ inline void put(const SampleArgs& a, int64_t r, int64_t id, double logp) {
+// The row's answer: token id, of mass e among S.
+__device__ inline void put(const SampleArgs& a, int64_t r, int64_t id, double e, double S) {
   if (threadIdx.x == 0) {
     a.ids[r] = (int32_t)id;
-    if (a.logp) a.logp[r] = (float)logp;
+    if (a.logp) a.logp[r] = (float)log(e / S);
   }
 }
 
@@ -978,18 +1067,36 @@ __global__ void __launch_bounds__(kThreads, 8) count_kernel(SampleArgs a) {
   __shared__ CountShared sh;
   const int64_t r = blockIdx.x;
   const Row<__bf16> row((const __bf16*)a.x + r * a.ld, a.V);
-  const Settings how = row_settings(a, r);
+  if (threadIdx.x == 0) sh.how = row_settings(a, r);
   clear_counts(sh);
   fill_pow64(sh.red);
   __syncthreads();
-  count_row(row, sh.cnt);
+  const Thirds parts(row, a.V < (1 << kPartShift));
+  count_row(row, sh.cnt(), parts);
   __syncthreads();
-  float logit = 0.f;
-  uint32_t nth = 0;
-  double logp = 0.0;
+  Drawn t{};
   int64_t id = kLeft;
-  if (pick_counted(row, sh, how, &logit, &nth, &logp)) id = nth_equal(row, sh.cnt, sh.red, sh.nth, logit, nth);
-  put(a, r, id, logp);
+  if (pick_counted(row, sh, parts.mask(), &t)) {
+    int64_t b = 0, e = a.V;
+    if (parts.on && t.n < 1u << kPartBits) {
+      const uint32_t n1 = t.parts & ((1u << kPartBits) - 1), n2 = t.parts >> kPartBits;
+      if (t.r <= n1) {
+        t.n = n1;
+        e = row.body_id(parts.b1);
+      } else if (t.r - n1 <= n2) {
+        t.r -= n1;
+        t.n = n2;
+        b = row.body_id(parts.b1);
+        e = row.body_id(parts.b2);
+      } else {
+        t.r -= n1 + n2;
+        t.n -= n1 + n2;
+        b = row.body_id(parts.b2);
+      }
+    }
+    id = b + nth_equal(Row<__bf16>(row.x + b, e - b), sh.cnt(), sh.red, sh.nth, t.logit, t.r, t.n);
+  }
+  put(a, r, id, t.e, t.S);
 }
 
 // Few long rows: `slices` workgroups count a row's slices, so that more of the
@@ -1007,11 +1114,12 @@ __global__ void __launch_bounds__(kThreads, 8) count_slice_kernel(SampleArgs a) 
   const int s = (int)(blockIdx.x - r * a.slices);
   clear_counts(sh);
   __syncthreads();
-  count_row(slice_of(a, r, s), sh.cnt);
+  const Row<__bf16> row = slice_of(a, r, s);
+  count_row(row, sh.cnt(), Thirds(row, false));
   __syncthreads();
   uint32_t* dst = (uint32_t*)(a.tables + (int64_t)blockIdx.x * kTable);
   for (int i = threadIdx.x; i < Counted::kCounts / 2; i += kThreads)
-    dst[i] = sh.cnt[2 * i] | sh.cnt[2 * i + 1] << 16;
+    dst[i] = sh.cnt()[2 * i] | sh.cnt()[2 * i + 1] << 16;
 }
 static_assert(Counted::kCounts % 2 == 0, "counts are stored in pairs");
 
@@ -1020,10 +1128,9 @@ __global__ void __launch_bounds__(kThreads, 8) count_finish_kernel(SampleArgs a)
   __shared__ uint32_t there[kSlicesMax];
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
-  const Settings how = row_settings(a, r);
+  if (tid == 0) sh.how = row_settings(a, r);
   const uint16_t* tables = a.tables + r * a.slices * kTable;
   fill_pow64(sh.red);
-  if (tid == 0) sh.first = 0xFFFFFFFFu;
   for (int i = tid; i < Counted::kCounts / 2; i += kThreads) {
     uint32_t lo = 0, hi = 0;
 #pragma unroll 4
@@ -1032,29 +1139,27 @@ __global__ void __launch_bounds__(kThreads, 8) count_finish_kernel(SampleArgs a)
       lo += w & 0xFFFFu;
       hi += w >> 16;
     }
-    sh.cnt[2 * i] = lo;
-    sh.cnt[2 * i + 1] = hi;
+    sh.cnt()[2 * i] = lo;
+    sh.cnt()[2 * i + 1] = hi;
   }
   __syncthreads();
-  float logit = 0.f;
-  uint32_t nth = 0;
-  double logp = 0.0;
+  Drawn d{};
   int64_t id = kLeft;
   const Row<__bf16> row((const __bf16*)a.x + r * a.ld, a.V);
-  if (pick_counted(row, sh, how, &logit, &nth, &logp)) {
-    // the slice that holds the nth such logit
+  if (pick_counted(row, sh, 0xFFFFFFFFu, &d)) {
+    // the slice that holds the r-th such logit
     if (tid < a.slices) {
       const uint16_t* t = tables + tid * kTable;
-      const uint32_t h = __builtin_bit_cast(uint32_t, logit) >> 16;
+      const uint32_t h = __builtin_bit_cast(uint32_t, d.logit) >> 16;
       const int at = (int)(h & 0x7FFFu) - (Counted::kLo - 1);
-      there[tid] = logit == 0.f ? (uint32_t)t[0] + t[Counted::kSign] : t[at + (h & 0x8000u ? Counted::kSign : 0)];
+      there[tid] = d.logit == 0.f ? (uint32_t)t[0] + t[Counted::kSign] : t[at + (h & 0x8000u ? Counted::kSign : 0)];
     }
     __syncthreads();
     int s = 0;
-    while (s + 1 < a.slices && nth > there[s]) nth -= there[s++];
-    id = s * a.slice_len + nth_equal(slice_of(a, r, s), sh.cnt, sh.red, sh.nth, logit, nth);
+    while (s + 1 < a.slices && d.r > there[s]) d.r -= there[s++];
+    id = s * a.slice_len + nth_equal(slice_of(a, r, s), sh.cnt(), sh.red, sh.nth, d.logit, d.r, there[s]);
   }
-  put(a, r, id, logp);
+  put(a, r, id, d.e, d.S);
 }
 
 // The general path: every row (direct), or those that the counting kernels left.

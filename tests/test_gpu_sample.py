@@ -266,6 +266,38 @@ def test_same_bits_every_time_and_on_two_streams(ckl):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+@pytest.mark.parametrize("V", [5003, 24577, 30001, 100003, 262143, 262144])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_which_of_equal_logits(ckl, V, dtype):
+    # n equal largest logits among ones that weigh nothing (e^-60 each): the
+    # draw is the ceil(u n)-th of them in id order.  Rows start at every
+    # alignment; the equal logits sit at the row's ends, at and beside the
+    # borders of its thirds (in whole rounds of 8,192) and anywhere.
+    N, ld = 72, V + 3
+    rng = np.random.default_rng(V)
+    b1 = V // 8 // 3 // 1024 * 8192
+    marks = sorted({m + k for m in (0, b1, 2 * b1, V - 1) for k in range(-9, 10) if 0 <= m + k < V})
+    x = np.full((N, ld), -40.0, np.float32)
+    u, want = np.empty(N, np.float32), []
+    for r in range(N):
+        n = (1, 2, 5, 127, 128, 129, 300, 4000)[r % 8]
+        if r % 3 == 0:
+            at = rng.choice(marks, min(n, len(marks)), replace=False)
+        elif r % 3 == 1:
+            at = rng.choice(V, n, replace=False)
+        else:  # one stretch
+            at = rng.integers(0, V - n + 1) + np.arange(n)
+        at = np.sort(at)
+        k = int(rng.integers(len(at))) if r >= 16 else (0 if r < 8 else len(at) - 1)
+        x[r, at] = 20.0
+        u[r] = (k + 0.5) / len(at)
+        want.append(int(at[k]))
+    X = torch.from_numpy(x).to("cuda:0")
+    X = (X.bfloat16() if dtype == "bf16" else X)[:, :V]
+    ids, _ = ckl.sample(X, torch.from_numpy(u).to("cuda:0"))
+    assert ids.tolist() == want
+
+
 def test_captured_and_replayed(ckl):
     x, u = rows(40, 9000, "bf16"), uniforms(40)
     s = torch.cuda.Stream()
