@@ -186,10 +186,10 @@ struct Scale {
   float mxf, cf;
   bool inf;            // the largest logit is +inf: equal ones weigh 1, all others nothing
   bool wide;           // c or the logits' differences may leave fp32's range
-  __device__ inline void set(float m, double T, int fix_bits) {
+  __device__ inline void set(float m, double over_t, int fix_bits) {
     inf = m == INFINITY;
     mx = (double)m;
-    c = 92.332482616893656877 / T;
+    c = over_t;
     fix = (double)(1ull << fix_bits);
     inv_fix = 1.0 / fix;
     mxf = m;
@@ -225,6 +225,14 @@ struct Scale {
       fn(std::false_type{});
   }
 };
+
+// A value that is the same in every lane, in scalar registers.
+__device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline float uniform(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(uint32_t, v))); }
+__device__ inline double uniform(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)uniform((uint32_t)(b >> 32)) << 32 | uniform((uint32_t)b));
+}
 
 // 2^(-f / 64) for f in [-1e-3, 1 + 1e-3]: the polynomial of degree 4 through the
 // Chebyshev points of [0, 1], its constant moved to 1 so that f = 0 is exact;
@@ -795,6 +803,7 @@ struct Counted {
 // A row's settings; in LDS, where they take no registers through the passes.
 struct Settings {
   double T, p, min_p, u;
+  double c;  // 64 log2(e) / T
   bool limit;
   uint32_t k;
 };
@@ -885,7 +894,6 @@ struct Drawn {
 
 // The draw from the counts in sh.  False: the row is one for the general path.
 __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared& sh, uint32_t mask, Drawn* out) {
-  const Settings& how = sh.how;
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int kPer = Counted::kPer, kPlaces = kPer + 1;
   const uint32_t* cnt = sh.cnt();
@@ -896,7 +904,7 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
   }
   if ((cnt[Counted::kW + 1] & mask) != 0) return false;  // 256 and more, +inf or NaN
   const bool low = (cnt[Counted::kSign + Counted::kW + 1] & mask) != 0;  // -256 and less, -inf or NaN
-  const uint32_t zeros = (cnt[0] & mask) + (cnt[Counted::kSign] & mask);
+  const uint32_t zeros = uniform((cnt[0] & mask) + (cnt[Counted::kSign] & mask));
   uint32_t n[kPer], mine = tid == Counted::kZeroThread ? zeros : 0;
   {
     const int s = tid * kPer;
@@ -919,12 +927,13 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
   const uint64_t any = __ballot(mine != 0);
   min_of_hits(mine != 0, (uint32_t)(tid * kPlaces + first), &sh.first);
   __syncthreads();
-  const uint32_t top = sh.first;
+  const uint32_t top = uniform(sh.first);
   if (top == 0xFFFFFFFFu) return false;
   Scale sc;
-  sc.set(Counted::value((int)(top / kPlaces), (int)(top % kPlaces)), how.T, 0);
+  sc.set(Counted::value((int)(top / kPlaces), (int)(top % kPlaces)), uniform(sh.how.c), 0);
   if (low && sc.y(-256.f) < (double)kBins) return false;
-  const double e0 = mass_of(sh.red, sc.y(0.f));  // of 0, where the row has it
+  const double e0 = uniform(mass_of(sh.red, sc.y(0.f)));  // of 0, where the row has it
+  const double min_p = uniform(sh.how.min_p);
   double sum = 0.0, likely = 0.0, before = 0.0, dummy;
   uint32_t cbefore = 0;
   if (any) {  // else every place of the wave is empty
@@ -940,7 +949,7 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
     for (int i = 0; i < kPer; ++i) {
       const double m = (double)n[i] * e;
       sum += m;
-      if (e >= how.min_p) likely += m;
+      if (e >= min_p) likely += m;
       if (i >= first) {
         y += dy;
         e = y < (double)kBins ? e * q : 0.0;
@@ -948,26 +957,29 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
     }
     if (tid == Counted::kZeroThread && zeros) {
       sum += (double)zeros * e0;
-      if (e0 >= how.min_p) likely += (double)zeros * e0;
+      if (e0 >= min_p) likely += (double)zeros * e0;
     }
   }
-  double S = block_prefix(sum, sh.red, &before);
-  if (how.limit) block_prefix(mine, sh.red, &cbefore);
-  const double s_min = how.min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
+  double S = uniform(block_prefix(sum, sh.red, &before));
+  const bool limit = sh.how.limit;
+  if (limit) block_prefix(mine, sh.red, &cbefore);
+  const double s_min = min_p > 0.0 ? uniform(block_prefix(likely, sh.red, &dummy)) : S;
   // nonzero logits below 2^-24 are taken as 0: off by 2^-24 / T of their mass
-  bool tiny_counts = zeros && (double)zeros * e0 * 0x1p-24 / how.T > 1e-13 * S;
+  bool tiny_counts = zeros && (double)zeros * e0 * 0x1p-24 > 1e-13 * sh.how.T * S;
 
   // Borders: k, then p, then the draw.  Each falls to the first thread at the
   // end of whose values it is reached (the last with mass if rounding leaves
   // none); that thread's wave takes its places one per lane.
   max_of_hits(sum > 0.0, (uint32_t)tid, &sh.last);
+  const double p = uniform(sh.how.p), u = uniform(sh.how.u);
+  const uint32_t k = uniform(sh.how.k);
 #pragma unroll 1
-  for (int kind = how.limit ? BY_COUNT : how.p < 1.0 ? BY_MASS : BY_MASS_OVER;;) {
+  for (int kind = limit ? BY_COUNT : p < 1.0 ? BY_MASS : BY_MASS_OVER;;) {
     if (kind == BY_MASS_OVER) S = fmin(S, s_min);
-    const double target = kind == BY_MASS ? how.p * S : how.u * S;
-    min_of_hits(sum > 0.0 && reached(kind, cbefore + mine, before + sum, how.k, target), (uint32_t)tid, &sh.pick[kind]);
+    const double target = kind == BY_MASS ? p * S : u * S;
+    min_of_hits(sum > 0.0 && reached(kind, cbefore + mine, before + sum, k, target), (uint32_t)tid, &sh.pick[kind]);
     __syncthreads();
-    const uint32_t hit = sh.pick[kind], at = hit != 0xFFFFFFFFu ? hit : sh.last;
+    const uint32_t hit = sh.pick[kind], at = uniform(hit != 0xFFFFFFFFu ? hit : sh.last);
     if (at >> 6 == (uint32_t)tid >> 6) {
       const double above0 = __shfl(before, (int)(at & 63));
       const uint32_t above_n0 = __shfl(cbefore, (int)(at & 63));
@@ -982,12 +994,12 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
       static_assert(kPlaces <= 16, "the places of a thread lie in one row of lanes");
       const double run = above0 + wave_scan((double)ns * e);
       const uint32_t crun = above_n0 + wave_scan(ns);
-      const uint64_t there = __ballot(ns && e > 0.0 && reached(kind, crun, run, how.k, target));
+      const uint64_t there = __ballot(ns && e > 0.0 && reached(kind, crun, run, k, target));
       const uint64_t some = __ballot(ns && e > 0.0);
       const int l = there ? __builtin_ctzll(there) : 63 - __builtin_clzll(some | 1ull);
       const uint32_t nl = __shfl(ns, l), before_n = __shfl(crun, l) - nl;
       const double el = __shfl(e, l), above = l > 0 ? __shfl(run, l > 0 ? l - 1 : 0) : above0;
-      const uint32_t r = nl ? equal_taken(kind, nl, before_n, above, el, how.k, target) : 0;
+      const uint32_t r = nl ? equal_taken(kind, nl, before_n, above, el, k, target) : 0;
       if (lane == 0) {
         sh.got[kind] = above + (double)r * el;
         sh.got_e[kind] = el;
@@ -1001,13 +1013,17 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
     tiny_counts |= sh.got_at[kind] % kPlaces == kPer;
     if (sh.got_r[kind] == 0) return false;  // nothing with mass there
     if (kind == BY_MASS_OVER) break;
-    S = fmin(S, sh.got[kind]);
-    kind = kind == BY_COUNT && how.p < 1.0 ? BY_MASS : BY_MASS_OVER;
+    S = fmin(S, uniform(sh.got[kind]));
+    kind = kind == BY_COUNT && p < 1.0 ? BY_MASS : BY_MASS_OVER;
   }
   if (tiny_counts && has_tiny(row)) return false;
-  const uint32_t at = sh.got_at[BY_MASS_OVER];
-  *out = Drawn{Counted::value((int)(at / kPlaces), (int)(at % kPlaces)), sh.got_r[BY_MASS_OVER], sh.got_n[BY_MASS_OVER],
-               sh.got_parts[BY_MASS_OVER], sh.got_e[BY_MASS_OVER], S};
+  const uint32_t at = uniform(sh.got_at[BY_MASS_OVER]);
+  out->logit = Counted::value((int)(at / kPlaces), (int)(at % kPlaces));
+  out->r = uniform(sh.got_r[BY_MASS_OVER]);
+  out->n = uniform(sh.got_n[BY_MASS_OVER]);
+  out->parts = uniform(sh.got_parts[BY_MASS_OVER]);
+  out->e = uniform(sh.got_e[BY_MASS_OVER]);
+  out->S = S;
   return true;
 }
 
@@ -1041,6 +1057,7 @@ __device__ inline Settings row_settings(const SampleArgs& a, int64_t r) {
     k = 1;
   }
   s.T = fmax(s.T, 1e-200);  // keeps 1 / T finite; only equal logits share the mass long before
+  s.c = 92.332482616893656877 / s.T;
   s.limit = k > 0 && k < a.V;
   s.k = (uint32_t)(s.limit ? k : a.V);
   if (!(s.min_p > 0.0)) s.min_p = 0.0;
@@ -1189,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     return;
   }
   Scale sc;
-  sc.set(mx, how.T, a.fix_bits);
+  sc.set(mx, how.c, a.fix_bits);
 
   // 2a. few tokens: those that reach the k-th largest of the threads' maxima
   if (a.direct && k <= (uint32_t)kFastK) {
