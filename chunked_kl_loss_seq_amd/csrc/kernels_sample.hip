@@ -102,6 +102,20 @@ struct Key<float> {
 __device__ inline uint64_t pack(uint32_t key, uint32_t id) { return ((uint64_t)key << 32) | (0xFFFFFFFFu - id); }
 __device__ inline uint32_t unpack_id(uint64_t c) { return 0xFFFFFFFFu - (uint32_t)c; }
 
+// A value that is the same in every lane, in scalar registers.
+__device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline float uniform(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(uint32_t, v))); }
+__device__ inline double uniform(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)uniform((uint32_t)(b >> 32)) << 32 | uniform((uint32_t)b));
+}
+// A lane's value, the lane being the same for all.
+__device__ inline uint32_t of_lane(uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); }
+__device__ inline double of_lane(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)of_lane((uint32_t)(b >> 32), l) << 32 | of_lane((uint32_t)b, l));
+}
+
 // A row as its 16-byte aligned chunks, `nb` of them, with the fewer than kN
 // elements before the first one and after the last one apart.
 template <typename T>
@@ -226,14 +240,6 @@ struct Scale {
   }
 };
 
-// A value that is the same in every lane, in scalar registers.
-__device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ inline float uniform(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(uint32_t, v))); }
-__device__ inline double uniform(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)uniform((uint32_t)(b >> 32)) << 32 | uniform((uint32_t)b));
-}
-
 // 2^(-f / 64) for f in [-1e-3, 1 + 1e-3]: the polynomial of degree 4 through the
 // Chebyshev points of [0, 1], its constant moved to 1 so that f = 0 is exact;
 // off by at most 5e-15.
@@ -280,7 +286,6 @@ struct Shared {
   uint64_t edge_mass[3];      // mass of the tokens of min_p's bin and of its neighbours that reach it
   uint32_t n_cand;
   uint32_t pick;
-  uint32_t nth[2];
   double pick_mass;           // mass above the chosen bin or digit
   uint32_t pick_count;        // tokens above it
   double got_mass;
@@ -487,101 +492,76 @@ __device__ inline bool may_equal(const u32x4_t& v, float l, __bf16*) {
 }
 
 // The id of the r-th token (1 <= r <= n) of the n of logit l in id order, in
-// every thread.  A wave reads 64 chunks at once; the equal logits of every such
-// piece (or group of pieces, in long rows) are counted from the row's nearer
-// end (by r among n) until the r-th is passed, then every wave alike goes
-// through the group that holds it.  cnt: kGroups words of LDS, pick: two.
-constexpr int kGroups = 2 * kThreads;
+// every thread.  A wave reads 64 chunks (a piece) at once, the workgroup 64
+// pieces a round, from the row's nearer end (by r among n); the wave that holds
+// the r-th finds it among its own.  room: kNthRoom words of LDS.
+constexpr int kNthPieces = 64;
+constexpr int kNthRoom = 2 * kNthPieces + 1;  // the pieces' counts of two rounds in turn, and the id
 template <typename T>
-__device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* cnt, Red& red, uint32_t* pick, float l,
-                                             uint32_t r, uint32_t n) {
-  constexpr int U = kFlight;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+__device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* room, float l, uint32_t r, uint32_t n) {
+  constexpr int U = kNthPieces / kWaves;
+  const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   // the r-th set bit of a mask of lanes
   auto nth_lane = [](uint64_t m, uint32_t n) {
     for (; n > 1; --n) m &= m - 1;
     return __builtin_ctzll(m);
   };
-  const uint64_t head = __ballot(lane < row.head && (float)row.x[lane < row.head ? lane : 0] == l);
-  const uint64_t tail = __ballot(lane < row.tail && (float)row.x[lane < row.tail ? row.tail_id() + lane : 0] == l);
+  const int ilane = (int)lane;
+  const uint64_t head = row.head == 0 ? 0 : __ballot(ilane < row.head && (float)row.x[ilane < row.head ? ilane : 0] == l);
+  const uint64_t tail =
+      row.tail == 0 ? 0 : __ballot(ilane < row.tail && (float)row.x[row.tail_id() + (ilane < row.tail ? ilane : 0)] == l);
   const uint32_t nh = (uint32_t)__popcll(head), in_body = n - nh - (uint32_t)__popcll(tail);
   if (r <= nh) return nth_lane(head, r);
   r -= nh;
   if (r > in_body) return row.tail_id() + nth_lane(tail, r - in_body);
-  if (row.nb == 0) return -1;
   const uint32_t pieces = (row.nb + 63) / 64;
-  int shift = 0;
-  while (((pieces - 1) >> shift) >= (uint32_t)kGroups) ++shift;
-  const uint32_t groups = ((pieces - 1) >> shift) + 1;
-  const bool back = r > in_body - r + 1;  // groups in falling order: the r-th is the (in_body - r + 1)-th
+  const bool back = r > in_body - r + 1;  // pieces in falling order: the r-th is the (in_body - r + 1)-th
   if (back) r = in_body - r + 1;
   __syncthreads();
-  for (uint32_t g = groups + tid; g < (uint32_t)kGroups; g += kThreads) cnt[g] = 0;  // the last round's rest
-  if (tid == 0) pick[0] = 0;
-  // rounds of U groups a wave, in order: after each, stop if the r-th is past
-  uint32_t done = 0;
-  while (done < groups) {
-    const uint32_t o0 = done + w;
-    uint32_t found[U];
+  uint32_t* cnt = room;
+  for (uint32_t done = 0; done < pieces; done += kNthPieces) {
+    u32x4_t v[U];
+    uint32_t c[U], m[U], upto[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) found[j] = 0;
-    for (uint32_t s = 0; s < (1u << shift); ++s) {
-      u32x4_t v[U];
-      uint32_t c[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const uint32_t o = o0 + j * kWaves;
-        const uint32_t g = o >= groups ? groups : back ? groups - 1 - o : o;
-        c[j] = ((g << shift) + s) * 64 + lane;
-        v[j] = row.body[c[j] < row.nb ? c[j] : row.nb - 1];
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const bool may = c[j] < row.nb && may_equal(v[j], l, (T*)nullptr);
-        if (__ballot(may) == 0) continue;
-        const uint32_t m = may ? equal_in(v[j], l, (T*)nullptr) : 0;
-#pragma unroll
-        for (int i = 0; i < Row<T>::kN; ++i) found[j] += (uint32_t)__popcll(__ballot((m >> i) & 1u));
-      }
+    for (int j = 0; j < U; ++j) {
+      const uint32_t o = done + j * kWaves + w;
+      c[j] = (o >= pieces ? pieces : back ? pieces - 1 - o : o) * 64 + lane;
+      v[j] = row.body[c[j] < row.nb ? c[j] : row.nb - 1];
     }
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (lane == 0 && o0 + j * kWaves < groups) cnt[o0 + j * kWaves] = found[j];
-    uint32_t sum = 0;
-#pragma unroll
-    for (int j = 0; j < U; ++j) sum += found[j];
-    __syncthreads();  // pick[0] is clear (first round), or read by all (later ones)
-    if (lane == 0 && sum) atomicAdd(&pick[0], sum);
+    for (int j = 0; j < U; ++j) {
+      const bool may = c[j] < row.nb && may_equal(v[j], l, (T*)nullptr);
+      m[j] = upto[j] = 0;
+      if (__ballot(may) != 0) {
+        m[j] = may ? equal_in(v[j], l, (T*)nullptr) : 0;
+        upto[j] = wave_scan((uint32_t)__popc(m[j]));
+      }
+      if (lane == 63) cnt[j * kWaves + w] = upto[j];
+    }
     __syncthreads();
-    done += U * kWaves;
-    if (pick[0] >= r) break;
-  }
-  // groups not reached count as empty
-  const uint32_t a = 2 * tid < done ? cnt[2 * tid] : 0, b = 2 * tid + 1 < done ? cnt[2 * tid + 1] : 0;
-  uint32_t before = 0;
-  block_prefix(a + b, red, &before);
-  if (before < r && before + a + b >= r) {
-    const bool second = before + a < r;
-    const uint32_t o = 2 * tid + (second ? 1 : 0), in = r - before - (second ? a : 0);
-    pick[0] = back ? groups - 1 - o : o;
-    pick[1] = back ? (second ? b : a) - in + 1 : in;
-  }
-  __syncthreads();
-  const uint32_t g = pick[0];
-  r = pick[1];
-  uint32_t seen = 0;
-  for (uint32_t s = 0; s < (1u << shift); ++s) {
-    const uint32_t c = ((g << shift) + s) * 64 + lane;
-    uint32_t m = equal_in(row.body[c < row.nb ? c : row.nb - 1], l, (T*)nullptr);
-    if (c >= row.nb) m = 0;
-    const uint32_t mine = (uint32_t)__popc(m), upto = seen + wave_scan(mine);
-    const uint64_t here = __ballot(upto - mine < r && upto >= r);
+    const uint32_t mine = cnt[lane], sum = wave_scan(mine);
+    const uint64_t here = __ballot(sum - mine < r && sum >= r);
     if (here) {
-      for (uint32_t skip = r - 1 - (upto - mine); skip > 0 && m; --skip) m &= m - 1;
       const int at = __builtin_ctzll(here);
-      return row.body_id(__shfl(c, at)) + __shfl(m ? __builtin_ctz(m) : 0, at);
+      const uint32_t of = of_lane(mine, at);
+      uint32_t in = r - (of_lane(sum, at) - of);
+      if (back) in = of - in + 1;
+      if ((uint32_t)at % kWaves == w) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          if (at / kWaves != j) continue;
+          uint32_t skip = in - 1 - (upto[j] - (uint32_t)__popc(m[j]));  // wraps where it lies in an earlier lane
+          if (skip < (uint32_t)__popc(m[j])) {
+            for (; skip > 0; --skip) m[j] &= m[j] - 1;
+            room[2 * kNthPieces] = (uint32_t)row.body_id(c[j]) + (uint32_t)__builtin_ctz(m[j]);
+          }
+        }
+      }
+      __syncthreads();
+      return (int64_t)uniform(room[2 * kNthPieces]);
     }
-    seen = __shfl(upto, 63);
+    r -= of_lane(sum, 63);
+    cnt = cnt == room ? room + kNthPieces : room;
   }
   return -1;  // not reached: the row holds n such logits
 }
@@ -756,7 +736,7 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
   const uint32_t r = equal_taken(kind, n, above_n, above, e, k, target);
   Found f{above + (double)r * e, l, -1};
   if (!want_id) return f;
-  f.id = nth_equal(row, (uint32_t*)sh.cand, sh.red, sh.nth, l, r, n);
+  f.id = nth_equal(row, (uint32_t*)sh.cand, l, r, n);
   return f;
 }
 
@@ -818,11 +798,10 @@ struct CountShared {
   double got_e[3];
   uint32_t got_at[3], got_r[3], got_n[3];  // its place, which of the equal ones it is, and how many there are
   uint32_t got_parts[3];
-  uint32_t nth[2];
   // the counts, so that a thread's values are whole 16-byte words
   __device__ inline uint32_t* cnt() { return (uint32_t*)words + 3; }
 };
-static_assert(kGroups <= Counted::kCounts, "the counts of groups take the counts' place");
+static_assert(kNthRoom <= Counted::kCounts, "the search takes the counts' place");
 
 // Rows of fewer than 2^18 logits: a count takes the low 18 bits of its word, and
 // above them two fields of 7 bits count its logits in the row's first and in
@@ -981,8 +960,8 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
     __syncthreads();
     const uint32_t hit = sh.pick[kind], at = uniform(hit != 0xFFFFFFFFu ? hit : sh.last);
     if (at >> 6 == (uint32_t)tid >> 6) {
-      const double above0 = __shfl(before, (int)(at & 63));
-      const uint32_t above_n0 = __shfl(cbefore, (int)(at & 63));
+      const double above0 = of_lane(before, (int)(at & 63));
+      const uint32_t above_n0 = of_lane(cbefore, (int)(at & 63));
       const bool zero = lane == kPer && at == Counted::kZeroThread;
       uint32_t word = lane < kPer || zero ? Counted::word(cnt, (int)at, lane) : 0, ns = word & mask;
       word >>= kPartShift;
@@ -997,8 +976,8 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
       const uint64_t there = __ballot(ns && e > 0.0 && reached(kind, crun, run, k, target));
       const uint64_t some = __ballot(ns && e > 0.0);
       const int l = there ? __builtin_ctzll(there) : 63 - __builtin_clzll(some | 1ull);
-      const uint32_t nl = __shfl(ns, l), before_n = __shfl(crun, l) - nl;
-      const double el = __shfl(e, l), above = l > 0 ? __shfl(run, l > 0 ? l - 1 : 0) : above0;
+      const uint32_t nl = of_lane(ns, l), before_n = of_lane(crun, l) - nl;
+      const double el = of_lane(e, l), above = l > 0 ? of_lane(run, l - 1) : above0;
       const uint32_t r = nl ? equal_taken(kind, nl, before_n, above, el, k, target) : 0;
       if (lane == 0) {
         sh.got[kind] = above + (double)r * el;
@@ -1111,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 8) count_kernel(SampleArgs a) {
         b = row.body_id(parts.b2);
       }
     }
-    id = b + nth_equal(Row<__bf16>(row.x + b, e - b), sh.cnt(), sh.red, sh.nth, t.logit, t.r, t.n);
+    id = b + nth_equal(Row<__bf16>(row.x + b, e - b), sh.cnt(), t.logit, t.r, t.n);
   }
   put(a, r, id, t.e, t.S);
 }
@@ -1174,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 8) count_finish_kernel(SampleArgs a)
     __syncthreads();
     int s = 0;
     while (s + 1 < a.slices && d.r > there[s]) d.r -= there[s++];
-    id = s * a.slice_len + nth_equal(slice_of(a, r, s), sh.cnt(), sh.red, sh.nth, d.logit, d.r, there[s]);
+    id = s * a.slice_len + nth_equal(slice_of(a, r, s), sh.cnt(), d.logit, d.r, there[s]);
   }
   put(a, r, id, d.e, d.S);
 }
