@@ -151,6 +151,13 @@ struct Row {
       }
     }
   }
+  __device__ static inline float largest(const u32x4_t& v) {
+    float f[kN];
+    unpack(v, f);
+#pragma unroll
+    for (int i = 1; i < kN; ++i) f[0] = fmaxf(f[0], f[i]);
+    return f[0];
+  }
 };
 
 // Every chunk of the row as chunk(words, index), the chunks of a thread in
@@ -1158,6 +1165,53 @@ __global__ void __launch_bounds__(kThreads, 8) count_finish_kernel(SampleArgs a)
   put(a, r, id, d.e, d.S);
 }
 
+// The row's answer from its first n (at most kFastK) tokens, sorted in sh.cand,
+// by one wave: each lane takes n / 64 adjacent ones.
+template <typename T>
+__device__ __forceinline__ void draw_from_list(const SampleArgs& a, int64_t r, const Shared& sh, int n, const Scale& sc,
+                                               const Settings& how) {
+  constexpr int kEach = kFastK / 64;
+  const int lane = threadIdx.x & 63, each = (n + 63) / 64, b = lane * each;
+  double e[kEach], mine = 0.0, likely = 0.0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    e[i] = i < each && b + i < n ? mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(sh.cand[b + i] >> 32)))) : 0.0;
+    mine += e[i];
+    if (e[i] >= how.min_p) likely += e[i];
+  }
+  const double upto = wave_scan(mine), up = __shfl_up(upto, 1), before = lane ? up : 0.0;
+  double S = of_lane(upto, 63);
+  // the first token at which the border is reached, the last if rounding leaves
+  // none, and the mass up to it
+  int at = 0;
+  auto border = [&](int kind, double target) {
+    int mine_at = -1;
+    double run = before, got = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      run += e[i];
+      const bool last = b + i == n - 1;
+      if (i < each && mine_at < 0 && b + i < n && (last || reached(kind, 0, run, 0, target))) {
+        mine_at = b + i;
+        got = run;
+      }
+    }
+    const int l = __builtin_ctzll(__ballot(mine_at >= 0));
+    at = (int)of_lane((uint32_t)mine_at, l);
+    return of_lane(got, l);
+  };
+  // p is a share of the first k's mass; min_p keeps at least the first token
+  const double s_min = how.min_p > 0.0 ? of_lane(wave_scan(likely), 63) : S;
+  if (how.p < 1.0) S = border(BY_MASS, how.p * S);
+  S = fmin(S, s_min);
+  border(BY_MASS_OVER, how.u * S);
+  const uint64_t c = sh.cand[at];
+  if (lane == 0) {
+    a.ids[r] = (int32_t)unpack_id(c);
+    if (a.logp) a.logp[r] = (float)log(mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(c >> 32)))) / S);
+  }
+}
+
 // The general path: every row (direct), or those that the counting kernels left.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
@@ -1175,7 +1229,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 
   // 1. the largest logit, and each thread's
   float mv = -INFINITY;
-  for_each(row, [&](float l, int64_t) { mv = fmaxf(mv, l); });
+  for_each_chunk<8>(
+      row, [&](const u32x4_t& v, uint32_t) { mv = fmaxf(mv, Row<T>::largest(v)); },
+      [&](T l, int64_t) { mv = fmaxf(mv, (float)l); });
   const float mx = block_max(mv, sh.red);
   if (mx == -INFINITY) {  // nothing to sample
     if (tid == 0) {
@@ -1218,42 +1274,29 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     __syncthreads();
     const uint32_t t0 = sh.pick;
     const float v0 = t0 <= Key<T>::of(-INFINITY) ? -INFINITY : Key<T>::value(t0);
-    for_each(row, [&](float l, int64_t id) {
+    auto hold = [&](float l, int64_t id) {
       if (l >= v0 && l > -INFINITY) {
         const uint32_t slot = atomicAdd(&sh.n_cand, 1u);
         if (slot < (uint32_t)kCap) sh.cand[slot] = pack(Key<T>::of(l), (uint32_t)id);
       }
-    });
+    };
+    if (mv >= v0)  // among the logits of this thread
+      for_each_chunk<kFlight>(
+          row,
+          [&](const u32x4_t& v, uint32_t c) {
+            if (Row<T>::largest(v) >= v0) {
+              float f[Row<T>::kN];
+              Row<T>::unpack(v, f);
+#pragma unroll
+              for (int i = 0; i < Row<T>::kN; ++i) hold(f[i], row.body_id(c) + i);
+            }
+          },
+          [&](T l, int64_t id) { hold((float)l, id); });
     __syncthreads();
     const uint32_t held = sh.n_cand;
     if (held <= (uint32_t)kCap) {
       sort_cand(sh, (int)held);
-      const int n = (int)(held < k ? held : k);
-      // the mass of the first n, the shortest prefixes for p and min_p, the draw
-      double S = 0.0, m = 0.0;
-      int j = 0;
-#pragma unroll 1
-      for (int step = 0; step < 4; ++step) {
-        if ((step == 1 && !(p < 1.0)) || (step == 2 && !(min_p > 0.0))) continue;
-        uint32_t len = (uint32_t)n;
-        if (step == 2) {  // the prefix with e >= min_p: its length is a count of the list
-          uint32_t c = 0, b = 0;
-          for (int i = tid; i < n; i += kThreads)
-            c += mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(sh.cand[i] >> 32)))) >= min_p;
-          len = block_prefix(c, sh.red, &b);
-          if (len == 0) len = 1;
-        }
-        const int kind = step == 1 ? BY_MASS : step == 3 ? BY_MASS_OVER : BY_COUNT;
-        const double target = step == 1 ? p * S : u * S;
-        j = pick_in_list<T>(sh, n, sc, kind, len, target, 0.0, 0, &m);
-        // p is a share of the first k's mass, which step 0 left in S
-        S = step == 0 ? m : step == 3 ? S : fmin(S, m);
-      }
-      if (tid == 0) {
-        const uint64_t c = sh.cand[j];
-        a.ids[r] = (int32_t)unpack_id(c);
-        if (a.logp) a.logp[r] = (float)log(mass_of(sh.red, sc.y(Key<T>::value((uint32_t)(c >> 32)))) / S);
-      }
+      if (tid < 64) draw_from_list<T>(a, r, sh, (int)(held < k ? held : k), sc, how);
       return;
     }
     __syncthreads();
