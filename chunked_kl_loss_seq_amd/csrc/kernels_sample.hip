@@ -283,7 +283,15 @@ __device__ inline double mass_of(const Red& red, double y) {
   return bin_top(red, (int)b) * __builtin_fma(r, f, 1.0);
 }
 
+// A row's settings; in LDS, where they take no registers through the passes.
+struct Settings {
+  double T, p, min_p, u;
+  double c;  // 64 log2(e) / T
+  bool limit;
+  uint32_t k;
+};
 struct Shared {
+  Settings how;
   uint64_t mass[kBins];       // integer masses relative to each bin's upper edge, then (fp64) masses
   uint32_t count[kBins];      // tokens per bin (kept while k limits)
   uint64_t cand[kCap];        // collected (key, id)
@@ -638,7 +646,7 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
     if (tid == 0) sh.pick = sh.n_cand;
     __syncthreads();
   }
-  const int bin = (int)sh.pick;
+  const int bin = (int)uniform(sh.pick);
   if (bin / kPerThread == tid) {
     double r = before;
     uint32_t c = cbefore;
@@ -653,9 +661,9 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
     sh.pick_count = c;
   }
   __syncthreads();
-  double above = sh.pick_mass;
-  uint32_t above_n = sh.pick_count;
-  const double top = bin_top(sh.red, bin);
+  double above = uniform(sh.pick_mass);
+  uint32_t above_n = uniform(sh.pick_count);
+  const double top = uniform(bin_top(sh.red, bin));
   const float p0 = (float)bin, p1 = (float)(bin + 1);
   // 2. the bin's tokens, narrowed by key digits until they fit
   uint32_t prefix = 0, prefix_mask = 0;
@@ -677,7 +685,7 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
       });
     });
     __syncthreads();
-    const uint32_t n = sh.n_cand;
+    const uint32_t n = uniform(sh.n_cand);
     if (n <= (uint32_t)kCap) {
       sort_cand(sh, (int)n);
       double mass = 0.0;
@@ -723,14 +731,14 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
     min_of_hits(dc && reached(kind, above_n + cb + dc, above + db + dm, k, target), (uint32_t)tid, &sh.pick);
     max_of_hits(dc != 0, (uint32_t)tid, &sh.n_cand);
     __syncthreads();
-    const uint32_t dg = sh.pick == 0xFFFFFFFFu ? sh.n_cand : sh.pick;
+    const uint32_t dg = uniform(sh.pick == 0xFFFFFFFFu ? sh.n_cand : sh.pick);
     if ((uint32_t)tid == dg) {
       sh.pick_mass = above + db;
       sh.pick_count = above_n + cb;
     }
     __syncthreads();
-    above = sh.pick_mass;
-    above_n = sh.pick_count;
+    above = uniform(sh.pick_mass);
+    above_n = uniform(sh.pick_count);
     prefix |= (255u - dg) << digits_left;
     prefix_mask |= 255u << digits_left;
   }
@@ -786,13 +794,6 @@ struct Counted {
     const int s = t * kPer + i;
     return i < kPer ? s < kW ? cnt[kW - s] : cnt[kSign + 1 + s - kW] : cnt[0];
   }
-};
-// A row's settings; in LDS, where they take no registers through the passes.
-struct Settings {
-  double T, p, min_p, u;
-  double c;  // 64 log2(e) / T
-  bool limit;
-  uint32_t k;
 };
 struct CountShared {
   Settings how;
@@ -1221,10 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   if (!a.direct && a.ids[r] != kLeft) return;
   const Row<T> row((const T*)a.x + r * a.ld, a.V);
 
-  const Settings how = row_settings(a, r);
-  const double p = how.p, min_p = how.min_p, u = how.u;
-  const bool limit = how.limit;
-  const uint32_t k = how.k;
+  if (tid == 0) sh.how = row_settings(a, r);
   fill_pow64(sh.red);  // read after the next barrier
 
   // 1. the largest logit, and each thread's
@@ -1232,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   for_each_chunk<8>(
       row, [&](const u32x4_t& v, uint32_t) { mv = fmaxf(mv, Row<T>::largest(v)); },
       [&](T l, int64_t) { mv = fmaxf(mv, (float)l); });
-  const float mx = block_max(mv, sh.red);
+  const float mx = uniform(block_max(mv, sh.red));
   if (mx == -INFINITY) {  // nothing to sample
     if (tid == 0) {
       a.ids[r] = -1;
@@ -1240,8 +1238,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     }
     return;
   }
+  const Settings& how = sh.how;
+  const uint32_t k = uniform(how.k);
   Scale sc;
-  sc.set(mx, how.c, a.fix_bits);
+  sc.set(mx, uniform(how.c), a.fix_bits);
 
   // 2a. few tokens: those that reach the k-th largest of the threads' maxima
   if (a.direct && k <= (uint32_t)kFastK) {
@@ -1272,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
       }
     }
     __syncthreads();
-    const uint32_t t0 = sh.pick;
+    const uint32_t t0 = uniform(sh.pick);
     const float v0 = t0 <= Key<T>::of(-INFINITY) ? -INFINITY : Key<T>::value(t0);
     auto hold = [&](float l, int64_t id) {
       if (l >= v0 && l > -INFINITY) {
@@ -1293,7 +1293,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
           },
           [&](T l, int64_t id) { hold((float)l, id); });
     __syncthreads();
-    const uint32_t held = sh.n_cand;
+    const uint32_t held = uniform(sh.n_cand);
     if (held <= (uint32_t)kCap) {
       sort_cand(sh, (int)held);
       if (tid < 64) draw_from_list<T>(a, r, sh, (int)(held < k ? held : k), sc, how);
@@ -1311,6 +1311,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   __syncthreads();
   // min_p's border: y <= y_min; the share of its bin and of the two beside it
   // (a bin is only within 1e-3 of y) is summed on the side
+  const double p = uniform(how.p), min_p = uniform(how.min_p), u = uniform(how.u);
+  const bool limit = uniform((uint32_t)how.limit) != 0;
   const double y_min = min_p > 0.0 ? -64.0 * log2(min_p) : (double)INFINITY;
   const int bin_min = y_min < (double)kBins ? (int)y_min : 2 * kBins;
   sc.either([&](auto plain) {
@@ -1349,9 +1351,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
       else if (b < bin_min)
         likely += m;
     }
-    S = block_prefix(all, sh.red, &before);
+    S = uniform(block_prefix(all, sh.red, &before));
     if (limit) block_prefix(tokens, sh.red, &cbefore);
-    s_min = min_p > 0.0 ? block_prefix(likely, sh.red, &dummy) : S;
+    s_min = min_p > 0.0 ? uniform(block_prefix(likely, sh.red, &dummy)) : S;
   }
   Found f;
 #pragma unroll 1
@@ -1360,7 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
     f = find_border(row, sh, sc, kind, k, kind == BY_MASS ? p * S : u * S, before, cbefore,
                     kind == BY_MASS_OVER);
     if (kind == BY_MASS_OVER) break;
-    S = fmin(S, f.mass);
+    S = fmin(S, uniform(f.mass));
     kind = kind == BY_COUNT && p < 1.0 ? BY_MASS : BY_MASS_OVER;
   }
   if (tid == 0) {
