@@ -686,6 +686,11 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
     });
     __syncthreads();
     const uint32_t n = uniform(sh.n_cand);
+    if (n == 1) {  // the usual case of a short row
+      const uint64_t c = sh.cand[0];
+      const float l = uniform(Key<T>::value((uint32_t)(c >> 32)));
+      return Found{above + mass_of(sh.red, sc.y(l)), l, (int64_t)unpack_id(c)};
+    }
     if (n <= (uint32_t)kCap) {
       sort_cand(sh, (int)n);
       double mass = 0.0;
