@@ -15,16 +15,17 @@
 //
 // The floor is reading a row once.  One workgroup of 1024 threads takes a row:
 //  1. bf16 rows (count_kernel): a count of every value, one LDS add per logit,
-//     from which all borders follow; then the row is read again from its start
-//     up to the drawn token, which is the n-th logit of its value.  N <= 64
+//     from which all borders follow; then the drawn token, the n-th logit of
+//     its value, is looked for in the third of the row that holds it.  N <= 64
 //     rows of 32,768 logits and more are counted by several workgroups each
 //     (count_slice_kernel, count_finish_kernel).
 //  2. The general path (sample_kernel): fp32 rows, bf16 rows that counting
-//     leaves (logits beyond +-256 that matter, and the like), and bf16 rows of
-//     which few tokens are wanted (direct_bf16).  First the largest logit, then
+//     leaves (logits beyond +-256 that matter, and the like), and a few bf16
+//     rows of which few tokens are wanted (direct_bf16).  First the largest
+//     logit, then
 //   a. 1 <= k <= 512: the k-th largest of the threads' maxima is a bound that
 //     at least k tokens reach; the tokens that do are collected, sorted in LDS,
-//     and everything else happens there;
+//     and one wave does everything else there;
 //   b. otherwise a histogram of the row's mass over 4096 bins, 1/64 octave of
 //     e each (64 octaves: what lies below weighs less than 2^-64 a token).
 //     Within a bin the masses e / (upper edge) lie in (2^-1/64, 1], so a short
@@ -36,14 +37,15 @@
 //     its rank in id order.
 //
 // Measured (MI355X):
-//  1,024 x 201,088 bf16, no limit: 149 us, 2.8 TB/s of the logits.  Counting is
-//    bound by the LDS (an add per logit: 117 us without the second read, against
-//    75 us for the bytes); by the histogram of 2b the same took 890 us.
-//  512 x 128,256 bf16, top-p: 59 us, 2.2 TB/s (two rounds of workgroups).
-//  64 x 32,000 bf16, top-k 50: 13 us by 2a (20 us by counting); fp32 top-p 29 us.
-//  1 x 201,088 bf16, top-k 50: 22 us by 2a, 28 us by counting in slices, 33 us
-//    by one counting workgroup: latency, a row is read by few compute units.
-//  1,024 x 201,088 fp32, no limit: 459 us, 1.8 TB/s, bound by the 64-bit LDS
+//  1,024 x 201,088 bf16, no limit: 100 us, 4.1 TB/s of the logits (80 us for
+//    the counting, the rest what follows a workgroup's last load; by the
+//    histogram of 2b 890 us).
+//  512 x 128,256 bf16, top-p: 42 us, 3.1 TB/s.
+//  1 x 201,088 bf16, top-k 50: 18 us, latency: one compute unit reads the row.
+//  61 x 32,000 fp32, limits of each row's own: 29 us, the rows without a top-k
+//    in 2b, half of it fp64 arithmetic on the row's one compute unit (with
+//    top-k 200: 16 us by 2a).
+//  1,024 x 201,088 fp32, no limit: 440 us, 1.9 TB/s, bound by the 64-bit LDS
 //    adds of 2b and the fp64 polynomial.
 #include <hip/hip_runtime.h>
 
@@ -1379,20 +1381,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
 }  // namespace
 
 namespace {
-// Whether bf16 rows go to the general path at once.  Counting clears and scans
-// about 8,700 counts a row, which short rows do not repay, and where every row
-// takes at most kFastK tokens the collected path reads the row at least as
-// fast: with k = 50 a row of 201,088 logits 22 us against 28, 64 x 32,000 13
-// against 20 (1,024 x 201,088: 157 against 147, the price of a simple rule).
+// Whether bf16 rows go to the general path at once: where each takes at most
+// 128 tokens, its collected path needs less than counting's scan of 8,192
+// counts, as long as no compute unit has a second row.  In us, that path and
+// counting:
+//   top_k     1 x 201,088   64 x 32,000   256 x 201,088   512 x 201,088
+//     1          13   22        8   15         28   34         53   57
+//   100          21   22       13   15         36   34         71   57
+//   250          26   22       18   15         46   34         89   57
 // A limit of each row's own cannot be read here.
-bool direct_bf16(int64_t V, const SampleParams& p) {
-  const bool few = !p.top_ks && !p.temperatures && ((p.top_k > 0 && p.top_k <= kFastK) || p.temperature == 0.0);
-  return V <= 4096 || few;
+constexpr int64_t kDirectK = 128, kDirectRows = 256;
+bool direct_bf16(int64_t N, const SampleParams& p) {
+  const bool few = !p.top_ks && !p.temperatures && ((p.top_k > 0 && p.top_k <= kDirectK) || p.temperature == 0.0);
+  return few && N <= kDirectRows;
 }
 
 // Workgroups per bf16 row: more than one for few rows (at most a quarter of
-// the 256 compute units busy) of at least 2 x 16,384 logits.  One row of
-// 201,088 logits takes 28 us so, 33 us by one workgroup.
+// the 256 compute units busy) of at least 2 x 16,384 logits.  With top-p, one row
+// of 201,088 logits takes 21 us so, 25 us by one workgroup; 64 rows 24 and 28.
 int slices_of(Dtype dt, int64_t N, int64_t V) {
   if (dt != DT_BF16 || N > 64) return 1;
   int64_t s = V / 16384;
@@ -1419,7 +1425,7 @@ hipError_t launch_sample(Dtype dt, const void* x, int64_t N, int64_t V, int64_t 
   a.fix_bits = 62 - lg < 51 ? 62 - lg : 51;  // V masses of at most 2^fix_bits stay below 2^63
   a.ids = ids;
   a.logp = logp;
-  a.direct = dt != DT_BF16 || direct_bf16(V, p);
+  a.direct = dt != DT_BF16 || direct_bf16(N, p);
   if (!a.direct) {
     a.slices = ws != nullptr ? slices_of(dt, N, V) : 1;
     hipError_t e;
