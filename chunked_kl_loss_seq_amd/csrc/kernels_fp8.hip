@@ -27,14 +27,15 @@
 // one register and its results are adjacent in memory.
 //
 //   * M <= 16 and a short weight (too few tiles to fill the chip), or M <= 2 and a
-//     very long one.  Weight rows
-//     go straight from memory to registers, no LDS; four waves share 32 rows,
-//     each taking a quarter of the k blocks, and add their sums through LDS.
+//     very long one.  Weight rows go straight from memory to registers, no LDS;
+//     four waves share 32 rows, each taking a quarter of the k blocks, and add
+//     their sums through LDS.  1 x 201,088 x 2,880: 105 us, 5.5 TB/s, the rate
+//     of reading the weight.
 //   * else tiles staged through a two-stage LDS ring by LDS DMA, one barrier
 //     per block of k, of the size that is expected to end first.  Up to about
 //     128 rows this is bound by reading the weight (16 x 201,088 x 2,880: 121 us,
 //     4.8 TB/s), beyond by the board's power: 2,048 x 201,088 x 2,880 takes
-//     1,277 us (1,860 TFLOP/s) with the matrix cores busy 39 % of the cycles at
+//     1,256 us (1,888 TFLOP/s) with the matrix cores busy 39 % of the cycles at
 //     1.77 GHz; loading the next block's fragments across the barrier made them
 //     busy 48 % of the cycles, at 1.56 GHz, in the same time.
 #include "gemm_core.hpp"
@@ -299,10 +300,10 @@ __device__ inline void dma4(const i32x4& rsrc, uint32_t voff, uint32_t lds_addr)
 // Copies R rows x 128 bytes (one block of k) of an operand into LDS, laid out
 // as KTile.  One instruction of a wave fills 8 rows; a wave's next one lies
 // NW x 8 rows on, a multiple of the swizzle's period, so one lane offset serves
-// all and the rows' distance is added to it (not put into the instruction's
-// scalar offset, which the range check need not cover).  Rows past the operand
-// lie past the resource's end, k past d only on the last block: both read as
-// zeros.
+// all and the resource moves on by the rows' distance (2,048 x 201,088 x 2,880
+// 1,256 us; added to the lane offset 1,316; the instruction's scalar offset
+// will not do, as the range check need not cover it).  Rows past the operand lie
+// past the resource's end, k past d only on the last block: both read as zeros.
 template <int R, int NW>
 struct BlockDMA {
   static constexpr int kBytes = R * kBlk;
@@ -323,12 +324,18 @@ struct BlockDMA {
     return (lane & 7) ^ ((row >> 1) & 7);
   }
   __device__ inline void issue(int64_t k0, int64_t d, uint32_t lds, int wave, int lane) const {
-    i32x4 rs = make_rsrc((const void*)(org + (uint64_t)k0));
-    rs.z = (int32_t)(rows * (uint32_t)d - (uint32_t)k0);
+    uint64_t at = org + (uint64_t)k0;
+    int32_t left = (int32_t)(rows * (uint32_t)d - (uint32_t)k0);
     uint32_t v = voff;
     if (d - k0 < kBlk && chunk(wave, lane) * 16 >= (int)(d - k0)) v = kOOB;
 #pragma unroll
-    for (int i = 0; i < kNI; ++i) dma16(rs, v + (uint32_t)i * step, lds + (uint32_t)((i * NW + wave) * 1024));
+    for (int i = 0; i < kNI; ++i) {
+      i32x4 rs = make_rsrc((const void*)at);
+      rs.z = left > 0 ? left : 0;
+      dma16(rs, v, lds + (uint32_t)((i * NW + wave) * 1024));
+      at += step;
+      left -= (int32_t)step;
+    }
   }
 };
 
