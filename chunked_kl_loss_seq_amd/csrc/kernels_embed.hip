@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
 // of the row (512 bf16 or 256 fp32 columns).  part[2 t] holds tile t's piece
 // of the run that came in from tile t - 1, part[2 t + 1] its piece of the run
 // that goes on into tile t + 1 (a tile inside one run has the first only).
+constexpr int kTileMax = 64;
 struct RunArgs {
   const uint32_t* skey;
   const uint32_t* spos;
@@ -376,16 +377,14 @@ __device__ inline bool occurs(const uint32_t* skey, int64_t N, uint32_t v) {
 // Zeros in the rows of absent tokens among the kZeroRows of block b (of n),
 // by all waves of the workgroup.  The blocks of one XCD (b % 8) take adjacent
 // words (1.4 % less time at 201,088 x 2,880 than words in block order).
-__device__ inline void zero_rows(const RunArgs& a, int64_t word0, int64_t n, int64_t b) {
+// present(word): a bit per token of the word that occurs.
+template <typename P>
+__device__ inline void zero_rows(const RunArgs& a, int64_t word0, int64_t n, int64_t b, P&& present_in) {
   const int64_t per = (n + 7) / 8, at = (b & 7) * per + (b >> 3);
   if ((b >> 3) >= per || at >= n) return;
   const int64_t word = word0 + at, v0 = word * kZeroRows;
   const int lane = threadIdx.x & 63, waves = blockDim.x / 64;
-  uint32_t present;
-  if (a.bits != nullptr)
-    present = a.bits[word];
-  else
-    present = (uint32_t)__ballot(lane < kZeroRows && occurs(a.skey, a.N, (uint32_t)(v0 + lane)));
+  const uint32_t present = present_in(word);
   const int64_t cols4 = a.d / 4;
   for (int r = threadIdx.x >> 6; r < kZeroRows; r += waves) {
     if (v0 + r >= a.V || ((present >> r) & 1u)) continue;
@@ -393,8 +392,89 @@ __device__ inline void zero_rows(const RunArgs& a, int64_t word0, int64_t n, int
     for (int64_t c = lane; c < cols4; c += 64) dst[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 }
+__device__ inline void zero_rows(const RunArgs& a, int64_t word0, int64_t n, int64_t b) {
+  zero_rows(a, word0, n, b, [&](int64_t word) {
+    const int lane = threadIdx.x & 63;
+    return a.bits != nullptr
+               ? a.bits[word]
+               : (uint32_t)__ballot(lane < kZeroRows && occurs(a.skey, a.N, (uint32_t)(word * kZeroRows + lane)));
+  });
+}
 // Blocks for n words: a whole number for each XCD.
 inline int64_t zero_blocks(int64_t n) { return (n + 7) / 8 * 8; }
+
+// At most kFewMax positions: one launch without a sort.  The workgroup of a
+// position (and slice) whose id does not occur before it sums the rows of all
+// its occurrences: a wave those among 64 positions in order, wave 0 then the
+// waves' sums in order.
+constexpr int kFewMax = 256;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) few_sum_kernel(RunArgs a, const int32_t* __restrict__ ids,
+                                                           const T* __restrict__ dY) {
+  constexpr int kN = Chunk<T>::kN;
+  static_assert(kFewMax == kThreads, "a key per thread");
+  __shared__ uint32_t keys[kFewMax];
+  __shared__ float sums[kThreads / 64][64 * kN];
+  const int lane = threadIdx.x & 63, N = (int)a.N;
+  keys[threadIdx.x] = (int)threadIdx.x < N ? key_of(ids, threadIdx.x, a.V) : a.V;
+  __syncthreads();
+  if ((int64_t)blockIdx.x >= a.sum_blocks) {
+    zero_rows(a, 0, a.zero_words, (int64_t)blockIdx.x - a.sum_blocks, [&](int64_t word) {
+      uint32_t m = 0;
+      for (int i = lane; i < N; i += 64) {
+        const uint32_t at = keys[i] - (uint32_t)(word * kZeroRows);
+        m |= at < (uint32_t)kZeroRows ? 1u << at : 0u;
+      }
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) m |= __shfl_xor(m, o);
+      return m;
+    });
+    return;
+  }
+  const int i = (int)(blockIdx.x / a.slices), slice = (int)(blockIdx.x - i * a.slices);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t key = __builtin_amdgcn_readfirstlane(keys[i]);
+  if (key >= a.V) return;
+  for (int b = 0; b <= i; b += 64) {
+    const uint64_t before = i - b < 64 ? (1ull << (i - b)) - 1 : ~0ull;
+    if (__ballot(keys[b + lane] == key) & before) return;  // that position's workgroup sums it
+  }
+  const int c = slice * 64 + lane, cl = c < a.cpr ? c : a.cpr - 1;
+  float acc[kN];
+#pragma unroll
+  for (int q = 0; q < kN; ++q) acc[q] = 0.f;
+  const u32x4_t* src = (const u32x4_t*)dY;
+  constexpr int U = 16;  // rows in flight
+  uint64_t m = __ballot(keys[64 * w + lane] == key);
+  while (m) {
+    u32x4_t v[U];
+    const int n = __popcll(m);
+    int p = 0;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      p = m ? 64 * w + __builtin_ctzll(m) : p;
+      m &= m - 1;
+      v[j] = src[(int64_t)p * a.cpr + cl];
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) asm volatile("" : "+v"(v[j]));  // none is put off to its use
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float f[kN];
+      Chunk<T>::unpack(v[j], f);
+#pragma unroll
+      for (int q = 0; q < kN; ++q) acc[q] += j < n ? f[q] : 0.f;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kN; ++q) sums[w][q * 64 + lane] = acc[q];
+  __syncthreads();
+  if (w > 0 || c >= a.cpr) return;
+  for (int j = 1; j < kThreads / 64; ++j)
+#pragma unroll
+    for (int q = 0; q < kN; ++q) acc[q] += sums[j][q * 64 + lane];
+  store_row<kN>(a.dW + (int64_t)key * a.d + (int64_t)c * kN, acc, a.scale, a.accumulate != 0);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* __restrict__ dY, int groups) {
@@ -417,7 +497,11 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* _
   const int64_t b = t * a.tlen, e = b + a.tlen < a.N ? b + a.tlen : a.N;
   const uint32_t before = b > 0 ? a.skey[b - 1] : 0xFFFFFFFFu;
   const uint32_t after = e < a.N ? a.skey[e] : 0xFFFFFFFFu;
-  uint32_t cur = a.skey[b];
+  // the tile's keys and positions, one a lane: read here at once, later by lane
+  static_assert(kTileMax <= 64, "a lane per position of a tile");
+  const int64_t mine = b + lane < e ? b + lane : e - 1;
+  const uint32_t keys = a.skey[mine], places = a.spos[mine];
+  uint32_t cur = __builtin_amdgcn_readlane(keys, 0);
   if (cur >= a.V) return;  // only positions without a token from here on
   const bool head = cur == before;
   bool first = true;  // the current run is the tile's first
@@ -443,11 +527,13 @@ __global__ void __launch_bounds__(kThreads) run_sum_kernel(RunArgs a, const T* _
     uint32_t k[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int64_t i = i0 + j < e ? i0 + j : e - 1;
-      k[j] = __builtin_amdgcn_readfirstlane(a.skey[i]);
-      const uint32_t p = __builtin_amdgcn_readfirstlane(a.spos[i]);
+      const int i = (int)((i0 + j < e ? i0 + j : e - 1) - b);
+      k[j] = __builtin_amdgcn_readlane(keys, i);
+      const uint32_t p = __builtin_amdgcn_readlane(places, i);
       v[j] = src[(int64_t)p * a.cpr + cl];
     }
+#pragma unroll
+    for (int j = 0; j < U; ++j) asm volatile("" : "+v"(v[j]));  // none is put off to its use
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (i0 + j >= e) break;
@@ -534,7 +620,7 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Sorted positions per tile: short tiles while there are few positions (more
 // waves in flight), long ones later (fewer partial rows).
-inline int tile_len(int64_t N) { return N <= 8192 ? 16 : N <= 16384 ? 32 : 64; }
+inline int tile_len(int64_t N) { return N <= 8192 ? 16 : N <= 16384 ? 32 : kTileMax; }
 
 struct BwdLayout {
   int64_t tiles = 0, sort_tiles = 0;
@@ -567,10 +653,16 @@ BwdLayout bwd_layout(int64_t N, int64_t d, int64_t V) {
 }
 
 template <typename T>
-hipError_t launch_runs(RunArgs a, const void* dY, hipStream_t s) {
+hipError_t launch_runs(RunArgs a, const int32_t* ids, const void* dY, hipStream_t s) {
   constexpr int kN = Chunk<T>::kN;
   a.cpr = (int)(a.d / kN);
   a.slices = (int)cdiv(a.cpr, 64);
+  if (a.N <= kFewMax) {
+    a.sum_blocks = a.N * a.slices;
+    hipLaunchKernelGGL(few_sum_kernel<T>, dim3((unsigned)(a.sum_blocks + zero_blocks(a.zero_words))), dim3(kThreads), 0,
+                       s, a, ids, (const T*)dY);
+    return hipGetLastError();
+  }
   const int groups = (int)cdiv(a.slices, kThreads / 64);
   a.sum_blocks = a.tiles * groups;
   a.join_blocks = (a.tiles - 1) * a.slices;
@@ -622,7 +714,9 @@ hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float 
   hipError_t e = hipSuccess;
 #define EMBED_TRY()                            \
   if ((e = hipGetLastError()) != hipSuccess) return e
-  if (L.passes == 0) {
+  if (N <= kFewMax) {
+    // no sort
+  } else if (L.passes == 0) {
     hipLaunchKernelGGL(rank_kernel, dim3((unsigned)cdiv(N, kThreads / kRankLanes)), dim3(kThreads), 0, s, ids, (int)N,
                        (uint32_t)V, skey, spos);
     EMBED_TRY();
@@ -669,7 +763,7 @@ hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float 
   a.part = (float*)(base + L.part);
   a.bits = bits;
   a.zero_words = accumulate ? 0 : cdiv(V, kZeroRows);
-  return dt == DT_BF16 ? launch_runs<__bf16>(a, dY, s) : launch_runs<float>(a, dY, s);
+  return dt == DT_BF16 ? launch_runs<__bf16>(a, ids, dY, s) : launch_runs<float>(a, ids, dY, s);
 }
 
 }  // namespace ckl

@@ -115,6 +115,14 @@ def test_gradient(ckl, dtype, kind, N, V, d):
     assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("kind", ["text", "uniform", "one", "none"])
+@pytest.mark.parametrize("N,V,d", [(63, 64, 520), (64, 10, 8), (65, 1000, 24), (255, 33, 1032), (256, 97, 256), (257, 97, 256)])
+def test_gradient_of_few_positions(ckl, kind, N, V, d):
+    # up to 256 positions take one launch: occurrences in each group of 64
+    # positions, more than 16 of them in one, and the first count past it
+    test_gradient(ckl, "bf16" if N % 2 else "f32", kind, N, V, d)
+
+
 @pytest.mark.parametrize("N,V", [(70001, 400000), (20000, 262143), (20000, 262144), (9000, 1 << 20)])
 def test_gradient_of_large_vocabularies(ckl, N, V):
     # keys of 18 bits and more: two and three radix passes; 70,001 positions: tiles of 64
