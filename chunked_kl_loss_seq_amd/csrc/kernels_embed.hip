@@ -18,6 +18,15 @@
 // a second kernel.  Rows without a token are written as zeros by other
 // workgroups of the same launches, so every byte of dW is written once; those
 // zeros bound the call for large vocabularies.
+//
+// Measured (MI355X, bf16):
+//  lookup of 32,768 x 2,880: 52 us, 7.3 TB/s of rows read and written (repeated
+//    rows come from the caches); of 4 x 2,880: 2 us on the device.
+//  gradient of 32,768 x 2,880 of 201,088: 515-525 us, 4.9 TB/s (dY read, dW
+//    written); the zeros alone, as a plain fill of dW, take 433 us (5.35 TB/s; a
+//    fill of 1 GiB reaches 6.9).
+//  gradient of 4,096 x 2,048 of 32,000: 60 us, 4.7 TB/s, of which rank 12, sum 32
+//    with most of the zeros, join 15 with the rest.
 #include <hip/hip_runtime.h>
 
 #include "launch.hpp"
@@ -195,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) sort_hist_kernel(const int32_t* __re
   __shared__ uint32_t h[kDigits];
   for (int i = threadIdx.x; i < kDigits; i += kThreads) h[i] = 0;
   if (bits != nullptr)
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (int64_t)tiles * kThreads) bits[i] = 0;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (int64_t)tiles * kThreads)
+      bits[i] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * kSortTile;
 #pragma unroll
@@ -285,7 +295,8 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
       same &= ((dg >> b) & 1u) ? m : ~m;
     }
     // the lanes of `same` hold this digit; earlier ones come first
-    const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+    const uint32_t before =
+        __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
     const uint32_t old = in ? cnt[w][dg] : 0;
     rank[r] = old + before;
     // one lane per digit moves the wave's counter on (LDS operations of one
@@ -406,7 +417,9 @@ inline int64_t zero_blocks(int64_t n) { return (n + 7) / 8 * 8; }
 // At most kFewMax positions: one launch without a sort.  The workgroup of a
 // position (and slice) whose id does not occur before it sums the rows of all
 // its occurrences: a wave those among 64 positions in order, wave 0 then the
-// waves' sums in order.
+// waves' sums in order.  Against rank, sum and join, 256 positions take 6 us for
+// 12 at 4,096 x 256 fp32 and 35 for 43 at 32,000 x 2,048 bf16 (the same token
+// 256 times: 6 for 11 and 36 for 42).
 constexpr int kFewMax = 256;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) few_sum_kernel(RunArgs a, const int32_t* __restrict__ ids,

@@ -144,8 +144,9 @@ __device__ inline void store8(uint8_t* q, const float* f, float s) {
 // Blocks of 1 x 128: 16 lanes per block, 8 values a lane.
 constexpr int kQThreads = 256;
 template <typename T>
-__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ x, int64_t R, int64_t C, int kb_n,
-                                                                 uint8_t* __restrict__ q, float* __restrict__ scales) {
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ x, int64_t R, int64_t C,
+                                                                 int kb_n, uint8_t* __restrict__ q,
+                                                                 float* __restrict__ scales) {
   const int64_t g = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);  // block index
   const int l = threadIdx.x & 15;
   if (g >= R * kb_n) return;  // whole groups of 16 lanes: the shuffles below stay within one
@@ -362,7 +363,8 @@ struct Frag8<float> {
 };
 
 template <typename TO, int BM, int BN, int WM>
-__global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2))) fp8_tile_kernel(Fp8Args p, GemmParams g) {
+__global__ void __launch_bounds__(WM* BN) __attribute__((amdgpu_waves_per_eu(2)))
+fp8_tile_kernel(Fp8Args p, GemmParams g) {
   constexpr int WN = BN / 64, NW = WM * WN, WTM = BM / WM, FM = WTM / 16, FN = 4;
   typedef BlockDMA<BM, NW> DA;
   typedef BlockDMA<BN, NW> DB;
@@ -546,14 +548,15 @@ hipError_t launch_tiles(const Fp8Args& p, hipStream_t s) {
 // 256 units together finish 256 tiles per `full` microseconds of each block
 // where there are many (bf16 results; fp32 results take about 1.6 times as long
 // for every tile).  Measured, in us (256 x 256, 128 x 128, 128 x 64, 64 x 64):
-//   2,048 x 201,088 x 2,880: 1,277 1,499 - -    300 x 100,000 x 512: 44 35 35 44
+//   2,048 x 201,088 x 2,880: 1,256 1,499 - -    300 x 100,000 x 512: 44 35 35 44
 //   128 x 201,088 x 2,880: 224 163 - -          1,000 x 5,000 x 1,024: 20 14 14 15
 //   256 x 32,000 x 2,048: 33 23 29 34           40 x 5,000 x 4,096: 49 23 18 15
 struct TileCost {
   int bm, bn;
   double alone, full;
 };
-constexpr TileCost kTileCosts[] = {{256, 256, 1.5, 2.26}, {128, 128, 0.90, 0.66}, {128, 64, 0.57, 0.44}, {64, 64, 0.48, 0.28}};
+constexpr TileCost kTileCosts[] = {
+    {256, 256, 1.5, 2.26}, {128, 128, 0.90, 0.66}, {128, 64, 0.57, 0.44}, {64, 64, 0.48, 0.28}};
 
 template <typename TO>
 hipError_t launch_product(const Fp8Args& p, hipStream_t s) {
@@ -596,9 +599,11 @@ hipError_t launch_quantize_fp8(Dtype dt, const void* x, int64_t R, int64_t C, bo
     const int64_t groups = R * kb, per = kQThreads / 16;
     const dim3 grid((unsigned)((groups + per - 1) / per));
     if (dt == DT_BF16)
-      hipLaunchKernelGGL(quantize_rows_kernel<__bf16>, grid, dim3(kQThreads), 0, s, (const __bf16*)x, R, C, kb, q, scales);
+      hipLaunchKernelGGL(quantize_rows_kernel<__bf16>, grid, dim3(kQThreads), 0, s, (const __bf16*)x, R, C, kb, q,
+                         scales);
     else
-      hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, dim3(kQThreads), 0, s, (const float*)x, R, C, kb, q, scales);
+      hipLaunchKernelGGL(quantize_rows_kernel<float>, grid, dim3(kQThreads), 0, s, (const float*)x, R, C, kb, q,
+                         scales);
   } else {
     const dim3 grid((unsigned)((R + kBlk - 1) / kBlk * kb));
     if (dt == DT_BF16)
