@@ -523,10 +523,13 @@ __device__ __forceinline__ int64_t nth_equal(const Row<T>& row, uint32_t* room, 
     for (; n > 1; --n) m &= m - 1;
     return __builtin_ctzll(m);
   };
-  const int ilane = (int)lane;
-  const uint64_t head = row.head == 0 ? 0 : __ballot(ilane < row.head && (float)row.x[ilane < row.head ? ilane : 0] == l);
-  const uint64_t tail =
-      row.tail == 0 ? 0 : __ballot(ilane < row.tail && (float)row.x[row.tail_id() + (ilane < row.tail ? ilane : 0)] == l);
+  // the lanes whose element of the n at `first` equals l
+  auto equal_at = [&](int64_t first, int n) -> uint64_t {
+    if (n == 0) return 0;
+    const bool in = (int)lane < n;
+    return __ballot(in && (float)row.x[first + (in ? (int)lane : 0)] == l);
+  };
+  const uint64_t head = equal_at(0, row.head), tail = equal_at(row.tail_id(), row.tail);
   const uint32_t nh = (uint32_t)__popcll(head), in_body = n - nh - (uint32_t)__popcll(tail);
   if (r <= nh) return nth_lane(head, r);
   r -= nh;
