@@ -874,10 +874,11 @@ __device__ inline void count_row(const Row<__bf16>& row, uint32_t* cnt, const Th
       });
 }
 
-// Whether the row holds a nonzero logit below 2^-26 in magnitude.
+// Whether the row holds a nonzero logit that is counted as 0.
 __device__ inline bool has_tiny(const Row<__bf16>& row) {
+  const float least = __builtin_bit_cast(float, (uint32_t)Counted::kLo << 16);  // 2^-24
   bool tiny = false;
-  for_each(row, [&](float l, int64_t) { tiny |= l != 0.f && fabsf(l) < 0x1p-26f; });
+  for_each(row, [&](float l, int64_t) { tiny |= l != 0.f && fabsf(l) < least; });
   return __syncthreads_or(tiny);
 }
 

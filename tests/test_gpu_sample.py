@@ -266,6 +266,20 @@ def test_same_bits_every_time_and_on_two_streams(ckl):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+@pytest.mark.parametrize("V", [1, 2, 3, 40, 5003])
+def test_logits_about_zero(ckl, V):
+    # every binary magnitude from 2^-30 to 2^-20 of either sign beside 0: where
+    # the counts of bf16 values stop telling them apart
+    g = torch.Generator().manual_seed(V)
+    for N in (7, 80):
+        e = torch.randint(-30, -19, (N, V), generator=g).double()
+        x = torch.randint(-1, 2, (N, V), generator=g) * 2.0 ** e * (1 + torch.randint(0, 128, (N, V), generator=g) / 128)
+        for r in range(0, N, 3):
+            x[r] = x[r].abs().clamp(min=2.0 ** -30)  # no zero among them
+        for how in ({}, {"temperature": 0.4}, {"top_p": 0.7}, {"top_k": 600, "min_p": 0.1}):
+            check(ckl, x.float().to("cuda:0").bfloat16(), uniforms(N, V), **how)
+
+
 @pytest.mark.parametrize("V", [5003, 24577, 30001, 100003, 262143, 262144])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_which_of_equal_logits(ckl, V, dtype):
