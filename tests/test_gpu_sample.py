@@ -312,6 +312,40 @@ def test_which_of_equal_logits(ckl, V, dtype):
     assert ids.tolist() == want
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_seeded_sweep(ckl, seed):
+    # random sizes, row distances, distributions and settings, some per row
+    g = torch.Generator().manual_seed(1000 + seed)
+
+    def rand(lo, hi):
+        return lo + (hi - lo) * torch.rand(1, generator=g).item()
+
+    N = (1, 7, 66, 80)[seed % 4]
+    V = int(2 ** rand(0, 16 if N < 60 else 14))
+    x = torch.randn(N, V + seed % 5, generator=g) * rand(0.5, 8)
+    shape = seed % 6
+    if shape == 1:  # a grid of values
+        x = (x * 2).round() / 2
+    elif shape == 2:  # zeros of either sign
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.5, torch.zeros(()), x) * torch.sign(x)
+    elif shape == 3:  # mostly masked
+        x[torch.rand(x.shape, generator=g) < 0.95] = -float("inf")
+    elif shape == 4:  # beyond +-256
+        x *= 40
+    elif shape == 5:  # tiny ones beside others
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.3, x * 1e-8, x * 0.01)
+    how = {}
+    for name, hi, as_type in (("temperature", 2.0, torch.float32), ("top_k", 900.0, torch.int32),
+                              ("top_p", 1.0, torch.float32), ("min_p", 0.2, torch.float32)):
+        turn = rand(0, 3)
+        if turn < 1:
+            how[name] = (torch.rand(N, generator=g) * hi).to(as_type).to("cuda:0")
+        elif turn < 2:
+            how[name] = int(rand(0, hi)) if as_type == torch.int32 else rand(0.05, hi)
+    for dtype in ("bf16", "f32"):
+        check(ckl, x.to("cuda:0").to(DT[dtype])[:, :V], uniforms(N, seed), **how)
+
+
 def test_captured_and_replayed(ckl):
     x, u = rows(40, 9000, "bf16"), uniforms(40)
     s = torch.cuda.Stream()
