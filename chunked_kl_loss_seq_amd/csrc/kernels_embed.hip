@@ -25,7 +25,7 @@
 //  gradient of 32,768 x 2,880 of 201,088: 515-525 us, 4.9 TB/s (dY read, dW
 //    written); the zeros alone, as a plain fill of dW, take 433 us (5.35 TB/s; a
 //    fill of 1 GiB reaches 6.9).
-//  gradient of 4,096 x 2,048 of 32,000: 60 us, 4.7 TB/s, of which rank 12, sum 32
+//  gradient of 4,096 x 2,048 of 32,000: 56 us, 5.0 TB/s, of which rank 8, sum 31
 //    with most of the zeros, join 15 with the rest.
 #include <hip/hip_runtime.h>
 
@@ -158,7 +158,17 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const int32_t* __restric
   for (int t0 = 0; t0 < N; t0 += kRankTile) {
     const int n = min(kRankTile, N - t0), n4 = (n + 3) & ~3;
     __syncthreads();
-    for (int j = threadIdx.x; j < n4; j += kThreads) tile[j] = j < n ? key_of(ids, t0 + j, V) : 0xFFFFFFFFu;
+    uint32_t k[kRankTile / kThreads];  // loaded together: one after the other they took most of the launch
+#pragma unroll
+    for (int q = 0; q < kRankTile / kThreads; ++q) {
+      const int j = q * kThreads + (int)threadIdx.x;
+      k[q] = key_of(ids, t0 + (j < n ? j : n - 1), V);
+    }
+#pragma unroll
+    for (int q = 0; q < kRankTile / kThreads; ++q) {
+      const int j = q * kThreads + (int)threadIdx.x;
+      tile[j] = j < n ? k[q] : 0xFFFFFFFFu;
+    }
     __syncthreads();
 #pragma unroll 8
     for (int j = 4 * part; j < n4; j += 4 * kRankLanes) {
@@ -207,12 +217,16 @@ __global__ void __launch_bounds__(kThreads) sort_hist_kernel(const int32_t* __re
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (int64_t)tiles * kThreads)
       bits[i] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kSortTile;
+  const int64_t base = (int64_t)blockIdx.x * kSortTile + threadIdx.x;
+  uint32_t key[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = base + r * kThreads + threadIdx.x;
-    if (i < N) atomicAdd(&h[(pass_key(ids, keys, i, V) >> shift) & (kDigits - 1)], 1u);
+    const int64_t i = base + r * kThreads;
+    key[r] = pass_key(ids, keys, i < N ? i : N - 1, V);
   }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    if (base + r * kThreads < N) atomicAdd(&h[(key[r] >> shift) & (kDigits - 1)], 1u);
   __syncthreads();
   for (int i = threadIdx.x; i < kDigits; i += kThreads) hist[(int64_t)blockIdx.x * kDigits + i] = h[i];
 }
@@ -256,11 +270,12 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
   for (int i = threadIdx.x; i < kSortWaves * kDigits; i += kThreads) (&cnt[0][0])[i] = 0;
   // wave w owns elements [64 kRounds w, 64 kRounds (w + 1)) of the tile, in order
   const int64_t base = (int64_t)blockIdx.x * kSortTile + (int64_t)w * 64 * kRounds;
-  uint32_t key[kRounds], rank[kRounds];
+  uint32_t key[kRounds], place[kRounds], rank[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = base + r * 64 + lane;
-    key[r] = i < N ? pass_key(ids, keys, i, V) : 0xFFFFFFFFu;
+    const int64_t i = base + r * 64 + lane < N ? base + r * 64 + lane : N - 1;
+    key[r] = pass_key(ids, keys, i, V);
+    place[r] = pos != nullptr ? pos[i] : (uint32_t)i;
   }
   // the places of this tile's digits 2 t and 2 t + 1
   const uint2* h = (const uint2*)hist;
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
     if (i < N) {
       const uint32_t at = cnt[w][(key[r] >> shift) & (kDigits - 1)] + rank[r];
       keys_out[at] = key[r];
-      pos_out[at] = pos != nullptr ? pos[i] : (uint32_t)i;
+      pos_out[at] = place[r];
       // the plain read spares a frequent token's word most of its atomics
       if (bits != nullptr && key[r] < V && ((bits[key[r] >> 5] >> (key[r] & 31)) & 1u) == 0)
         atomicOr(&bits[key[r] >> 5], 1u << (key[r] & 31));
