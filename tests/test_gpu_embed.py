@@ -197,17 +197,32 @@ def test_tied_weights_add_to_the_head_gradient(ckl):
     ckl.fused_kl(ckl.embedding(text, Wt, 8.0), Wt, ids, T).backward()
     both = head + ckl.embed_bwd(text, dH, 500, 8.0)
     assert torch.allclose(dW, both, rtol=2e-6, atol=1e-9) and torch.allclose(Wt.grad, both, rtol=2e-6, atol=1e-9)
-    # and it is the derivative of the loss: a step along a direction
+    # and it is the derivative of the loss: a step along a direction E
     E = torch.randn_like(W)
-    d = []
-    for s in (1e-3, -1e-3):
-        Ws = (W.double() + s * E.double())
-        z = (Ws[text.long()] * 8.0) @ Ws.t()
-        p = torch.softmax(T.double(), 1)
-        lp = torch.log_softmax(z, 1).gather(1, ids.long())
-        d.append(((p * (p.log() - lp)).sum(1)).mean().item())
-    slope = (d[0] - d[1]) / 2e-3
-    assert abs(slope - (dW.double() * E.double()).sum().item()) <= 1e-4 * abs(slope) + 1e-6
+
+    def difference(s):
+        d = []
+        for step in (s, -s):
+            Ws = (W.double() + step * E.double())
+            z = (Ws[text.long()] * 8.0) @ Ws.t()
+            p = torch.softmax(T.double(), 1)
+            lp = torch.log_softmax(z, 1).gather(1, ids.long())
+            d.append(((p * (p.log() - lp)).sum(1)).mean().item())
+        return (d[0] - d[1]) / (2 * s)
+
+    # A central difference is off by s^2 f3 / 6 + s^4 f5 / 120 + ..; two of them
+    # cancel the first term.  Along E a logit is z0 + a s + b s^2 with a of about 8
+    # x sqrt(2 x 64) x 0.02 = 2 and b of about 8 x 8 = 64, so f3 goes as 3 a b and
+    # f5 as 15 a b^2: the second term is s^2 / 20 x 5 b = 2e-5 of the first, and a
+    # hundredth of the difference between the two steps covers what is left.
+    wide, narrow = difference(1e-3), difference(5e-4)
+    slope, off = (4 * narrow - wide) / 3, 0.01 * abs(wide - narrow) + 1e-10
+    # The gradient's error e has a norm below 1e-5 of each part's (the fp32 path's
+    # bound on dW, and on dH, whose rows add up in groups of up to m positions).
+    # E is drawn apart from it, so e . E is normal with deviation |e|: six of them.
+    m = torch.bincount(text.long()).max().item()
+    e = 1e-5 * (head.double().norm() + 8.0 * m ** 0.5 * dH.double().norm()).item()
+    assert abs(slope - (dW.double() * E.double()).sum().item()) <= 6 * e + off
 
 
 def test_two_streams_at_once(ckl):
