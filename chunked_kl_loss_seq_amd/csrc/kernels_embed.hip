@@ -25,7 +25,7 @@
 //  gradient of 32,768 x 2,880 of 201,088: 515-525 us, 4.9 TB/s (dY read, dW
 //    written); the zeros alone, as a plain fill of dW, take 433 us (5.35 TB/s; a
 //    fill of 1 GiB reaches 6.9).
-//  gradient of 4,096 x 2,048 of 32,000: 56 us, 5.0 TB/s, of which rank 8, sum 31
+//  gradient of 4,096 x 2,048 of 32,000: 54 us, 5.2 TB/s, of which rank 6, sum 31
 //    with most of the zeros, join 15 with the rest.
 #include <hip/hip_runtime.h>
 
@@ -143,12 +143,13 @@ __device__ inline uint32_t block_before(uint32_t v, uint32_t* wsum) {
 
 // Few positions: a position's place is the number of positions before it in
 // (id, position) order, counted directly: one launch in place of the radix
-// sort's four.  16 lanes share one position and the list passes through LDS
-// (4,096 positions: 49 us with 4 lanes a position, which left most of the chip
-// idle).
+// sort's four.  32 lanes share one position and the list passes through LDS
+// (whole calls of 4,096 and 8,192 positions, d = 64, with 16, 32 and 64 lanes a
+// position: 22, 20, 20 and 30, 29, 30 us; by the radix sort 8,192 x 2,048 takes 79
+// us, so 72).
 constexpr int kRankMax = 8192;
 constexpr int kRankTile = 4096;
-constexpr int kRankLanes = 16;
+constexpr int kRankLanes = 32;
 __global__ void __launch_bounds__(kThreads) rank_kernel(const int32_t* __restrict__ ids, int N, uint32_t V,
                                                         uint32_t* __restrict__ skey, uint32_t* __restrict__ spos) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[kRankTile];
