@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
   // wave w owns elements [64 kRounds w, 64 kRounds (w + 1)) of the tile, in order
   const int64_t base = (int64_t)blockIdx.x * kSortTile + (int64_t)w * 64 * kRounds;
   uint32_t key[kRounds], place[kRounds], rank[kRounds];
+  bool marks[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     const int64_t i = base + r * 64 + lane < N ? base + r * 64 + lane : N - 1;
@@ -315,6 +316,15 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
         __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
     const uint32_t old = in ? cnt[w][dg] : 0;
     rank[r] = old + before;
+    // The lower digits are in order, so lanes of one key are neighbours among
+    // the lanes of `same`: the first of them marks the token.  (With a mark by
+    // every position, a launch for 10,595 positions of 1,497 tokens took 36 us, not 13.)
+    const uint64_t lower = same & ((1ull << lane) - 1);
+    marks[r] = in;
+    if (bits != nullptr) {
+      const uint32_t other = __shfl(key[r], lower ? 63 - __builtin_clzll(lower) : lane);
+      marks[r] = in && (lower == 0 || other != key[r]);
+    }
     // one lane per digit moves the wave's counter on (LDS operations of one
     // wave are in order; the barriers keep the compiler from moving them)
     __builtin_amdgcn_wave_barrier();
@@ -341,8 +351,8 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const int32_t* _
       const uint32_t at = cnt[w][(key[r] >> shift) & (kDigits - 1)] + rank[r];
       keys_out[at] = key[r];
       pos_out[at] = place[r];
-      // the plain read spares a frequent token's word most of its atomics
-      if (bits != nullptr && key[r] < V && ((bits[key[r] >> 5] >> (key[r] & 31)) & 1u) == 0)
+      // the plain read spares a frequent token's word more atomics
+      if (bits != nullptr && marks[r] && key[r] < V && ((bits[key[r] >> 5] >> (key[r] & 31)) & 1u) == 0)
         atomicOr(&bits[key[r] >> 5], 1u << (key[r] & 31));
     }
   }
