@@ -22,7 +22,7 @@
 // Measured (MI355X, bf16):
 //  lookup of 32,768 x 2,880: 52 us, 7.3 TB/s of rows read and written (repeated
 //    rows come from the caches); of one row: 2 us on the device.
-//  gradient of 32,768 x 2,880 of 201,088: 515-525 us, 4.9 TB/s (dY read, dW
+//  gradient of 32,768 x 2,880 of 201,088: 503-515 us, 4.9 TB/s (dY read, dW
 //    written); the zeros alone, as a plain fill of dW, take 433 us (5.35 TB/s; a
 //    fill of 1 GiB reaches 6.9).
 //  gradient of 4,096 x 2,048 of 32,000: 54 us, 5.2 TB/s, of which rank 6, sum 31
