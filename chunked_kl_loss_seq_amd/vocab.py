@@ -249,7 +249,8 @@ def _check_fp8(torch, q, scales, shape, name, dev):
 def matmul_fp8(xq, xs, wq, ws, dtype=None, out=None):
     """xq [M, d] times the transposed weight wq [V, d], both in 8 bits with the scales
     ``quantize_fp8`` gives (rows, and a weight): [M, V] in ``dtype`` (bfloat16 if
-    None, or float32), summed in fp32 and rounded once.  No gradient."""
+    None, or float32), summed in fp32 and rounded once (for bfloat16 results,
+    products 14 bits below the largest of their 8 may be dropped).  No gradient."""
     import torch
 
     dev = _gpu(xq, "xq")

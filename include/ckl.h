@@ -288,7 +288,10 @@ int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t blo
 
 /* out[m][v] = sum over blocks kb of xs[kb][m] ws[v / 128][kb]
  *             (sum over k of block kb of xq[m][k] wq[v][k]),
- * block sums and the sum over blocks in fp32, rounded once to out_dtype.
+ * block sums and the sum over blocks in fp32, rounded once to out_dtype.  For
+ * bf16 results the products of a group of 8 k are aligned to the group's
+ * largest and what lies 14 bits and more below it may be dropped (less than
+ * 7 x 2^-13 of that product a group); fp32 results keep fp32's bits.
  *   xq, xs    [M, d] and [ceil(d / 128), M], as ckl_quantize_fp8 writes rows
  *   wq, ws    [V, d] and [ceil(V / 128), ceil(d / 128)], as it writes a weight
  *   out       [M, V] in out_dtype (overwritten)
