@@ -287,7 +287,7 @@ __device__ inline double mass_of(const Red& red, double y) {
 
 // A row's settings; in LDS, where they take no registers through the passes.
 struct Settings {
-  double T, p, min_p, u;
+  double p, min_p, u;
   double c;  // 64 log2(e) / T
   bool limit;
   uint32_t k;
@@ -773,8 +773,8 @@ __device__ __forceinline__ Found find_border(const Row<T>& row, Shared& sh, cons
 // smaller ones are one count, larger ones another, so that a logit's place is
 // eight packed 16-bit operations for two logits, without a branch.  Where
 // logits beyond +-256 matter, or nonzero ones below 2^-24 do (by 1e-13 of the
-// mass, or because a border falls among them), the row is left to the general
-// path (id kLeft).
+// mass, because a border falls among them, min_p's too, or because the largest
+// logit is one of them), the row is left to the general path (id kLeft).
 //
 // The counting itself keeps up with the memory (1,024 rows of 201,088: 80 us,
 // 5.2 TB/s; without the LDS adds 77), so what follows it is kept short: a
@@ -932,6 +932,18 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
   if (low && sc.y(-256.f) < (double)kBins) return false;
   const double e0 = uniform(mass_of(sh.red, sc.y(0.f)));  // of 0, where the row has it
   const double min_p = uniform(sh.how.min_p);
+  // Nonzero logits below 2^-24 are taken as 0, and weigh between the e of -2^-24
+  // and of 2^-24 (which may be far apart: T may be smaller still).  They show by
+  // that much mass, where min_p's border lies between the two, and where 0 is the
+  // largest logit, as every e is relative to that.
+  bool tiny_counts = zeros && top % kPlaces == kPer;
+  double spread = 0.0;
+  if (zeros && !tiny_counts) {
+    const double w = 0x1p-24 * sc.c, y0 = sc.y(0.f);
+    const double hi = uniform(mass_of(sh.red, fmax(y0 - w, 0.0))), lo = uniform(mass_of(sh.red, y0 + w));
+    spread = uniform((double)zeros * (hi - lo));
+    tiny_counts = lo < min_p && min_p <= hi;
+  }
   double sum = 0.0, likely = 0.0, before = 0.0, dummy;
   uint32_t cbefore = 0;
   if (any) {  // else every place of the wave is empty
@@ -962,8 +974,7 @@ __device__ __forceinline__ bool pick_counted(const Row<__bf16>& row, CountShared
   const bool limit = sh.how.limit;
   if (limit) block_prefix(mine, sh.red, &cbefore);
   const double s_min = min_p > 0.0 ? uniform(block_prefix(likely, sh.red, &dummy)) : S;
-  // nonzero logits below 2^-24 are taken as 0: off by 2^-24 / T of their mass
-  bool tiny_counts = zeros && (double)zeros * e0 * 0x1p-24 > 1e-13 * sh.how.T * S;
+  tiny_counts |= spread > 1e-13 * S;
 
   // Borders: k, then p, then the draw.  Each falls to the first thread at the
   // end of whose values it is reached (the last with mass if rounding leaves
@@ -1046,16 +1057,16 @@ constexpr int kSlicesMax = 16;
 // The row's settings; a temperature that is not above zero is greedy.
 __device__ inline Settings row_settings(const SampleArgs& a, int64_t r) {
   Settings s;
-  s.T = a.p.temperatures ? (double)a.p.temperatures[r] : a.p.temperature;
+  double T = a.p.temperatures ? (double)a.p.temperatures[r] : a.p.temperature;
   int64_t k = a.p.top_ks ? (int64_t)a.p.top_ks[r] : a.p.top_k;
   s.p = a.p.top_ps ? (double)a.p.top_ps[r] : a.p.top_p;
   s.min_p = a.p.min_ps ? (double)a.p.min_ps[r] : a.p.min_p;
-  if (!(s.T > 0.0)) {
-    s.T = 1.0;
+  if (!(T > 0.0)) {
+    T = 1.0;
     k = 1;
   }
-  s.T = fmax(s.T, 1e-200);  // keeps 1 / T finite; only equal logits share the mass long before
-  s.c = 92.332482616893656877 / s.T;
+  T = fmax(T, 1e-200);  // keeps 1 / T finite; only equal logits share the mass long before
+  s.c = 92.332482616893656877 / T;
   s.limit = k > 0 && k < a.V;
   s.k = (uint32_t)(s.limit ? k : a.V);
   if (!(s.min_p > 0.0)) s.min_p = 0.0;
