@@ -104,6 +104,11 @@ struct Key<float> {
 __device__ inline uint64_t pack(uint32_t key, uint32_t id) { return ((uint64_t)key << 32) | (0xFFFFFFFFu - id); }
 __device__ inline uint32_t unpack_id(uint64_t c) { return 0xFFFFFFFFu - (uint32_t)c; }
 
+// The larger of two logits, NaN if either is.  (fmaxf would go on from what comes
+// after a signalling NaN, and forget the largest before it.  Comparisons, which
+// leave NaN out at once, made one row of 201,088 bf16 logits 26 us for 18.)
+__device__ inline float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // A value that is the same in every lane, in scalar registers.
 __device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ inline float uniform(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(uint32_t, v))); }
@@ -153,11 +158,12 @@ struct Row {
       }
     }
   }
+  // NaN where one of them is
   __device__ static inline float largest(const u32x4_t& v) {
     float f[kN];
     unpack(v, f);
 #pragma unroll
-    for (int i = 1; i < kN; ++i) f[0] = fmaxf(f[0], f[i]);
+    for (int i = 1; i < kN; ++i) f[0] = larger(f[0], f[i]);
     return f[0];
   }
 };
@@ -1250,8 +1256,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
   // 1. the largest logit, and each thread's
   float mv = -INFINITY;
   for_each_chunk<8>(
-      row, [&](const u32x4_t& v, uint32_t) { mv = fmaxf(mv, Row<T>::largest(v)); },
-      [&](T l, int64_t) { mv = fmaxf(mv, (float)l); });
+      row, [&](const u32x4_t& v, uint32_t) { mv = larger(mv, Row<T>::largest(v)); },
+      [&](T l, int64_t) { mv = larger(mv, (float)l); });
+  if (mv != mv) {  // the thread met NaN: its largest by comparisons
+    mv = -INFINITY;
+    for_each(row, [&](float l, int64_t) { mv = l > mv ? l : mv; });
+  }
   const float mx = uniform(block_max(mv, sh.red));
   if (mx == -INFINITY) {  // nothing to sample
     if (tid == 0) {
@@ -1306,7 +1316,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
       for_each_chunk<kFlight>(
           row,
           [&](const u32x4_t& v, uint32_t c) {
-            if (Row<T>::largest(v) >= v0) {
+            if (!(Row<T>::largest(v) < v0)) {  // also beside NaN
               float f[Row<T>::kN];
               Row<T>::unpack(v, f);
 #pragma unroll
