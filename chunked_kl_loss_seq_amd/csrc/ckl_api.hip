@@ -624,6 +624,7 @@ int ckl_embed(int dtype, const int32_t* ids, const void* W, float scale, int64_t
   if (st != CKL_OK || N == 0) return st;
   if (!ids || !W || !out) return CKL_EINVAL;
   if (!aligned(ids, 4) || !aligned(W, 16) || !aligned(out, 16)) return CKL_EINVAL;
+  if (embed_blocks(to_dt(dtype), N, d) >= kMaxBlocks256) return CKL_EUNSUPPORTED;
   try {
     Timed t(T_EMBED, stream);
     CKL_TRY(launch_embed(to_dt(dtype), ids, W, scale, N, d, V, out, stream));

@@ -717,12 +717,22 @@ hipError_t launch_runs(RunArgs a, const int32_t* ids, const void* dY, hipStream_
 
 }  // namespace
 
-hipError_t launch_embed(Dtype dt, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V,
-                        void* out, hipStream_t s) {
-  const int cpr = (int)(d / (dt == DT_BF16 ? 8 : 4));
+namespace {
+// Lanes of a row, as their binary logarithm.
+inline int embed_lanes(int cpr) {
   int lg = 0;
   while (lg < 6 && (1 << lg) < cpr) ++lg;
-  const unsigned grid = (unsigned)cdiv(N, kThreads >> lg);
+  return lg;
+}
+inline int row_chunks(Dtype dt, int64_t d) { return (int)(d / (dt == DT_BF16 ? 8 : 4)); }
+}  // namespace
+
+int64_t embed_blocks(Dtype dt, int64_t N, int64_t d) { return cdiv(N, kThreads >> embed_lanes(row_chunks(dt, d))); }
+
+hipError_t launch_embed(Dtype dt, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V,
+                        void* out, hipStream_t s) {
+  const int cpr = row_chunks(dt, d), lg = embed_lanes(cpr);
+  const unsigned grid = (unsigned)embed_blocks(dt, N, d);
   if (dt == DT_BF16)
     hipLaunchKernelGGL(embed_kernel<__bf16>, dim3(grid), dim3(kThreads), 0, s, ids, (const __bf16*)W, scale, N, V, cpr,
                        lg, (__bf16*)out);

@@ -93,6 +93,8 @@ hipError_t launch_topk(Dtype dt, const void* x, int64_t N, int64_t V, int64_t K,
 // out[n] = scale W[ids[n]] (zeros for an id outside [0, V)), see kernels_embed.hip.
 hipError_t launch_embed(Dtype dt, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V,
                         void* out, hipStream_t s);
+// Its workgroups, of 256 threads.
+int64_t embed_blocks(Dtype dt, int64_t N, int64_t d);
 // dW[v] (+)= scale x the sum of dY's rows with id v; ws of embed_bwd_workspace bytes.
 uint64_t embed_bwd_workspace(int64_t N, int64_t d, int64_t V);
 hipError_t launch_embed_bwd(Dtype dt, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,

@@ -205,7 +205,9 @@ int ckl_topk(int dtype, const void* logits, int64_t N, int64_t V, int64_t K, int
  *   ids       int32 [N]; an id outside [0, V) is a position without a token:
  *             its row of out is zeros
  *   W         [V, d], out [N, d], 16-byte aligned
- * N < 2^26, V <= 2^26, d % 8 == 0, d <= 2^20.  No workspace. */
+ * N < 2^26, V <= 2^26, d % 8 == 0, d <= 2^20; CKL_EUNSUPPORTED also where a
+ * launch would pass 2^24 - 1 workgroups (the last three N, for rows of more than
+ * 512 bytes).  No workspace. */
 int ckl_embed(int dtype, const int32_t* ids, const void* W, float scale, int64_t N, int64_t d, int64_t V, void* out,
               hipStream_t stream);
 
@@ -222,7 +224,7 @@ int ckl_embed(int dtype, const int32_t* ids, const void* W, float scale, int64_t
  * Sums are fp32 in a fixed order, so the result depends on the inputs alone.
  * Positions without a token contribute nothing.  N = 0: dW = 0, or nothing.
  * Shapes as for ckl_embed; CKL_EUNSUPPORTED also where a launch would pass
- * 2^24 workgroups. */
+ * 2^24 - 1 workgroups. */
 int ckl_embed_bwd(int dtype, const int32_t* ids, const void* dY, float scale, int64_t N, int64_t d, int64_t V,
                   int accumulate, float* dW, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
 int ckl_embed_bwd_workspace(int64_t N, int64_t d, int64_t V, uint64_t* bytes_out);
