@@ -249,8 +249,11 @@ def _check_fp8(torch, q, scales, shape, name, dev):
 def matmul_fp8(xq, xs, wq, ws, dtype=None, out=None):
     """xq [M, d] times the transposed weight wq [V, d], both in 8 bits with the scales
     ``quantize_fp8`` gives (rows, and a weight): [M, V] in ``dtype`` (bfloat16 if
-    None, or float32), summed in fp32 and rounded once (for bfloat16 results,
-    products 14 bits below the largest of their 8 may be dropped).  No gradient."""
+    None, or float32), summed in fp32 and rounded once.  For bfloat16 results,
+    products 14 bits below the largest of their 8 may be dropped, except in calls
+    of up to 16 rows under fewer than 16,384 ids, or of one or two rows under a
+    weight of more than 2^28 values: there a row's results can differ from those
+    that it has among more rows, within that bound.  No gradient."""
     import torch
 
     dev = _gpu(xq, "xq")
@@ -277,7 +280,8 @@ def matmul_fp8(xq, xs, wq, ws, dtype=None, out=None):
 def logits_fp8(H, wq, ws, dtype=None, out=None):
     """Logits [M, V] of hidden states H [M, d] (bfloat16 or float32) under a head held
     in 8 bits (``wq``, ``ws`` = ``quantize_fp8(W, 128)``, once): H's rows are
-    quantised in the call, then ``matmul_fp8``."""
+    quantised in the call, then ``matmul_fp8``, whose accuracy and results they
+    have (``dtype`` float32 keeps every product).  No gradient."""
     xq, xs = quantize_fp8(H)
     return matmul_fp8(xq, xs, wq, ws, dtype=dtype, out=out)
 
@@ -287,8 +291,11 @@ def teacher_topk(H, wq, ws, K, chunk=0):
     int32 [N, K], values float32 [N, K]) as ``topk`` of their bfloat16 logits.
 
     Positions go in chunks (``chunk`` rows; 0: about 1 GiB of logits), so the
-    N x V logits are never held at once.  As for ``topk``, NaN logits (a hidden
-    row that is not finite) are outside its inputs.
+    N x V logits are never held at once.  The logits are ``logits_fp8`` of each
+    chunk: with ``chunk`` 0 they are those of all rows in one call, a given chunk
+    of few rows may take the product's other arithmetic (see ``matmul_fp8``).  As
+    for ``topk``, NaN logits (a hidden row that is not finite) are outside its
+    inputs.
     """
     import torch
 
@@ -298,14 +305,21 @@ def teacher_topk(H, wq, ws, K, chunk=0):
     N, V, K, chunk = H.shape[0], wq.shape[0], int(K), int(chunk)
     if chunk < 0 or K < 1 or K > V:
         raise ValueError("chunk must be at least 0 and K in 1 .. V")
+    least = 0  # rows of the last chunk: a few rows could take another kernel than the chunks before
     if chunk == 0:
-        chunk = max(256, (1 << 30) // (2 * V) // 256 * 256)
+        chunk = max(1, (1 << 30) // (2 * V))
+        chunk = chunk // 256 * 256 or chunk
+        least = min(128, chunk // 2)
     ids = torch.empty((N, K), dtype=torch.int32, device=dev)
     vals = torch.empty((N, K), dtype=torch.float32, device=dev)
     logits = torch.empty((min(chunk, N), V), dtype=torch.bfloat16, device=dev)
     with _on(torch, dev):
-        for r in range(0, N, chunk):
+        r = 0
+        while r < N:
             n = min(chunk, N - r)
+            if 0 < N - r - n < least:
+                n = N - r - least
             logits_fp8(H[r:r + n], wq, ws, out=logits[:n])
             topk(logits[:n], K, ids_out=ids[r:r + n], vals_out=vals[r:r + n])
+            r += n
     return ids, vals

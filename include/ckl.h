@@ -293,7 +293,10 @@ int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t blo
  * block sums and the sum over blocks in fp32, rounded once to out_dtype.  For
  * bf16 results the products of a group of 8 k are aligned to the group's
  * largest and what lies 14 bits and more below it may be dropped (less than
- * 7 x 2^-13 of that product a group); fp32 results keep fp32's bits.
+ * 7 x 2^-13 of that product a group); fp32 results keep fp32's bits.  Up to 16
+ * rows with V < 16,384, and one or two with V d > 2^28, go by a kernel that keeps
+ * them for bf16 results too; all other calls give a row the same bits whatever
+ * the rows beside it.
  *   xq, xs    [M, d] and [ceil(d / 128), M], as ckl_quantize_fp8 writes rows
  *   wq, ws    [V, d] and [ceil(V / 128), ceil(d / 128)], as it writes a weight
  *   out       [M, V] in out_dtype (overwritten)
