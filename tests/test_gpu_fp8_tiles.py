@@ -53,7 +53,8 @@ def check(out, xq, xs, wq, ws, rows=slice(None)):
         w = w * s[:w.shape[0], :d]
         want, mag = x @ w.t(), x.abs() @ w.abs().t()
         lost = 7 * 2.0 ** -13 if out.dtype == BF16 else 0.0
-        bound = ((128 + blocks + 3) * 2.0 ** -23 + lost) * mag + want.abs() * (2.0 ** -8 if out.dtype == BF16 else 2.0 ** -24)
+        half_step = 2.0 ** -8 if out.dtype == BF16 else 2.0 ** -24
+        bound = ((128 + blocks + 3) * 2.0 ** -23 + lost) * mag + want.abs() * half_step
         err = (out[:, v:v + 16384].double() - want).abs()
         assert torch.all(err <= bound), (v, float((err - bound).max()))
 
@@ -99,5 +100,6 @@ def test_rows_alone(ckl, dtype):
     for r, n in ((0, 300), (1900, 149), (1024, 70), (7, 17), (2040, 9), (2048, 1), (300, 2)):
         assert torch.equal(ckl.logits_fp8(x[r:r + n], wq, ws, dtype=dtype), out[r:r + n]), (r, n)
     # up to 16 rows under fewer than 16,384 ids: another kernel, within the bound
-    few = ckl.matmul_fp8(xq[:9].contiguous(), xs[:, :9].contiguous(), wq[:9000].contiguous(), ws[:71].contiguous(), dtype=dtype)
+    few = ckl.matmul_fp8(xq[:9].contiguous(), xs[:, :9].contiguous(), wq[:9000].contiguous(), ws[:71].contiguous(),
+                         dtype=dtype)
     check(few, xq, xs, wq[:9000], ws[:71], slice(0, 9))

@@ -57,8 +57,8 @@ def test_low_temperatures(ckl, T, fill):
     step = 2.0 ** -32  # of bf16 below 2^-24
     for top in (2.0 ** -24, 2.0 ** -24 * (1 + 2.0 ** -7), 2.0 ** -24 - step, 2.0 ** -23):
         check(ckl, [top] + [2.0 ** -24 - 2 * step] * 3 + tail, US, "tiny beside the largest", temperature=T)
-        check(ckl, [0.0, 2.0 ** -24 - 2 * step, -2.0 ** -24 + step, top, -0.0] + tail, US, "tiny, zeros and the largest",
-              temperature=T)
+        check(ckl, [0.0, 2.0 ** -24 - 2 * step, -2.0 ** -24 + step, top, -0.0] + tail, US,
+              "tiny, zeros and the largest", temperature=T)
         check(ckl, [top] + [2.0 ** -24 - 2 * step] * 3 + tail, US, "tiny beside the largest", temperature=T, top_p=0.6)
     got = check(ckl, [2.0 ** -24] + [2.0 ** -24 - step] * 3 + tail, US, "tiny beside 2^-24", temperature=T)
     if T >= 1e-9:  # each of the three weighs 0.79 and more of the largest
