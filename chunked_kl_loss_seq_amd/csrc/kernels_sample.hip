@@ -9,9 +9,12 @@
 // and S the mass of the shortest of the three, the token is the first of the
 // order whose cumulative mass exceeds u S, and logp = log(e_token / S).
 //
-// A token changes where its border moves, so masses and borders are held to
-// about 1e-14 of the total: exponentials in fp64, sums in 64-bit integers (in
-// any order the same) and fp64.
+// A token changes where its border moves, so exponentials are fp64 and sums 64-bit
+// integers (in any order the same) and fp64.  The integers of the general path
+// hold a token's mass to half a unit of 2^-min(51, 62 - ceil(log2 V)) of its bin's
+// edge and equal logits round alike, so borders are held to V / 2^62 of the total
+// (4e-14 at 201,088 tokens), plus 5e-15 of the exponentials.  Counted rows may
+// leave out 1e-13 of it.
 //
 // The floor is reading a row once.  One workgroup of 1024 threads takes a row:
 //  1. bf16 rows (count_kernel): a count of every value, one LDS add per logit,
@@ -45,8 +48,11 @@
 //  61 x 32,000 fp32, limits of each row's own: 29 us, the rows without a top-k
 //    in 2b, half of it fp64 arithmetic on the row's one compute unit (with
 //    top-k 200: 16 us by 2a).
-//  1,024 x 201,088 fp32, no limit: 440 us, 1.9 TB/s, bound by the 64-bit LDS
-//    adds of 2b and the fp64 polynomial.
+//  1,024 x 201,088 fp32, no limit: 436 us, 1.9 TB/s, bound by the 64-bit LDS
+//    adds of 2b and the fp64 polynomial (with top-k 50, by 2a: 185 us).
+//  A bf16 row that counting leaves to the general path keeps its compute unit
+//    busy for 40 to 100 us more: 1,024 x 201,088 normal logits of deviation 1, 3
+//    of which rows hold a nonzero one below 2^-24, take 192 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

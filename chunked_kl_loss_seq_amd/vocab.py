@@ -145,8 +145,10 @@ class _Embedding:
 def embedding(ids, W, scale=1.0):
     """``embed`` as a differentiable torch function of W (gradient: ``embed_bwd``).
 
-    A stream capture takes it only where no gradient is asked for; a captured
-    training step calls ``embed`` and ``embed_bwd``.
+    W is copied where it is not contiguous, in every call; a bfloat16 W's gradient
+    is summed in a float32 [V, d] and then rounded.  A stream capture takes it only
+    where no gradient is asked for; a captured training step calls ``embed`` and
+    ``embed_bwd``.
     """
     import torch
 

@@ -261,8 +261,9 @@ typedef struct ckl_sampling {
  *   ids_out   int32 [N]; -1 for a row without a token that can be drawn
  *   logp_out  fp32 [N] or NULL: log(e / S) of the drawn token (-inf for -1)
  * Masses and borders are computed in 64 bits, so the token is that of the
- * formulas except where a border is within about 1e-13 of the total; tokens
- * whose e is below 2^-64 count as 0.  V <= 2^26, N < 2^22.
+ * formulas except where a border is within about 1e-13 + V / 2^62 of the total
+ * (1.4e-13 at 201,088 tokens, 1.5e-11 at 2^26); tokens whose e is below 2^-64
+ * count as 0.  V <= 2^26, N < 2^22.
  *   workspace NULL, or a device buffer of at least ckl_sample_workspace bytes
  *             (0 for most shapes), 256-byte aligned, not shared by calls that
  *             may overlap: with it, long rows of a small batch are split over
@@ -280,8 +281,8 @@ int ckl_sample_workspace(int dtype, int64_t N, int64_t V, uint64_t* bytes_out);
  *           1 x 128 block, blocks of columns outermost
  *   weight  [R, C] with block_rows = 128: scales [ceil(R / 128), ceil(C / 128)]
  * ckl_quantize_fp8: scale = amax / 448 of the block's finite values (1 for a
- * block of zeros, at least 2^-126), q = x / scale rounded to nearest even;
- * values that are not finite become NaN, and only they.
+ * block of zeros, at least 2^-126), q = the fp32 quotient x / scale rounded to
+ * nearest even; values that are not finite become NaN, and only they.
  *   dtype     ckl_dtype of x (16-byte aligned, as q_out)
  *   C         a multiple of 16, at most 2^20; the last block of 128 columns
  *             and of 128 rows may be short */
@@ -290,7 +291,9 @@ int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t blo
 
 /* out[m][v] = sum over blocks kb of xs[kb][m] ws[v / 128][kb]
  *             (sum over k of block kb of xq[m][k] wq[v][k]),
- * block sums and the sum over blocks in fp32, rounded once to out_dtype.  For
+ * block sums and the sum over blocks in fp32, rounded once to out_dtype.  The
+ * two scales are multiplied first, in fp32: a product of theirs below 2^-126
+ * loses bits, one past fp32's range is inf.  For
  * bf16 results the products of a group of 8 k are aligned to the group's
  * largest and what lies 14 bits and more below it may be dropped (less than
  * 7 x 2^-13 of that product a group); fp32 results keep fp32's bits.  Up to 16
