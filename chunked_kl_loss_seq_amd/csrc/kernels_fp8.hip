@@ -33,11 +33,13 @@
 //     of reading the weight.
 //   * else tiles staged through a two-stage LDS ring by LDS DMA, one barrier
 //     per block of k, of the size that is expected to end first.  Up to about
-//     128 rows this is bound by reading the weight (16 x 201,088 x 2,880: 121 us,
-//     4.8 TB/s), beyond by the board's power: 2,048 x 201,088 x 2,880 takes
-//     1,256 us (1,888 TFLOP/s) with the matrix cores busy 39 % of the cycles at
-//     1.77 GHz; loading the next block's fragments across the barrier made them
-//     busy 48 % of the cycles, at 1.56 GHz, in the same time.
+//     128 rows this is bound by reading the weight (16 x 201,088 x 2,880: 117-121
+//     us, 4.8 TB/s).  2,048 x 201,088 x 2,880 takes 1,250 us (1,900 TFLOP/s; the
+//     library's product with one scale 1,215): the matrix cores are busy 45 % of
+//     the cycles at 2.0 GHz, vector instructions issue in 36 % of them, and a third
+//     of the waves' time goes to the barrier and loads, a third to waiting for
+//     issue.  Loading the next block's fragments across the barrier did not make
+//     it faster (1,285 us for 1,277).  fp32 results of the same shape take 2,100 us.
 #include "gemm_core.hpp"
 #include "launch.hpp"
 
