@@ -2,7 +2,8 @@
 
 ``binding`` loads libckl.so on first use and raises if it is missing;
 ``vocab`` has the operators around the vocabulary table (embedding,
-sampling, the head's product with an 8-bit weight);
+sampling, the head's product with an 8-bit weight); ``residual`` the end of a
+block before it (norms around the residual, dropout);
 ``workloads`` draws the seeded synthetic inputs.
 """
 from .binding import (  # noqa: F401
@@ -19,6 +20,13 @@ from .binding import (  # noqa: F401
     topk,
     timing_query,
     workspace_bytes_held,
+)
+from .residual import (  # noqa: F401
+    add_norm,
+    add_norm_bwd,
+    drop,
+    dropout,
+    residual_norm,
 )
 from .vocab import (  # noqa: F401
     embed,

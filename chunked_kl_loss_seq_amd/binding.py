@@ -17,7 +17,7 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 PASSES = {"fused": 0, "fwd": 1, "bwd": 2}
 TIMING_KINDS = {"logits": 0, "rows": 1, "dh": 2, "dh_reduce": 3, "dw": 4, "other": 5, "topk": 6, "embed": 7,
-                "sample": 8, "fp8": 9}
+                "sample": 8, "fp8": 9, "norm": 10}
 
 _lib = None
 
@@ -28,6 +28,21 @@ class Sampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_double), ("top_k", ctypes.c_int64), ("top_p", ctypes.c_double),
                 ("min_p", ctypes.c_double), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
                 ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
+
+
+class Drop(ctypes.Structure):
+    """ckl_drop: a dropout's probability, seed and offset."""
+
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p)]
+
+
+class Norm(ctypes.Structure):
+    """ckl_norm: weights, gate and numbers of the residual's norms."""
+
+    _fields_ = [("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_rows", ctypes.c_int), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("drop", ctypes.POINTER(Drop))]
 
 
 class CklError(RuntimeError):
@@ -78,6 +93,15 @@ def lib():
     L.ckl_quantize_fp8.restype = ctypes.c_int
     L.ckl_matmul_fp8.argtypes = [ctypes.c_int, vp, vp, vp, vp, i64, i64, i64, vp, vp]
     L.ckl_matmul_fp8.restype = ctypes.c_int
+    L.ckl_dropout.argtypes = [ctypes.c_int, vp, i64, ctypes.POINTER(Drop), vp, vp]
+    L.ckl_dropout.restype = ctypes.c_int
+    L.ckl_add_norm.argtypes = [ctypes.c_int, vp, vp, ctypes.POINTER(Norm), i64, i64, vp, vp, vp, vp]
+    L.ckl_add_norm.restype = ctypes.c_int
+    L.ckl_add_norm_bwd.argtypes = [ctypes.c_int, vp, vp, ctypes.POINTER(Norm), i64, i64, vp, vp, vp, vp, vp, vp, vp, vp,
+                                   vp, u64, vp]
+    L.ckl_add_norm_bwd.restype = ctypes.c_int
+    L.ckl_add_norm_bwd_workspace.argtypes = [i64, i64, ctypes.c_int, ctypes.POINTER(u64)]
+    L.ckl_add_norm_bwd_workspace.restype = ctypes.c_int
     L.ckl_release_workspace.argtypes = []
     L.ckl_release_workspace.restype = None
     L.ckl_workspace_bytes_held.argtypes = []

@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libckl.so")
 SOURCES = ["ckl_api.hip", "kernels_embed.hip", "kernels_fp8.hip", "kernels_gemm.hip", "kernels_logits.hip",
-           "kernels_rows.hip", "kernels_sample.hip", "kernels_topk.hip"]
+           "kernels_norm.hip", "kernels_rows.hip", "kernels_sample.hip", "kernels_topk.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

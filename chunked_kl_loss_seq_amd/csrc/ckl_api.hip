@@ -291,7 +291,7 @@ struct TraceRange {
 };
 
 // ------------------------------------------------------------------ timing
-enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_KINDS };
+enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_NORM, T_KINDS };
 struct TimingState {
   bool on = false;
   std::vector<std::pair<hipEvent_t, hipEvent_t>> pool;
@@ -522,6 +522,48 @@ int embed_shape(int64_t N, int64_t d, int64_t V) {
   return CKL_OK;
 }
 
+// A caller's dropout settings as the kernels take them; NULL drops nothing.
+int drop_of(const ckl_drop* how, Drop* out) {
+  *out = Drop{0, 0, nullptr, 0u, 1.f};
+  if (!how) return CKL_OK;
+  if (!(how->p >= 0.0 && how->p <= 1.0) || !aligned(how->offset_dev, 8)) return CKL_EINVAL;  // NaN fails too
+  out->seed = how->seed;
+  out->offset = how->offset;
+  out->at = how->offset_dev;
+  out->border = (uint32_t)(how->p * 65536.0 + 0.5);
+  out->keep = out->border < 65536u ? (float)(65536.0 / (double)(65536u - out->border)) : 0.f;
+  return CKL_OK;
+}
+
+int norm_shape(int64_t N, int64_t d) {
+  if (N < 0 || d <= 0) return CKL_EINVAL;
+  if (d % 8 != 0 || d > kMaxNormWidth || N > (int64_t)1 << 31) return CKL_EUNSUPPORTED;
+  return CKL_OK;
+}
+
+// The part of the kernels' arguments that both directions share.
+int norm_args(int dtype, const void* y, const void* r, const ckl_norm* how, int64_t N, int64_t d, NormArgs* p) {
+  if (!how || !(how->eps >= 0.f) || (how->gate_rows != 0 && how->gate_rows != 1)) return CKL_EINVAL;
+  const uintptr_t el = dtype == CKL_DTYPE_BF16 ? 2 : 4;
+  if (!aligned(y, el) || !aligned(r, el) || !aligned(how->w_post, el) || !aligned(how->w_pre, el) ||
+      !aligned(how->gate, el))
+    return CKL_EINVAL;
+  *p = NormArgs{};
+  const int st = drop_of(how->drop, &p->drop);
+  if (st != CKL_OK) return st;
+  p->y = y;
+  p->r = r;
+  p->w_post = how->w_post;
+  p->w_pre = how->w_pre;
+  p->gate = how->gate;
+  p->gate_rows = how->gate_rows != 0;
+  p->scale = how->scale;
+  p->eps = how->eps;
+  p->N = N;
+  p->d = d;
+  return CKL_OK;
+}
+
 inline Dtype to_dt(int dtype) { return dtype == CKL_DTYPE_BF16 ? DT_BF16 : DT_F32; }
 
 }  // namespace
@@ -741,6 +783,101 @@ int ckl_matmul_fp8(int out_dtype, const uint8_t* xq, const float* xs, const uint
   try {
     Timed t(T_FP8, stream);
     CKL_TRY(launch_matmul_fp8(to_dt(out_dtype), xq, xs, wq, ws, M, V, d, out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_dropout(int dtype, const void* x, int64_t n, const ckl_drop* how, void* out, hipStream_t stream) {
+  if (!dtype_ok(dtype) || n < 0 || !how) return CKL_EINVAL;
+  Drop r;
+  const int st = drop_of(how, &r);
+  if (st != CKL_OK) return st;
+  if (n >= (int64_t)1 << 37 || dropout_blocks(n) >= kMaxBlocks256) return CKL_EUNSUPPORTED;
+  if (n == 0) return CKL_OK;
+  const uintptr_t el = dtype == CKL_DTYPE_BF16 ? 2 : 4;
+  if (!x || !out || !aligned(x, el) || !aligned(out, el)) return CKL_EINVAL;
+  try {
+    Timed t(T_NORM, stream);
+    CKL_TRY(launch_dropout(to_dt(dtype), x, n, r, out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_add_norm(int dtype, const void* y, const void* r, const ckl_norm* how, int64_t N, int64_t d, void* r_out,
+                 void* x, float* stats, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return CKL_EINVAL;
+  int st = norm_shape(N, d);
+  if (st != CKL_OK) return st;
+  NormArgs p;
+  st = norm_args(dtype, y, r, how, N, d, &p);
+  if (st != CKL_OK) return st;
+  const uintptr_t el = dtype == CKL_DTYPE_BF16 ? 2 : 4;
+  if (!aligned(r_out, el) || !aligned(x, el) || !aligned(stats, 4)) return CKL_EINVAL;
+  if (N == 0) return CKL_OK;
+  if (!y || !r || !r_out || (p.w_pre != nullptr) != (x != nullptr)) return CKL_EINVAL;
+  p.r_out = r_out;
+  p.x = x;
+  p.stats = stats;
+  try {
+    Timed t(T_NORM, stream);
+    CKL_TRY(launch_add_norm(to_dt(dtype), p, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_add_norm_bwd_workspace(int64_t N, int64_t d, int sums, uint64_t* bytes_out) {
+  if (!bytes_out || sums < 0 || sums > 3) return CKL_EINVAL;
+  const int st = norm_shape(N, d);
+  if (st != CKL_OK) return st;
+  *bytes_out = align256(add_norm_bwd_workspace(N, d, sums));
+  return CKL_OK;
+}
+
+int ckl_add_norm_bwd(int dtype, const void* y, const void* r, const ckl_norm* how, int64_t N, int64_t d,
+                     const float* stats, const void* dx, const void* dr_in, void* dy, void* dr, float* dw_post,
+                     float* dw_pre, void* dgate, void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return CKL_EINVAL;
+  int st = norm_shape(N, d);
+  if (st != CKL_OK) return st;
+  NormArgs p;
+  st = norm_args(dtype, y, r, how, N, d, &p);
+  if (st != CKL_OK) return st;
+  const uintptr_t el = dtype == CKL_DTYPE_BF16 ? 2 : 4;
+  const bool sums_gate = p.gate != nullptr && !p.gate_rows;
+  if ((p.w_post != nullptr) != (dw_post != nullptr) || (p.w_pre != nullptr) != (dw_pre != nullptr)) return CKL_EINVAL;
+  // without positions only the sums over them have something to hold
+  if ((N > 0 || sums_gate) && (p.gate != nullptr) != (dgate != nullptr)) return CKL_EINVAL;
+  if (!aligned(stats, 4) || !aligned(dx, el) || !aligned(dr_in, el) || !aligned(dy, el) || !aligned(dr, el) ||
+      !aligned(dw_post, 4) || !aligned(dw_pre, 4) || !aligned(dgate, sums_gate ? 4 : el) || !aligned(workspace, 256))
+    return CKL_EINVAL;
+  NormGrads q{};
+  q.sums = (dw_post != nullptr) + (dw_pre != nullptr) + (sums_gate ? 1 : 0);
+  try {
+    if (N == 0) {
+      if (dw_post) CKL_TRY(launch_fill_f32(dw_post, d, 0.f, stream));
+      if (dw_pre) CKL_TRY(launch_fill_f32(dw_pre, d, 0.f, stream));
+      if (sums_gate) CKL_TRY(launch_fill_f32((float*)dgate, d, 0.f, stream));
+      return CKL_OK;
+    }
+    if (!y || !r || !stats || !dy || !dr || (!dx && !dr_in) || (dx && !p.w_pre)) return CKL_EINVAL;
+    if (q.sums && (!workspace || workspace_bytes < add_norm_bwd_workspace(N, d, q.sums))) return CKL_EINVAL;
+    p.stats_in = stats;
+    q.dx = dx;
+    q.dr_in = dr_in;
+    q.dy = dy;
+    q.dr = dr;
+    q.dw_post = dw_post;
+    q.dw_pre = dw_pre;
+    q.dgate = dgate;
+    q.part = (float*)workspace;
+    Timed t(T_NORM, stream);
+    CKL_TRY(launch_add_norm_bwd(to_dt(dtype), p, q, stream));
     return CKL_OK;
   } catch (...) {
     return CKL_EHIP;

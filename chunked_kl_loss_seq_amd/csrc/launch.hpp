@@ -127,6 +127,52 @@ hipError_t launch_quantize_fp8(Dtype dt, const void* x, int64_t R, int64_t C, bo
 hipError_t launch_matmul_fp8(Dtype out_dt, const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                              int64_t M, int64_t V, int64_t d, void* out, hipStream_t s);
 
+// A dropout's draw: elements whose 16 bits (see philox in row_io.hpp) are below
+// `border` go, the others are multiplied by keep = 65536 / (65536 - border).
+// `at`, if not null, is a device word added to the offset when the kernel runs,
+// so that a captured step can move it on.
+struct Drop {
+  uint64_t seed, offset;
+  const int64_t* at;
+  uint32_t border;  // 0: nothing is dropped; 65536: everything
+  float keep;
+};
+// out[i] = x[i] keep or 0, i < n (out may be x), see kernels_norm.hip; its workgroups, of 256 threads.
+hipError_t launch_dropout(Dtype dt, const void* x, int64_t n, const Drop& r, void* out, hipStream_t s);
+int64_t dropout_blocks(int64_t n);
+
+// The residual's norms around a block, see kernels_norm.hip.
+struct NormArgs {
+  const void* y;       // [N, d] the block's output
+  const void* r;       // [N, d] residual
+  const void* w_post;  // [d] or null: y is not normalised
+  const void* w_pre;   // [d] or null: no x
+  const void* gate;    // [d], or [N, d] with gate_rows, or null
+  bool gate_rows;
+  float scale, eps;
+  Drop drop;
+  int64_t N, d;
+  void* r_out;            // [N, d]
+  void* x;                // [N, d]
+  float* stats;           // [2, N] reciprocal rms of y and of r', or null
+  const float* stats_in;  // the same, of the forward call (backward)
+};
+struct NormGrads {
+  const void* dx;     // [N, d] or null
+  const void* dr_in;  // [N, d] gradient of r_out, or null
+  void* dy;           // [N, d]
+  void* dr;           // [N, d]
+  float* dw_post;     // [d]
+  float* dw_pre;      // [d]
+  void* dgate;        // fp32 [d], or [N, d] in the path's type
+  int sums;           // how many of dw_post, dw_pre and a gate [d]'s gradient there are
+  float* part;        // add_norm_bwd_workspace bytes
+};
+constexpr int64_t kMaxNormWidth = 16384;  // d: a row is held in one workgroup's registers
+hipError_t launch_add_norm(Dtype dt, const NormArgs& p, hipStream_t s);
+uint64_t add_norm_bwd_workspace(int64_t N, int64_t d, int sums);
+hipError_t launch_add_norm_bwd(Dtype dt, const NormArgs& p, const NormGrads& q, hipStream_t s);
+
 // Valid-token count n and scale 1/n (0 if n = 0) into scal (int64 n, float s).
 hipError_t launch_mask_count(const uint8_t* mask, int64_t N, void* scal, hipStream_t s);
 // Compaction of the chunk whose mask, H rows, ids and teacher logits start at

@@ -308,6 +308,74 @@ int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t blo
 int ckl_matmul_fp8(int out_dtype, const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
                    int64_t V, int64_t d, void* out, hipStream_t stream);
 
+/* Dropout whose mask is never stored.  Element i of a tensor takes 16 bits of
+ * Philox4x32-10 under the key `seed`: with the counter (i / 8, offset), bits
+ * 16 (j % 2) .. + 15 of word j / 2, j = i % 8.  It goes if they are below
+ * border = floor(65536 p + 0.5), and is multiplied by 65536 / (65536 - border)
+ * if not, so the mean is kept whatever p rounds to.  The same seed, offset and
+ * shape give the same mask, in every call that takes a ckl_drop and in their
+ * gradients.
+ *   p           [0, 1]; below 2^-17 nothing goes, at 1 everything
+ *   offset_dev  NULL, or a device int64 (8-byte aligned) added to offset when
+ *               the call's kernels run: a captured step that moves it on draws
+ *               another mask in every replay */
+typedef struct ckl_drop {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const int64_t* offset_dev;
+} ckl_drop;
+
+/* out[i] = x[i] x 65536 / (65536 - border), or 0 where element i goes (also where
+ * x[i] is not finite), in fp32, rounded once to dtype.  It is its own gradient:
+ * dx is the call on dout with the same ckl_drop.  out may be x.
+ *   x, out   [n] of ckl_dropout's dtype, aligned to an element; n < 2^37 */
+int ckl_dropout(int dtype, const void* x, int64_t n, const ckl_drop* how, void* out, hipStream_t stream);
+
+/* The residual's norms around a block:
+ *   u  = w_post y / rms(y)            u = y without w_post; rms(v) = sqrt(mean(v^2) + eps) over a row
+ *   r' = r + scale gate u             u's elements dropped as ckl_dropout drops them, element index n d + j
+ *   x  = w_pre r' / rms(r')
+ * in fp32, r' and x each rounded once: x is that of the fp32 r'.  The last
+ * block's x is the H of the loss calls.
+ *   dtype     ckl_dtype of y, r, w_post, w_pre, gate, r_out and x
+ *   w_post    [d] or NULL;  w_pre [d], or NULL: x (then NULL) is not computed
+ *   gate      [d], or [N, d] with gate_rows = 1, or NULL for 1
+ *   drop      NULL: nothing is dropped
+ *   r_out     [N, d], may be r (a gradient needs r as it was); x [N, d]
+ *   stats     fp32 [2, N] or NULL: 1 / rms(y) and 1 / rms(r') (1 where not
+ *             computed), for the gradient
+ * d % 8 == 0, d <= 16384, N <= 2^31; arrays aligned to an element.  A row of
+ * zeros with eps = 0 gives NaN, as the formula does. */
+typedef struct ckl_norm {
+  const void* w_post;
+  const void* w_pre;
+  const void* gate;
+  int gate_rows;
+  float scale;
+  float eps; /* >= 0 */
+  const ckl_drop* drop;
+} ckl_norm;
+int ckl_add_norm(int dtype, const void* y, const void* r, const ckl_norm* how, int64_t N, int64_t d, void* r_out,
+                 void* x, float* stats, hipStream_t stream);
+
+/* Its gradient.  `how` (the same arrays, numbers and drop), y, r and stats are the
+ * forward call's.
+ *   dx, dr_in   gradients of x and of r_out; either may be NULL for zeros (dx is
+ *               NULL without w_pre), not both
+ *   dy, dr      [N, d] in dtype; dr may be dr_in, dy may be dx
+ *   dw_post, dw_pre  fp32 [d], each NULL exactly where the weight is
+ *   dgate       fp32 [d], or [N, d] in dtype with gate_rows, NULL without a gate
+ *   workspace   at least ckl_add_norm_bwd_workspace(N, d, sums) bytes, sums = how
+ *               many of dw_post, dw_pre and a gate [d]'s gradient there are;
+ *               256-byte aligned, need not be cleared, not shared by calls that
+ *               may overlap
+ * Sums over rows are fp32 in a fixed order.  N = 0: their outputs are zeros. */
+int ckl_add_norm_bwd(int dtype, const void* y, const void* r, const ckl_norm* how, int64_t N, int64_t d,
+                     const float* stats, const void* dx, const void* dr_in, void* dy, void* dr, float* dw_post,
+                     float* dw_pre, void* dgate, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+int ckl_add_norm_bwd_workspace(int64_t N, int64_t d, int sums, uint64_t* bytes_out);
+
 /* Chunk planner of the fused call (pure host computation, needs no GPU).  The
  * sequence is cut into chunks of C rows so that the loss's own device memory
  * stays bounded independently of N ("A New Trick...", section "Does this
@@ -360,12 +428,14 @@ int ckl_debug_rows(const float* Z, const int32_t* idx, const float* tlogit, cons
 
 /* Measurement support.  While enabled, every kernel launch of a loss call
  * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk), and all launches of one ckl_embed,
- * ckl_embed_bwd, ckl_sample, ckl_quantize_fp8 or ckl_matmul_fp8 call together, are
- * bracketed by HIP events on the call's stream.  ckl_timing_query waits for the recorded events and returns the
- * summed milliseconds and launch count of one kernel kind: 0 logits GEMM,
+ * ckl_embed_bwd, ckl_sample, ckl_quantize_fp8, ckl_matmul_fp8, ckl_dropout,
+ * ckl_add_norm or ckl_add_norm_bwd call together, are bracketed by HIP events on
+ * the call's stream.  ckl_timing_query waits for the recorded events and returns
+ * the summed milliseconds and launch count of one kernel kind: 0 logits GEMM,
  * 1 row pass, 2 dH GEMM, 3 dH split reduce, 4 dW GEMM, 5 other, 6 top-K
- * (ckl_topk), 7 embedding, 8 sampling, 9 8-bit products and
- * quantisers.  Not for concurrent use from several threads. */
+ * (ckl_topk), 7 embedding, 8 sampling, 9 8-bit products and quantisers,
+ * 10 dropout and the residual's norms.  Not for concurrent use from several
+ * threads. */
 int ckl_timing_enable(int on);
 int ckl_timing_query(int kind, double* total_ms, int64_t* launches);
 
