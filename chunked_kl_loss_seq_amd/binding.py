@@ -17,7 +17,7 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 PASSES = {"fused": 0, "fwd": 1, "bwd": 2}
 TIMING_KINDS = {"logits": 0, "rows": 1, "dh": 2, "dh_reduce": 3, "dw": 4, "other": 5, "topk": 6, "embed": 7,
-                "sample": 8, "fp8": 9, "norm": 10}
+                "sample": 8, "fp8": 9, "norm": 10, "logprob": 11}
 
 _lib = None
 
@@ -93,6 +93,20 @@ def lib():
     L.ckl_quantize_fp8.restype = ctypes.c_int
     L.ckl_matmul_fp8.argtypes = [ctypes.c_int, vp, vp, vp, vp, i64, i64, i64, vp, vp]
     L.ckl_matmul_fp8.restype = ctypes.c_int
+    L.ckl_logprobs.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, u64, vp]
+    L.ckl_logprobs.restype = ctypes.c_int
+    L.ckl_logprobs_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(u64)]
+    L.ckl_logprobs_workspace.restype = ctypes.c_int
+    L.ckl_logprobs_bwd.argtypes = [ctypes.c_int, vp, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.ckl_logprobs_bwd.restype = ctypes.c_int
+    L.ckl_head_logprobs.argtypes = [ctypes.c_int, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, u64, vp]
+    L.ckl_head_logprobs.restype = ctypes.c_int
+    L.ckl_head_logprobs_bwd.argtypes = [ctypes.c_int, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp,
+                                        ctypes.c_int, ctypes.c_int, vp, vp, u64, vp]
+    L.ckl_head_logprobs_bwd.restype = ctypes.c_int
+    L.ckl_head_logprobs_plan.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, u64,
+                                         ctypes.POINTER(i64), ctypes.POINTER(u64)]
+    L.ckl_head_logprobs_plan.restype = ctypes.c_int
     L.ckl_dropout.argtypes = [ctypes.c_int, vp, i64, ctypes.POINTER(Drop), vp, vp]
     L.ckl_dropout.restype = ctypes.c_int
     L.ckl_add_norm.argtypes = [ctypes.c_int, vp, vp, ctypes.POINTER(Norm), i64, i64, vp, vp, vp, vp]

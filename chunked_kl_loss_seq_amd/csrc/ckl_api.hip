@@ -291,7 +291,7 @@ struct TraceRange {
 };
 
 // ------------------------------------------------------------------ timing
-enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_NORM, T_KINDS };
+enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_NORM, T_LOGPROB, T_KINDS };
 struct TimingState {
   bool on = false;
   std::vector<std::pair<hipEvent_t, hipEvent_t>> pool;
@@ -520,6 +520,119 @@ int embed_shape(int64_t N, int64_t d, int64_t V) {
   if (N < 0 || d <= 0 || V <= 0) return CKL_EINVAL;
   if (d % 8 != 0 || d > (int64_t)1 << 20 || V > (int64_t)1 << 26 || N >= (int64_t)1 << 26) return CKL_EUNSUPPORTED;
   return CKL_OK;
+}
+
+// ------------------------------------------------------------------ log-probabilities
+// Arguments that the calls on logits share.
+int logprob_shape(int dtype, const void* logits, int64_t N, int64_t V, int64_t ld, const int32_t* ids, int64_t T) {
+  if (!dtype_ok(dtype) || N < 0 || V <= 0 || ld < 0 || T < 0) return CKL_EINVAL;
+  if (V > (int64_t)1 << 26 || N >= kMaxSampleRows || T > kMaxK) return CKL_EUNSUPPORTED;
+  if (!aligned(logits, dtype == CKL_DTYPE_BF16 ? 2 : 4) || !aligned(ids, 4)) return CKL_EINVAL;
+  if (N > 0 && (!logits || (T > 0 && !ids))) return CKL_EINVAL;
+  return CKL_OK;
+}
+
+// Device workspace of a call on hidden states with chunks of C rows.
+struct HeadLayout {
+  int64_t C = 0, pblk = 0;
+  int n_slices = 0, splits = 0;
+  bool tiled = false;  // backward: a tiled copy of W
+  uint64_t live_off = 0, hc_off = 0, vidx_off = 0, pos_off = 0, part_off = 0, parta_off = 0, w_off = 0, g_off = 0,
+           coef_off = 0, slab_off = 0, dw_off = 0, total = 0;
+};
+
+// Rows from which the backward call copies W into tiles.
+constexpr int64_t kTileCopyRows = 8192;
+
+HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C, size_t esz, bool dw_sum) {
+  HeadLayout L;
+  L.C = C;
+  L.pblk = tile_row_stride(V);
+  L.n_slices = (int)((V + 127) / 128);
+  uint64_t off = 0;
+  const auto take = [&off](uint64_t bytes) {
+    const uint64_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.live_off = take(4);
+  L.hc_off = take((uint64_t)C * d * esz);
+  L.vidx_off = take((uint64_t)C * 4);
+  L.pos_off = take((uint64_t)C * 4);
+  if (!backward) {
+    L.part_off = take((uint64_t)C * L.n_slices * 8);
+    L.parta_off = take((uint64_t)C * L.n_slices * 4);
+  } else {
+    L.tiled = N >= kTileCopyRows;
+    if (L.tiled) L.w_off = take((uint64_t)((V + 63) / 64) * tile_row_stride(d) * esz);
+    L.splits = dh_splits(esz == 2 ? DT_BF16 : DT_F32, C, d, V);
+    L.g_off = take((uint64_t)((C + 63) / 64) * L.pblk * esz);
+    L.coef_off = take((uint64_t)C * 16);
+    L.slab_off = take((uint64_t)L.splits * C * d * 4);
+    if (dw_sum && C < N) L.dw_off = take((uint64_t)V * d * 4);  // a bf16 dW's sums over chunks
+  }
+  L.total = off;
+  return L;
+}
+
+int head_plan(bool backward, int dtype, int dw_dtype, int64_t N, int64_t d, int64_t V, int64_t chunk, uint64_t budget,
+              HeadLayout* out) {
+  if (!dtype_ok(dtype) || N < 0 || d <= 0 || V <= 0 || chunk < 0) return CKL_EINVAL;
+  if (backward && (!dtype_ok(dw_dtype) || (dw_dtype == CKL_DTYPE_BF16 && dtype != CKL_DTYPE_BF16))) return CKL_EINVAL;
+  if (d % 8 != 0 || V > (int64_t)1 << 26 || N > (int64_t)1 << 26 || d > (int64_t)1 << 20) return CKL_EUNSUPPORTED;
+  *out = HeadLayout{};
+  if (N == 0) return CKL_OK;
+  budget = budget_from_env(budget);
+  const size_t esz = dtype == CKL_DTYPE_BF16 ? 2 : 4;
+  const bool sum = backward && dw_dtype == CKL_DTYPE_BF16;
+  // rows per chunk at most: 2^22 tiles of 256 x 256, so that a launch stays below 2^32 threads
+  const int64_t most_tiles = ((int64_t)1 << 22) / ((V + 255) / 256);
+  const int64_t most = most_tiles >= kMaxChunk / 256 ? kMaxChunk : most_tiles * 256;
+  if (chunk > 0) {
+    const int64_t C = chunk < N ? chunk : N;
+    if (C > most) return CKL_EUNSUPPORTED;
+    const HeadLayout L = head_layout(backward, N, d, V, C, esz, sum);
+    if (L.total > budget) return CKL_EBUDGET;
+    *out = L;
+    return CKL_OK;
+  }
+  // the fewest chunks of a multiple of 256 rows (or all rows) that fit
+  int64_t C = N < most ? N : most;
+  while (true) {
+    const HeadLayout L = head_layout(backward, N, d, V, C, esz, sum);
+    if (L.total <= budget) {
+      *out = L;
+      return CKL_OK;
+    }
+    if (C <= kRowStep) return CKL_EBUDGET;
+    // even chunks, one more than now (N / 256 steps at most; far fewer, as C falls with 1 / chunks)
+    const int64_t next = roundup((N + (N + C - 1) / C) / ((N + C - 1) / C + 1), kRowStep);
+    C = next < C ? next : (C - 1) / kRowStep * kRowStep;
+  }
+}
+
+// One call on hidden states: the shared chunk loop.  `grad` null: forward.
+struct HeadCall {
+  Dtype dt;
+  size_t esz;
+  const uint8_t* mask;
+  char* ws;
+};
+struct Chunk {
+  const void* Hc;
+  const int *vidx, *pos, *live;
+};
+hipError_t head_chunk(const HeadCall& c, const HeadLayout& L, const void* H, int64_t d, int64_t r0, int64_t rows,
+                      float* zero_out, Chunk* out, hipStream_t s) {
+  *out = Chunk{(const char*)H + (size_t)r0 * d * c.esz, nullptr, nullptr, nullptr};
+  if (!c.mask) return hipSuccess;
+  int* live = (int*)(c.ws + L.live_off);
+  int* vidx = (int*)(c.ws + L.vidx_off);
+  int* pos = (int*)(c.ws + L.pos_off);
+  const hipError_t e = launch_compact(c.dt, c.mask + r0, rows, L.C, out->Hc, d, nullptr, nullptr, 0, vidx, pos, live,
+                                      zero_out, nullptr, c.ws + L.hc_off, nullptr, nullptr, s);
+  *out = Chunk{c.ws + L.hc_off, vidx, pos, live};
+  return e;
 }
 
 // A caller's dropout settings as the kernels take them; NULL drops nothing.
@@ -783,6 +896,194 @@ int ckl_matmul_fp8(int out_dtype, const uint8_t* xq, const float* xs, const uint
   try {
     Timed t(T_FP8, stream);
     CKL_TRY(launch_matmul_fp8(to_dt(out_dtype), xq, xs, wq, ws, M, V, d, out, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_logprobs_workspace(int64_t N, int64_t V, int64_t top, uint64_t* bytes_out) {
+  if (!bytes_out || N < 0 || V <= 0 || top < 0 || top > V) return CKL_EINVAL;
+  if (V > (int64_t)1 << 26 || N >= kMaxSampleRows || top > kMaxTop) return CKL_EUNSUPPORTED;
+  *bytes_out = align256(logprob_workspace(N, V, (int)top));
+  return CKL_OK;
+}
+
+int ckl_logprobs(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const int32_t* ids, int64_t T,
+                 const uint8_t* mask, int64_t top, float* logp, float* entropy, float* stats, int32_t* top_ids,
+                 float* top_logp, void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  const int st = logprob_shape(dtype, logits, N, V, row_stride, ids, T);
+  if (st != CKL_OK) return st;
+  if (top < 0 || top > V) return CKL_EINVAL;
+  if (top > kMaxTop) return CKL_EUNSUPPORTED;
+  if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(stats, 4) || !aligned(top_ids, 4) || !aligned(top_logp, 4))
+    return CKL_EINVAL;
+  if (N == 0) return CKL_OK;
+  if ((T > 0 && !logp) || !entropy || !stats || (top > 0 && (!top_ids || !top_logp))) return CKL_EINVAL;
+  const uint64_t need = logprob_workspace(N, V, (int)top);
+  if (workspace && (!aligned(workspace, 256) || workspace_bytes < need)) return CKL_EINVAL;
+  LogprobArgs p{};
+  p.x = logits;
+  p.N = N;
+  p.V = V;
+  p.ld = row_stride;
+  p.ids = ids;
+  p.T = (int)T;
+  p.top = (int)top;
+  p.mask = mask;
+  p.logp = logp;
+  p.entropy = entropy;
+  p.stats = stats;
+  p.top_ids = top_ids;
+  p.top_logp = top_logp;
+  try {
+    Timed t(T_LOGPROB, stream);
+    CKL_TRY(launch_logprob(to_dt(dtype), p, need ? workspace : nullptr, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_logprobs_bwd(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const int32_t* ids,
+                     int64_t T, const uint8_t* mask, const float* stats, const float* entropy, const float* dlogp,
+                     const float* dentropy, void* dlogits, int64_t out_stride, hipStream_t stream) {
+  const int st = logprob_shape(dtype, logits, N, V, row_stride, ids, T);
+  if (st != CKL_OK) return st;
+  if (out_stride < V) return CKL_EINVAL;
+  if (!aligned(stats, 4) || !aligned(entropy, 4) || !aligned(dlogp, 4) || !aligned(dentropy, 4) ||
+      !aligned(dlogits, dtype == CKL_DTYPE_BF16 ? 2 : 4))
+    return CKL_EINVAL;
+  if (logprob_grad_blocks(N, V) >= kMaxBlocks256) return CKL_EUNSUPPORTED;
+  if (N == 0) return CKL_OK;
+  if (!stats || !dlogits || (T > 0 && !dlogp) || (dentropy && !entropy)) return CKL_EINVAL;
+  if (dlogits == logits && N > 1 && out_stride != row_stride) return CKL_EINVAL;
+  LogprobGradArgs p{};
+  p.x = logits;
+  p.N = N;
+  p.V = V;
+  p.ld = row_stride;
+  p.ldo = out_stride;
+  p.ids = ids;
+  p.T = (int)T;
+  p.mask = mask;
+  p.stats = stats;
+  p.entropy = entropy;
+  p.dlogp = dlogp;
+  p.dentropy = dentropy;
+  p.out = dlogits;
+  try {
+    Timed t(T_LOGPROB, stream);
+    CKL_TRY(launch_logprob_grad(to_dt(dtype), p, stream));
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_head_logprobs_plan(int backward, int dtype, int dw_dtype, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                           uint64_t budget_bytes, int64_t* chunk_out, uint64_t* workspace_bytes_out) {
+  if (backward != 0 && backward != 1) return CKL_EINVAL;
+  try {
+    HeadLayout L;
+    const int st = head_plan(backward != 0, dtype, dw_dtype, N, d, V, chunk, budget_bytes, &L);
+    if (st != CKL_OK) return st;
+    if (chunk_out) *chunk_out = L.C;
+    if (workspace_bytes_out) *workspace_bytes_out = L.total;
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EINVAL;
+  }
+}
+
+int ckl_head_logprobs(int dtype, const void* H, const void* W, const int32_t* ids, const uint8_t* mask, int64_t N,
+                      int64_t d, int64_t V, int64_t T, int64_t chunk, float* logp, float* entropy, float* stats,
+                      void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  try {
+    HeadLayout L;
+    const int st = head_plan(false, dtype, 0, N, d, V, chunk, 0, &L);
+    if (st != CKL_OK) return st;
+    if (T < 0) return CKL_EINVAL;
+    if (T > kMaxK || N * T > (int64_t)1 << 26) return CKL_EUNSUPPORTED;
+    if (!aligned(H, 16) || !aligned(W, 16) || !aligned(ids, 4) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+        !aligned(stats, 4) || !aligned(workspace, 256))
+      return CKL_EINVAL;
+    if (N == 0) return CKL_OK;
+    if (!H || !W || (T > 0 && (!ids || !logp)) || !entropy || !stats || !workspace || workspace_bytes < L.total)
+      return CKL_EINVAL;
+    char* ws = (char*)workspace;
+    const HeadCall c{to_dt(dtype), dtype == CKL_DTYPE_BF16 ? (size_t)2 : (size_t)4, mask, ws};
+    const HeadArgs p{H, W, N, d, V, ids, (int)T, mask, logp, entropy, stats};
+    float2* part = (float2*)(ws + L.part_off);
+    float* part_a = (float*)(ws + L.parta_off);
+    TraceRange range("ckl head logprobs N=%lld d=%lld V=%lld T=%lld chunk=%lld", (long long)N, (long long)d, (long long)V,
+                     (long long)T, (long long)L.C);
+    Timed t(T_LOGPROB, stream);
+    if (T > 0) CKL_TRY(launch_given_logits(c.dt, p, stream));
+    for (int64_t r0 = 0; r0 < N; r0 += L.C) {
+      const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
+      Chunk k;
+      CKL_TRY(head_chunk(c, L, H, d, r0, rows, entropy + r0, &k, stream));
+      CKL_TRY(launch_head_stats(c.dt, p, k.Hc, rows, part, part_a, L.n_slices, k.live, stream));
+      CKL_TRY(launch_head_rows(p, r0, rows, part, part_a, L.n_slices, k.pos, stream));
+    }
+    return CKL_OK;
+  } catch (...) {
+    return CKL_EHIP;
+  }
+}
+
+int ckl_head_logprobs_bwd(int dtype, const void* H, const void* W, const int32_t* ids, const uint8_t* mask, int64_t N,
+                          int64_t d, int64_t V, int64_t T, int64_t chunk, const float* logp, const float* entropy,
+                          const float* stats, const float* dlogp, const float* dentropy, void* dH, int dw_dtype,
+                          int accumulate, void* dW, void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  try {
+    HeadLayout L;
+    const int st = head_plan(true, dtype, dw_dtype, N, d, V, chunk, 0, &L);
+    if (st != CKL_OK) return st;
+    if (T < 0 || (accumulate != 0 && accumulate != 1) || (accumulate && dw_dtype != CKL_DTYPE_F32)) return CKL_EINVAL;
+    if (T > kMaxK || N * T > (int64_t)1 << 26) return CKL_EUNSUPPORTED;
+    if (!aligned(H, 16) || !aligned(W, 16) || !aligned(ids, 4) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+        !aligned(stats, 4) || !aligned(dlogp, 4) || !aligned(dentropy, 4) || !aligned(dH, 16) || !aligned(dW, 16) ||
+        !aligned(workspace, 256))
+      return CKL_EINVAL;
+    if (!dW) return CKL_EINVAL;
+    const bool round = dw_dtype == CKL_DTYPE_BF16;
+    if (N == 0) {  // V d is a multiple of 8: a bf16 dW is whole 32-bit words
+      if (!accumulate) CKL_TRY(launch_fill_f32((float*)dW, round ? V * d / 2 : V * d, 0.f, stream));
+      return CKL_OK;
+    }
+    if (!H || !W || !stats || !dH || (T > 0 && (!ids || !logp || !dlogp)) || (dentropy && !entropy) || !workspace ||
+        workspace_bytes < L.total)
+      return CKL_EINVAL;
+    char* ws = (char*)workspace;
+    const HeadCall c{to_dt(dtype), dtype == CKL_DTYPE_BF16 ? (size_t)2 : (size_t)4, mask, ws};
+    const HeadGradArgs p{N, d, V, ids, (int)T, logp, stats, entropy, dlogp, dentropy};
+    void* G = ws + L.g_off;
+    float4* coef = (float4*)(ws + L.coef_off);
+    float* slab = (float*)(ws + L.slab_off);
+    float* sums = round ? (L.C < N ? (float*)(ws + L.dw_off) : nullptr) : (float*)dW;
+    const void* Wt = L.tiled ? ws + L.w_off : W;
+    TraceRange range("ckl head logprobs backward N=%lld d=%lld V=%lld T=%lld chunk=%lld", (long long)N, (long long)d,
+                     (long long)V, (long long)T, (long long)L.C);
+    Timed t(T_LOGPROB, stream);
+    if (L.tiled) CKL_TRY(launch_tile_copy(c.dt, W, V, d, ws + L.w_off, stream));
+    for (int64_t r0 = 0; r0 < N; r0 += L.C) {
+      const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
+      Chunk k;
+      // (the compaction writes a zero per masked row somewhere: the rows' coefficients, written after it)
+      CKL_TRY(head_chunk(c, L, H, d, r0, rows, (float*)coef, &k, stream));
+      CKL_TRY(launch_head_grad(c.dt, p, Wt, L.tiled, k.Hc, r0, rows, k.vidx, k.live, coef, G, L.pblk, stream));
+      int splits = dh_splits(c.dt, rows, d, V);
+      const int64_t cap = (int64_t)L.splits * L.C / rows;  // slab capacity in splits of this chunk
+      if (splits > cap) splits = dh_fit_splits(c.dt, V, (int)cap);
+      CKL_TRY(launch_dh(c.dt, G, L.pblk, Wt, V, d, rows, slab, splits, k.live, stream, L.tiled));
+      CKL_TRY(launch_dh_reduce(c.dt, slab, splits, rows, d, k.pos, (char*)dH + (size_t)r0 * d * c.esz, stream));
+      if (round && r0 + rows >= N)
+        CKL_TRY(launch_dw_round(G, L.pblk, k.Hc, V, d, rows, r0 > 0 ? sums : nullptr, dW, k.live, stream));
+      else
+        CKL_TRY(launch_dw(c.dt, G, L.pblk, k.Hc, V, d, rows, sums, r0 > 0 || accumulate ? 1 : 0, k.live, stream));
+    }
     return CKL_OK;
   } catch (...) {
     return CKL_EHIP;

@@ -80,6 +80,9 @@ enum EpilogueKind : int {
   EPI_LOGITS = 0,  // per (n, 128-row slice of m): mx = max D, P[n][m] = exp(D[m][n] - mx), (mx, sum P)
   EPI_SLAB = 1,    // out[m][n] = D[m][n] (fp32), one slab per k-split
   EPI_ACCUM = 2,   // out[m][n] = D[m][n] (beta = 0) or out[m][n] += D[m][n] (beta = 1)
+  EPI_STATS = 3,   // per (n, 128-row slice of m): mx = max D, (mx, sum exp(D - mx)) and sum exp(D - mx) (D - mx)
+  EPI_GRAD = 4,    // out[n][m] = -p (c + u l), l = log p = D[m][n] - max - log sum, by the row's coefficients
+  EPI_ROUND = 5,   // out[m][n] = D[m][n], plus old[m][n] where given, rounded to bf16
 };
 
 struct GemmParams {
@@ -89,12 +92,12 @@ struct GemmParams {
   int splits;            // k-splits; each covers k_tiles_per_split k-steps
   int k_tiles_per_split;
   int group_m;           // m-tiles per group in the tile order
-  void* out;             // EPI_LOGITS: exp values (tiled, element type T); else fp32 slab base or dW
-  int64_t ldo;           // EPI_LOGITS: elements between tile rows of out; else row stride
+  void* out;             // EPI_LOGITS, EPI_GRAD: tiled, element type T; EPI_ROUND: bf16; else fp32 slab base or dW
+  int64_t ldo;           // tiled out: elements between its tile rows; else row stride
   int64_t split_stride;  // elements between k-split slabs (EPI_SLAB)
   int64_t valid_m, valid_n;  // stores are limited to m < valid_m, n < valid_n
-  float2* part;          // EPI_LOGITS: partial (max, sum exp) per [n][slice]
-  int n_slices;          // EPI_LOGITS: slices per row of part
+  float2* part;          // EPI_LOGITS, EPI_STATS: partial (max, sum exp) per [n][slice]
+  int n_slices;          // slices per row of part
   int beta;              // EPI_ACCUM
   // Device int or null: the chunk's rows (tokens) at and after *live are all
   // masked.  Logits tiles of those rows return at once, dH tiles of them
@@ -122,6 +125,13 @@ struct GemmParams {
   const int* g_rowmap;
   const float* g_scale;
   const float* g_gscale;
+  // EPI_STATS: the third sum, per [n][slice] beside part
+  float* part_a;
+  // EPI_GRAD: (max, log sum, c, u) of row n; rows at and past valid_n (and
+  // *live) and ids at and past valid_m get zeros
+  const float4* coef;
+  // EPI_ROUND: fp32 values to add, laid out as out, or null
+  const float* old;
 };
 
 // ---------------------------------------------------------------- LDS layouts
@@ -503,12 +513,13 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
   typedef SlabDMA<T, BM, NW, AK, KB> DA;
   typedef SlabDMA<T, BN, NW, BKM, KB> DB;
   constexpr int NIT = DA::kNI + DB::kNI;  // this wave's loads per slab
-  static_assert(MS == 32 || (MS == 16 && sizeof(T) == 2 && AK && BKM && EPI == EPI_LOGITS),
+  constexpr bool kLogits = EPI == EPI_LOGITS || EPI == EPI_STATS || EPI == EPI_GRAD;  // D = logits, m = ids, n = rows
+  static_assert(MS == 32 || (MS == 16 && sizeof(T) == 2 && AK && BKM && kLogits),
                 "16 x 16 blocks: bf16 logits (both operands k-major) only");
   static_assert(WTM % MS == 0 && WTN % MS == 0, "wave tile must be a multiple of the MFMA block");
   static_assert(SUB % 2 == 0 && SUB >= 2, "the pipeline assumes an even sub-step count");
   static_assert(NS >= 2 && (NS - 1) * NIT < 64, "stages in flight must fit the vmcnt counter");
-  static_assert(EPI != EPI_LOGITS || WTM == 128, "logit partials are per 128-row slice");
+  static_assert(!kLogits || WTM == 128, "logit partials are per 128-row slice");
   constexpr int STAGE = DA::kBytes + DB::kBytes;
   constexpr int SPARE = DA::kSpare > DB::kSpare ? DA::kSpare : DB::kSpare;
   constexpr int XOFF = NS * STAGE + SPARE;  // id tables (logits only)
@@ -528,7 +539,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
   int kt_end = min(p.k_tiles, kt_begin + p.k_tiles_per_split);
   if (p.live != nullptr) {
     const int lv = __builtin_amdgcn_readfirstlane(*p.live);
-    if constexpr (EPI == EPI_LOGITS) {
+    if constexpr (kLogits) {
       if (n0 >= lv) return;  // whole workgroup: no barrier reached yet
     } else if constexpr (EPI == EPI_SLAB) {
       if (m0 >= lv) kt_end = kt_begin;  // the epilogue writes this tile's zeros
@@ -692,7 +703,136 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
   const int h = lane >> 5, col = lane & 31;
   const int64_t mw = m0 + wm * WTM, nw = n0 + wn * WTN;
   const bool full = (mw + WTM <= p.valid_m) && (nw + WTN <= p.valid_n);
-  if constexpr (MS == 16) {
+  if constexpr (EPI == EPI_STATS || EPI == EPI_GRAD) {
+    // Rows of D are ids, columns are tokens; a lane holds, of each block, runs
+    // of four consecutive ids of one token: run q of block i starts at wave row
+    // 32 i + 8 q + 4 h (32 x 32 blocks) or 16 i + 4 g (16 x 16, g = lane / 16).
+    constexpr int RUNS = NR / 4;
+    const int cl = lane & (MS - 1), sub = lane / MS;
+    const int vm = (int)(p.valid_m < (int64_t)0x7FFFFFFF ? p.valid_m : (int64_t)0x7FFFFFFF);
+    const bool mfull = mw + WTM <= p.valid_m;
+    auto run0 = [&](int i, int q) { return MS == 32 ? 32 * i + 8 * q + 4 * sub : 16 * i + 4 * sub; };
+    if constexpr (EPI == EPI_STATS) {
+      const int slice = (int)(mw / 128);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int64_t n = nw + MS * j + cl;
+        if (!mfull) {  // ids past the vocabulary weigh nothing
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+              if ((int)mw + run0(i, r / 4) + r % 4 >= vm) acc[i][j][r] = -INFINITY;
+        }
+        float mx = -INFINITY, s = 0.f, a = 0.f;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) mx = fmaxf(mx, acc[i][j][r]);
+#pragma unroll
+        for (int o = MS; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+        // z - mx is held at -1000, whose exponential is 0: 0 x -inf never arises; NaN stays
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float t = __builtin_elementwise_maximum(acc[i][j][r] - mx, -1000.f);
+            const float e = __builtin_amdgcn_exp2f(t * kLog2e);
+            s += e;
+            a = __builtin_fmaf(e, t, a);
+          }
+#pragma unroll
+        for (int o = MS; o < 64; o <<= 1) {
+          s += __shfl_xor(s, o);
+          a += __shfl_xor(a, o);
+        }
+        if (sub == 0 && n < p.valid_n && slice < p.n_slices) {
+          p.part[n * p.n_slices + slice] = make_float2(mx, s);
+          p.part_a[n * p.n_slices + slice] = a;
+        }
+      }
+    } else {
+      const int live = p.live != nullptr ? __builtin_amdgcn_readfirstlane(*p.live) : 0x7FFFFFFF;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int64_t n = nw + MS * j + cl;
+        const bool rok = n < p.valid_n && n < live;
+        const float4 c = rok ? p.coef[n] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float l = __builtin_elementwise_maximum((acc[i][j][r] - c.x) - c.y, -1000.f);
+            const float g = -__builtin_amdgcn_exp2f(l * kLog2e) * __builtin_fmaf(c.w, l, c.z);
+            acc[i][j][r] = rok && (mfull || (int)mw + run0(i, r / 4) + r % 4 < vm) ? g : 0.f;
+          }
+      }
+      if constexpr (sizeof(T) == 2) {
+        // through the wave's 16 KiB of LDS, as 16 coalesced 1 KiB stores (see the logits epilogue below)
+        static_assert(WTM == 128 && WTN == 64 && NW * 16384 <= NS * STAGE, "one wave = two 64 x 64 tiles");
+        typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
+        __syncthreads();
+        char* wl = smem + wave * 16384;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int t = MS * j + cl;
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int q = 0; q < RUNS; ++q) {
+              const int o = run0(i, q) & 63, vb = (MS == 32 ? 32 * i : 16 * i) >> 6;
+              const bf16x4 v = {(__bf16)acc[i][j][4 * q], (__bf16)acc[i][j][4 * q + 1], (__bf16)acc[i][j][4 * q + 2],
+                                (__bf16)acc[i][j][4 * q + 3]};
+              *(bf16x4*)(wl + vb * 8192 + t * 128 + (((o >> 3) ^ (t & 7)) << 4) + 2 * (o & 4)) = v;
+            }
+        }
+        __syncthreads();
+        if (nw < p.valid_n) {
+          T* tile0 = (T*)p.out + (nw >> 6) * p.ldo + (mw >> 6) * 4096;
+#pragma unroll
+          for (int sidx = 0; sidx < 16; ++sidx) {
+            const int idx = sidx * 64 + lane;
+            const int vb = idx >> 9, t = (idx >> 3) & 63, cc = idx & 7;
+            if (mw + 64 * vb < p.valid_m)
+              *(u32x4*)(tile0 + vb * 4096 + t * 64 + cc * 8) =
+                  *(const u32x4*)(wl + vb * 8192 + t * 128 + ((cc ^ (t & 7)) << 4));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int64_t n = nw + MS * j + cl;
+          if (n >= p.valid_n) continue;
+          T* prow = (T*)p.out + (n >> 6) * p.ldo + (n & 63) * 64;
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int q = 0; q < RUNS; ++q) {
+              const int64_t m = mw + run0(i, q);
+              if (m < p.valid_m)
+                *(f32x4*)(prow + (m >> 6) * 4096 + (m & 63)) =
+                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            }
+        }
+      }
+    }
+  } else if constexpr (EPI == EPI_ROUND) {
+    __bf16* out = (__bf16*)p.out;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int64_t n = nw + j * 32 + col;
+        if (!full && n >= p.valid_n) continue;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t m = mw + i * 32 + (r >> 2) * 8 + h * 4 + (r & 3);
+          if (!full && m >= p.valid_m) continue;
+          const float v = acc[i][j][r];
+          out[m * p.ldo + n] = (__bf16)(p.old != nullptr ? p.old[m * p.ldo + n] + v : v);
+        }
+      }
+  } else if constexpr (MS == 16) {
     // Logits from 16 x 16 blocks: lane l, slot r of block (i, j) holds the
     // logit of id mw + 16 i + 4 g + r (g = l / 16) and token nw + 16 j + c
     // (c = l % 16), so the four lanes c, c + 16, c + 32, c + 48 hold a token's

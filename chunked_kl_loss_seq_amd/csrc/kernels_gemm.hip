@@ -48,13 +48,14 @@ int dh_fit_splits(Dtype dt, int64_t V, int s) {
 }
 
 hipError_t launch_dh(Dtype dt, const void* G, int64_t gblk, const void* Wt, int64_t V, int64_t d, int64_t rows,
-                     float* slab, int splits, const int* live, hipStream_t s) {
+                     float* slab, int splits, const int* live, hipStream_t s, bool tiled) {
   const int bn = d_tile(dt, d);
   const int bk = dt == DT_BF16 ? 64 : 32;
   GemmParams p{};
   p.live = live;
   p.a = Operand{G, 0, rows, V, gblk};  // tiled: storage row = token, column = vocabulary id
-  p.b = Operand{Wt, 0, d, V, tile_row_stride(d)};  // tiled: storage row = vocabulary id (k), column = d (n)
+  // storage row = vocabulary id (k), column = d (n)
+  p.b = tiled ? Operand{Wt, 0, d, V, tile_row_stride(d)} : Operand{Wt, d, d, V, 0};
   p.tiles_m = cdiv64(rows, 256);
   p.tiles_n = cdiv64(d, bn);
   p.k_tiles = cdiv64(V, bk);

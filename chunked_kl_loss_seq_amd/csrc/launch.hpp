@@ -66,9 +66,9 @@ hipError_t launch_logits(Dtype dt, const void* Wt, const void* Hc, int64_t V, in
 
 // dH partial slabs of one chunk: slab[s][n][j] = sum over the s-th vocabulary
 // split of G[n][v] W[v][j].  G is tiled like P, tile rows gblk elements apart;
-// Wt is the tiled copy of the weight.
+// Wt is the tiled copy of the weight, or the row-major weight where `tiled` is false.
 hipError_t launch_dh(Dtype dt, const void* G, int64_t gblk, const void* Wt, int64_t V, int64_t d, int64_t rows,
-                     float* slab, int splits, const int* live, hipStream_t s);
+                     float* slab, int splits, const int* live, hipStream_t s, bool tiled = true);
 // dH rows = sum of the slabs in split order, rounded once to the output type.
 // With pos (compacted chunk), dH row j takes slab row pos[j], or zeros if -1.
 hipError_t launch_dh_reduce(Dtype dt, const float* slab, int splits, int64_t rows, int64_t d, const int* pos,
@@ -173,6 +173,84 @@ hipError_t launch_add_norm(Dtype dt, const NormArgs& p, hipStream_t s);
 uint64_t add_norm_bwd_workspace(int64_t N, int64_t d, int sums);
 hipError_t launch_add_norm_bwd(Dtype dt, const NormArgs& p, const NormGrads& q, hipStream_t s);
 
+// Log-probabilities of given tokens, entropy and alternatives of rows of logits,
+// and their gradient, see kernels_logprob.hip.
+struct LogprobArgs {
+  const void* x;        // [N, V], rows ld elements apart
+  int64_t N, V, ld;
+  const int32_t* ids;   // [N, T]
+  int T, top;
+  const uint8_t* mask;  // [N] or null
+  float* logp;          // [N, T]
+  float* entropy;       // [N]
+  float* stats;         // [2, N]: largest logit, log of the sum of exp(z - largest)
+  int32_t* top_ids;     // [N, top]
+  float* top_logp;      // [N, top]
+  int slices;           // of a row, `per` logits each (set by the launcher, as what follows)
+  int64_t per;
+  float4* part;         // [N, slices] (largest, reference, sum, weighted sum)
+  void* pairs;          // [N, slices, top] 64-bit (key, id) pairs
+};
+uint64_t logprob_workspace(int64_t N, int64_t V, int top);
+// ws of logprob_workspace bytes, or null: rows are then not split.
+hipError_t launch_logprob(Dtype dt, LogprobArgs p, void* ws, hipStream_t s);
+
+struct LogprobGradArgs {
+  const void* x;           // [N, V], rows ld elements apart
+  int64_t N, V, ld, ldo;
+  const int32_t* ids;      // [N, T]
+  int T;
+  const uint8_t* mask;     // [N] or null
+  const float* stats;      // [2, N]
+  const float* entropy;    // [N], or null without dentropy
+  const float* dlogp;      // [N, T]
+  const float* dentropy;   // [N] or null
+  void* out;               // [N, V], rows ldo elements apart; may be x
+  int64_t runs;            // workgroups of a row (set by the launcher)
+};
+hipError_t launch_logprob_grad(Dtype dt, LogprobGradArgs p, hipStream_t s);
+int64_t logprob_grad_blocks(int64_t N, int64_t V);  // its workgroups, of 256 threads
+
+// The same from hidden states H [N, d] and the head's weight W [V, d], see kernels_head.hip.
+struct HeadArgs {
+  const void *H, *W;
+  int64_t N, d, V;
+  const int32_t* ids;   // [N, T]
+  int T;
+  const uint8_t* mask;  // [N] or null
+  float* logp;          // [N, T]
+  float* entropy;       // [N]
+  float* stats;         // [2, N]
+};
+// logp[n][t] = H_n . W_id for ids in [0, V) of rows that count.
+hipError_t launch_given_logits(Dtype dt, const HeadArgs& p, hipStream_t s);
+// The slices' statistics of a chunk of rows Hc (all of them, or the *live compacted ones).
+hipError_t launch_head_stats(Dtype dt, const HeadArgs& a, const void* Hc, int64_t rows, float2* part, float* part_a,
+                             int n_slices, const int* live, hipStream_t s);
+// Entropy, stats and log-probabilities of rows [r0, r0 + rows); pos: of a compacted chunk, or null.
+hipError_t launch_head_rows(const HeadArgs& p, int64_t r0, int64_t rows, const float2* part, const float* part_a,
+                            int n_slices, const int* pos, hipStream_t s);
+struct HeadGradArgs {
+  int64_t N, d, V;
+  const int32_t* ids;      // [N, T]
+  int T;
+  const float* logp;       // [N, T]
+  const float* stats;      // [2, N]
+  const float* entropy;    // [N], or null without dentropy
+  const float* dlogp;      // [N, T]
+  const float* dentropy;   // [N] or null
+};
+// G of a chunk (tiled, tile rows gblk elements apart); W row-major, or its tiled copy; coef: [rows].
+hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, bool tiled, const void* Hc, int64_t r0,
+                            int64_t rows, const int* vidx, const int* live, float4* coef, void* G, int64_t gblk,
+                            hipStream_t s);
+// bf16 dW = G^T H_c, plus the fp32 `old` where given (bf16 operands).
+hipError_t launch_dw_round(const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
+                           const float* old, void* dW, const int* live, hipStream_t s);
+
+constexpr int kMaxK = 2048;
+constexpr int kMaxTop = 512;  // alternatives of a row
+
 // Valid-token count n and scale 1/n (0 if n = 0) into scal (int64 n, float s).
 hipError_t launch_mask_count(const uint8_t* mask, int64_t N, void* scal, hipStream_t s);
 // Compaction of the chunk whose mask, H rows, ids and teacher logits start at
@@ -232,7 +310,6 @@ hipError_t launch_untile(Dtype g_dt, const void* P, int64_t pblk, int64_t rows, 
 // loss = s * sum of kl[0..N) in a fixed order, accumulated in double.
 hipError_t launch_finalize(const float* kl, int64_t N, const void* scal, float* out_loss, hipStream_t s);
 
-constexpr int kMaxK = 2048;
 // byte offsets, in the device scalar block, of the gradient weight 1 / n_valid
 // (fp32) and of the input-check flags (bit 0: a cached id outside [0, V);
 // bit 1: an id repeated within a row)

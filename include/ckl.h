@@ -308,6 +308,84 @@ int ckl_quantize_fp8(int dtype, const void* x, int64_t R, int64_t C, int64_t blo
 int ckl_matmul_fp8(int out_dtype, const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
                    int64_t V, int64_t d, void* out, hipStream_t stream);
 
+/* Log-probabilities of given tokens, entropy and the most likely alternatives of
+ * rows of logits.  Of a row z, with M its largest logit and L = log sum exp(z - M):
+ *   logp[t]  = z[ids[t]] - M - L      entropy = -sum p log p, p = exp(z - M - L)
+ *   top      the `top` largest logits, ordered as ckl_topk orders them, with their
+ *            log-probabilities
+ *   dtype      ckl_dtype of logits
+ *   logits     [N, V], rows row_stride >= 0 elements apart, elements of a row
+ *              adjacent, aligned to an element.  -inf has probability 0 and adds
+ *              nothing to the entropy; a row of nothing else has entropy 0 and
+ *              log-probabilities -inf.  NaN or +inf makes its row's logp, entropy,
+ *              stats (L) and top_logp NaN
+ *   ids        int32 [N, T]; an id outside [0, V) is an entry without a token: its
+ *              logp is 0.  NULL with T = 0
+ *   mask       uint8 [N], 0 = the row is not read: its outputs are 0 and its
+ *              top_ids -1; NULL: every row counts
+ *   logp       fp32 [N, T];  entropy fp32 [N]
+ *   stats      fp32 [2, N]: M and L, for the gradient (M + L is the log-normaliser)
+ *   top_ids    int32 [N, top], top_logp fp32 [N, top]; -1 and -inf where a row has
+ *              fewer logits above -inf (NaN is never one).  NULL with top = 0
+ *   workspace  NULL, or at least ckl_logprobs_workspace bytes (0 for most shapes),
+ *              256-byte aligned, not shared by calls that may overlap: with it,
+ *              rows of a small batch are split over several workgroups
+ * T <= 2048, top <= min(V, 512), V <= 2^26, N < 2^22.  Sums are fp32, with or
+ * without a workspace in an order of their own. */
+int ckl_logprobs(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const int32_t* ids, int64_t T,
+                 const uint8_t* mask, int64_t top, float* logp, float* entropy, float* stats, int32_t* top_ids,
+                 float* top_logp, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+int ckl_logprobs_workspace(int64_t N, int64_t V, int64_t top, uint64_t* bytes_out);
+
+/* Gradient of sum_t dlogp[t] logp[t] + dentropy entropy with respect to the logits:
+ *   dz_j = (sum of dlogp over the entries with id j) - p_j (W + dentropy (log p_j + entropy)),
+ * W the sum of dlogp over the row's entries with a token.  logits, ids, mask, stats
+ * and entropy are the forward call's.
+ *   dlogp     fp32 [N, T], NULL with T = 0;  dentropy fp32 [N] or NULL for zeros
+ *             (entropy may then be NULL)
+ *   dlogits   [N, V] in dtype, rows out_stride >= V elements apart; may be logits
+ *             with the same stride.  Masked rows and rows without a logit above
+ *             -inf are zeros
+ * The same id may be given several times.  N, V and T as above, and N x (V in runs
+ * of 8,192) below 2^24.  No workspace. */
+int ckl_logprobs_bwd(int dtype, const void* logits, int64_t N, int64_t V, int64_t row_stride, const int32_t* ids,
+                     int64_t T, const uint8_t* mask, const float* stats, const float* entropy, const float* dlogp,
+                     const float* dentropy, void* dlogits, int64_t out_stride, hipStream_t stream);
+
+/* The same from hidden states, for logits z = H W^T that are never held: rows go in
+ * chunks, as in the loss calls.
+ *   dtype      ckl_dtype of H [N, d] and W [V, d], 16-byte aligned
+ *   ids, mask, logp, entropy, stats   as for ckl_logprobs (masked rows cost no
+ *              contraction)
+ *   chunk      rows per chunk, 0 = what ckl_head_logprobs_plan chooses
+ *   workspace  at least the bytes that ckl_head_logprobs_plan gives for this call,
+ *              256-byte aligned, need not be cleared, not shared by calls that may
+ *              overlap
+ * d % 8 == 0, d <= 2^20, V <= 2^26, N T <= 2^26, N <= 2^26. */
+int ckl_head_logprobs(int dtype, const void* H, const void* W, const int32_t* ids, const uint8_t* mask, int64_t N,
+                      int64_t d, int64_t V, int64_t T, int64_t chunk, float* logp, float* entropy, float* stats,
+                      void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* Its gradient, recomputing the logits: dH = G W and dW = G^T H with G = dz above in
+ * dtype (rounded once for bf16), sums in fp32.
+ *   logp, entropy, stats   the forward call's outputs (entropy as for ckl_logprobs_bwd)
+ *   dH         [N, d] in dtype, 16-byte aligned; zeros for masked rows
+ *   dW         [V, d], 16-byte aligned: fp32 (dw_dtype CKL_DTYPE_F32), overwritten, or
+ *              added to with accumulate = 1 (as a loss call wrote it); or bf16 with a
+ *              bf16 W, rounded once after the last chunk (accumulate = 0)
+ * N = 0: dW = 0, or nothing. */
+int ckl_head_logprobs_bwd(int dtype, const void* H, const void* W, const int32_t* ids, const uint8_t* mask, int64_t N,
+                          int64_t d, int64_t V, int64_t T, int64_t chunk, const float* logp, const float* entropy,
+                          const float* stats, const float* dlogp, const float* dentropy, void* dH, int dw_dtype,
+                          int accumulate, void* dW, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* Rows per chunk and workspace bytes of the two calls (pure host computation):
+ * backward = 0 or 1, dw_dtype as for ckl_head_logprobs_bwd (ignored for the forward
+ * call), chunk > 0 checks that many rows against the budget, budget_bytes 0 =
+ * CKL_WORKSPACE_BYTES or 6 GiB.  Returns as ckl_plan_pass does. */
+int ckl_head_logprobs_plan(int backward, int dtype, int dw_dtype, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                           uint64_t budget_bytes, int64_t* chunk_out, uint64_t* workspace_bytes_out);
+
 /* Dropout whose mask is never stored.  Element i of a tensor takes 16 bits of
  * Philox4x32-10 under the key `seed`: with the counter (i / 8, offset), bits
  * 16 (j % 2) .. + 15 of word j / 2, j = i % 8.  It goes if they are below
@@ -429,12 +507,12 @@ int ckl_debug_rows(const float* Z, const int32_t* idx, const float* tlogit, cons
 /* Measurement support.  While enabled, every kernel launch of a loss call
  * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk), and all launches of one ckl_embed,
  * ckl_embed_bwd, ckl_sample, ckl_quantize_fp8, ckl_matmul_fp8, ckl_dropout,
- * ckl_add_norm or ckl_add_norm_bwd call together, are bracketed by HIP events on
- * the call's stream.  ckl_timing_query waits for the recorded events and returns
+ * ckl_add_norm*, ckl_logprobs* or ckl_head_logprobs* call together, are bracketed by
+ * HIP events on the call's stream.  ckl_timing_query waits for the recorded events and returns
  * the summed milliseconds and launch count of one kernel kind: 0 logits GEMM,
  * 1 row pass, 2 dH GEMM, 3 dH split reduce, 4 dW GEMM, 5 other, 6 top-K
  * (ckl_topk), 7 embedding, 8 sampling, 9 8-bit products and quantisers,
- * 10 dropout and the residual's norms.  Not for concurrent use from several
+ * 10 dropout and the residual's norms, 11 log-probabilities.  Not for concurrent use from several
  * threads. */
 int ckl_timing_enable(int on);
 int ckl_timing_query(int kind, double* total_ms, int64_t* launches);
