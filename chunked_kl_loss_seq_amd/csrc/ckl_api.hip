@@ -1158,7 +1158,7 @@ int ckl_add_norm_bwd(int dtype, const void* y, const void* r, const ckl_norm* ho
       !aligned(dw_post, 4) || !aligned(dw_pre, 4) || !aligned(dgate, sums_gate ? 4 : el) || !aligned(workspace, 256))
     return CKL_EINVAL;
   NormGrads q{};
-  q.sums = (dw_post != nullptr) + (dw_pre != nullptr) + (sums_gate ? 1 : 0);
+  const int n_sums = (dw_post != nullptr) + (dw_pre != nullptr) + (sums_gate ? 1 : 0);
   try {
     if (N == 0) {
       if (dw_post) CKL_TRY(launch_fill_f32(dw_post, d, 0.f, stream));
@@ -1167,7 +1167,7 @@ int ckl_add_norm_bwd(int dtype, const void* y, const void* r, const ckl_norm* ho
       return CKL_OK;
     }
     if (!y || !r || !stats || !dy || !dr || (!dx && !dr_in) || (dx && !p.w_pre)) return CKL_EINVAL;
-    if (q.sums && (!workspace || workspace_bytes < add_norm_bwd_workspace(N, d, q.sums))) return CKL_EINVAL;
+    if (n_sums && (!workspace || workspace_bytes < add_norm_bwd_workspace(N, d, n_sums))) return CKL_EINVAL;
     p.stats_in = stats;
     q.dx = dx;
     q.dr_in = dr_in;

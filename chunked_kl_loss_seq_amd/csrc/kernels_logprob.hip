@@ -177,13 +177,15 @@ __device__ inline int collect_top(const T* row, int64_t lo, int64_t hi, float mx
     if (t % (NT / kGroups) == 0) sh.keys[t / (NT / kGroups)] = g;
     __syncthreads();
     if (t < 64) {
-      const uint32_t v = sh.keys[t];
-      int rank = 0;
-      for (int j = 0; j < kGroups; ++j) {
-        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, j);
-        rank += o > v || (o == v && j < t);
+      // the largest 16-bit prefix that K of the maxima reach (0 if there are fewer)
+      const uint32_t v = sh.keys[t] >> 16;
+      uint32_t best = 0;
+#pragma unroll
+      for (int b = 15; b >= 0; --b) {
+        const uint32_t next = best | (1u << b);
+        if (__builtin_popcountll(__ballot(v >= next)) >= K) best = next;
       }
-      if (rank == K - 1) sh.bound = v;
+      if (t == 0) sh.bound = best << 16;
     }
     __syncthreads();
   } else if (K <= NT / 2) {
@@ -326,10 +328,16 @@ __device__ inline void write_top_rest(const LogprobArgs& p, int64_t row, int n, 
   }
 }
 
-// The number of larger pairs in the list.
+// The number of larger pairs in the list (kList long; entries past n may hold anything).
 __device__ inline int rank_in(const u64* list, int n, u64 pair) {
   int rank = 0;
-  for (int j = 0; j < n; ++j) rank += list[j] > pair;
+  for (int j = 0; j < n; j += 8) {
+    u64 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = list[j + i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rank += j + i < n && o[i] > pair;
+  }
   return rank;
 }
 
@@ -388,11 +396,11 @@ __global__ void __launch_bounds__(NT) logprob_slice_kernel(LogprobArgs p) {
   }
 }
 
-// Joins a row's slices (at most 64, and at most kList pairs).
+// Joins a row's slices (2 to 64, and at most kList pairs).
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT) logprob_join_kernel(LogprobArgs p) {
   __shared__ u64 list[kList];
-  __shared__ u64 tails[64];
+  __shared__ u64 least;
   __shared__ float got[3];
   __shared__ int n;
   const int64_t row = blockIdx.x;
@@ -411,7 +419,21 @@ __global__ void __launch_bounds__(NT) logprob_join_kernel(LogprobArgs p) {
       v.s = q.z;
       v.a = q.w;
     }
-    if (p.top) tails[t] = t < p.slices ? pairs[t * p.top + p.top - 1] : 0;
+    if (p.top) {
+      // Of the slices' q-th largest pairs, the r-th largest is a bound that q r >=
+      // top pairs reach; q about 2 top / slices, so that r is about half the slices.
+      const int q = (2 * p.top + p.slices - 1) / p.slices < p.top ? (2 * p.top + p.slices - 1) / p.slices : p.top;
+      const int r = (p.top + q - 1) / q;
+      const u64 v = t < p.slices ? pairs[t * p.top + q - 1] : 0;
+      const uint32_t hi = (uint32_t)(v >> 32);
+      uint32_t best = 0;
+#pragma unroll
+      for (int b = 31; b >= 0; --b) {
+        const uint32_t next = best | (1u << b);
+        if (__builtin_popcountll(__ballot(hi >= next)) >= r) best = next;
+      }
+      if (t == 0) least = (u64)best << 32 > 1 ? (u64)best << 32 : 1;
+    }
     v.mx = wave_max(v.mx);
     v.move(fmaxf(v.mx, kLowest));
     v.s = lanes_sum(v.s, 64);
@@ -431,9 +453,7 @@ __global__ void __launch_bounds__(NT) logprob_join_kernel(LogprobArgs p) {
   const RowResult r(v);
   write_row<T>(p, row, r, t, NT);
   if (p.top == 0) return;
-  // the last of a full slice is a bound that `top` pairs reach
-  u64 bound = 1;
-  for (int i = 0; i < p.slices; ++i) bound = tails[i] > bound ? tails[i] : bound;
+  const u64 bound = least;
   for (int i = t; i < p.slices * p.top; i += NT) {
     const u64 pair = pairs[i];
     if (pair >= bound) list[atomicAdd(&n, 1)] = pair;

@@ -55,411 +55,559 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* __restri
 }
 
 // ------------------------------------------------------------------ norms
-// A row goes to a team of `lanes` lanes of one wave (a power of two that covers
-// d / 8, several rows a wave for short rows), or to all waves of a workgroup;
-// lane t holds elements 8 (t + i team) .. + 7, i < NV, in registers, so a row is
-// read once.  Workgroups walk over rows, and in the backward pass each keeps its
-// columns' sums in registers until its last row.
+// A row goes to a team: `lanes` lanes of one wave (a power of two that covers
+// d / 8; several rows a wave for short rows), or all waves of a workgroup.  Lane
+// t of it holds elements 8 (t + i width) .. + 7, i < NV, in registers, so a row is
+// read once; the weights of its columns stay there too.  Workgroups walk over
+// rows, and the next row's loads are issued before the current row's sums are
+// joined.
 struct Team {
   int lanes;   // lanes of one row within a wave
-  int teams;   // rows side by side in a wave (64 / lanes; 1 for several waves)
-  int waves;   // waves of a workgroup
+  int rows;    // rows side by side in a workgroup
+  int span;    // waves of one row (1, or all of the workgroup's)
 };
 
-__device__ inline float team_sum(float v, const Team& t, float* red, int slot) {
-  v = lanes_sum(v, t.lanes);
-  if (t.waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) red[slot * 16 + (threadIdx.x >> 6)] = v;
-  return v;
-}
+// Where a thread stands in its team.
+struct Place {
+  int t, width, sub;  // lane of the team, its lanes, the team's number in the workgroup
+  __device__ inline Place(const Team& m) {
+    if (m.span > 1) {
+      t = threadIdx.x;
+      width = blockDim.x;
+      sub = 0;
+    } else {
+      t = threadIdx.x & (m.lanes - 1);
+      width = m.lanes;
+      sub = threadIdx.x / m.lanes;
+    }
+  }
+};
 
 // Sums of K values over the team, in every lane.  `red` alternates between two
 // halves from one call to the next, so one barrier a call is enough.
 template <int K>
-__device__ inline void team_sums(float (&v)[K], const Team& t, float* red, int& half) {
-  float* to = red + half * (K * 16);
+__device__ inline void team_sums(float (&v)[K], const Team& m, float* red, int& half) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = team_sum(v[k], t, to, k);
-  if (t.waves == 1) return;
-  __syncthreads();
+  for (int k = 0; k < K; ++k) v[k] = lanes_sum(v[k], m.lanes);
+  if (m.span == 1) return;
+  float* to = red + half * (K * 16);
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) to[k * 16 + (threadIdx.x >> 6)] = v[k];
+  }
+  lds_barrier();
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float s = 0.f;
-    for (int w = 0; w < t.waves; ++w) s += to[k * 16 + w];
+    for (int w = 0; w < m.span; ++w) s += to[k * 16 + w];
     v[k] = s;
   }
   half ^= 1;
 }
 
-template <typename T, int NV, int MT>
-__global__ void __launch_bounds__(MT) add_norm_kernel(NormArgs p, Team team) {
+// One vector of an array at byte `off` from the first of the workgroup's rows, if
+// the array is there.  Nothing is done with it here, so that all of a row's loads
+// are under way together: lanes without a column read the first ones, and are
+// zeroed when the row's turn comes.  One 32-bit offset a vector serves all arrays.
+template <typename T>
+__device__ inline void load_at(Eight<T>& v, const void* rows, uint32_t off) {
+  if (rows != nullptr) v.load((const T*)((const char*)rows + off));
+}
+template <typename T>
+__device__ inline const void* rows_of(const void* x, int64_t row, int64_t d) {
+  return x != nullptr ? (const T*)x + row * d : nullptr;
+}
+template <typename T>
+__device__ inline T* row_at(void* x, int64_t row, int64_t d, uint32_t off) {
+  return (T*)((char*)((T*)x + row * d) + off);
+}
+// The byte offset of vector c of this team's row, of rows row0 .. (a team past the
+// last row takes the last one, and stores nothing).
+template <typename T>
+__device__ inline uint32_t offset_of(int64_t row0, int64_t N, int sub, uint32_t d, int c, bool in) {
+  const uint32_t at = row0 + sub < N ? (uint32_t)sub : (uint32_t)(N - 1 - row0);
+  return (at * d + (in ? 8u * (uint32_t)c : 0u)) * (uint32_t)sizeof(T);
+}
+
+// The columns' weights, in LDS for all rows of a workgroup (in registers they would
+// halve the waves that a compute unit holds): `f`, the scale (and the kept ones'
+// factor) x w_post x a gate [d], then `w2`, w_pre or zeros.  The two halves of a
+// vector of 8 lie d / 2 apart, so that lanes read 16 adjacent bytes each.
+__device__ inline float* half_at(float* w, int d, int c, int h) { return w + h * (d >> 1) + 4 * c; }
+__device__ inline void read8(float* w, int d, int c, float (&v)[8]) {
+  const row_f32x4 a = *(const row_f32x4*)half_at(w, d, c, 0), b = *(const row_f32x4*)half_at(w, d, c, 1);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = a[e];
+    v[4 + e] = b[e];
+  }
+}
+template <typename T, bool ROWS>
+__device__ inline void column_weights(const NormArgs& p, float* f, float* w2) {
+  const float k = p.drop.border ? p.scale * p.drop.keep : p.scale;
+  const int d = (int)p.d;
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+    float v = k;
+    if (p.w_post != nullptr) v *= (float)((const T*)p.w_post)[c];
+    if (!ROWS && p.gate != nullptr) v *= (float)((const T*)p.gate)[c];
+    const int at = ((c >> 2) & 1) * (d >> 1) + (c >> 3) * 4 + (c & 3);
+    f[at] = v;
+    w2[at] = p.w_pre != nullptr ? (float)((const T*)p.w_pre)[c] : 0.f;
+  }
+  __syncthreads();
+}
+
+// Bit e: element e of the vector at element index 8 g is kept.
+__device__ inline uint32_t kept_bits(const Drop& r, uint64_t offset, uint64_t g) {
+  const row_u32x4 w = philox(g, offset, r.seed);
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m |= (bits16(w, e) >= r.border ? 1u : 0u) << e;
+  return m;
+}
+
+// Waves a SIMD: what the registers are held to, and what the grids count on.
+template <typename T, int NV, int MT, bool ROWS>
+constexpr int fwd_waves() {
+  if (MT > 512) return 4;
+  return sizeof(T) == 2 ? (NV == 1 ? (ROWS ? 6 : 7) : 4) : (NV == 1 ? (ROWS ? 5 : 6) : (ROWS ? 3 : 4));
+}
+template <typename T, int NV, int MT, bool ROWS>
+constexpr int bwd_waves() {
+  if (MT > 512) return 4;
+  return sizeof(T) == 2 ? (NV == 1 ? 4 : 2) : (NV == 1 ? 3 : 2);
+}
+
+template <typename T, int NV, int MT, bool ROWS, bool DROP>
+__global__ void __launch_bounds__(MT) __attribute__((amdgpu_waves_per_eu(fwd_waves<T, NV, MT, ROWS>())))
+add_norm_kernel(NormArgs p, Team team) {
   __shared__ float red[2 * 16];
   int half = 0;
-  const int lane = threadIdx.x & 63;
-  const int t = team.waves > 1 ? threadIdx.x : lane & (team.lanes - 1);
-  const int width = team.waves > 1 ? team.waves * 64 : team.lanes;
-  const int sub = team.waves > 1 ? 0 : lane / team.lanes;
+  const Place at(team);
   const int d8 = (int)(p.d >> 3);
-  const uint64_t offset = p.drop.border ? drop_offset(p.drop) : 0;
-  const T* w1 = (const T*)p.w_post;
-  const T* w2 = (const T*)p.w_pre;
-  const T* gate = (const T*)p.gate;
+  const uint64_t offset = DROP ? drop_offset(p.drop) : 0;
   const float inv_d = 1.f / (float)p.d;
-  const int64_t step = (int64_t)gridDim.x * team.teams;
-  // every lane of a workgroup makes the same number of turns: the sums cross lanes
-  for (int64_t row0 = (int64_t)blockIdx.x * team.teams; row0 < p.N; row0 += step) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.N;
-    const int64_t base = row * p.d;
-    Eight<T> y[NV], r[NV];
+  extern __shared__ float columns[];
+  float *f = columns, *w2 = columns + p.d;
+  Eight<T> y[NV], r[NV], g[ROWS ? NV : 1];
+  const auto fetch = [&](int64_t row0) {
+    const void *ys = rows_of<T>(p.y, row0, p.d), *rs = rows_of<T>(p.r, row0, p.d);
+    const void* gs = ROWS ? rows_of<T>(p.gate, row0, p.d) : nullptr;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * width;
-      if (live && c < d8) {
-        y[i].load((const T*)p.y + base + 8 * c);
-        r[i].load((const T*)p.r + base + 8 * c);
-      }
+      const int c = at.t + i * at.width;
+      const uint32_t off = offset_of<T>(row0, p.N, at.sub, (uint32_t)p.d, c, c < d8);
+      y[i].load((const T*)((const char*)ys + off));
+      r[i].load((const T*)((const char*)rs + off));
+      if constexpr (ROWS) g[i].load((const T*)((const char*)gs + off));
     }
-    float inv1 = 1.f;
-    if (w1 != nullptr) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = t + i * width;
-        if (live && c < d8) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(y[i].get(e), y[i].get(e), s[0]);
-        }
-      }
-      team_sums(s, team, red, half);
-      inv1 = 1.f / sqrtf(s[0] * inv_d + p.eps);
-    }
-    float o[NV][8];
+  };
+  const int64_t step = (int64_t)gridDim.x * team.rows;
+  fetch((int64_t)blockIdx.x * team.rows);
+  column_weights<T, ROWS>(p, f, w2);
+  // every lane of a workgroup makes the same number of turns: the sums cross lanes
+  for (int64_t row0 = (int64_t)blockIdx.x * team.rows; row0 < p.N; row0 += step) {
+    const bool live = row0 + at.sub < p.N;
+    const uint64_t group0 = (uint64_t)row0 * (uint64_t)d8 + (uint64_t)(uint32_t)(at.sub * d8);
+    float b[NV][8], o[NV][8];  // the branch before its norm, then r'
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * width;
-      if (!live || c >= d8) continue;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = p.scale;
-      if (p.drop.border) {
-        const row_u32x4 w = philox((uint64_t)(base >> 3) + (uint64_t)c, offset, p.drop.seed);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = bits16(w, e) >= p.drop.border ? p.scale * p.drop.keep : 0.f;
+      uint32_t kept = 0xFFu;
+      if constexpr (DROP) kept = kept_bits(p.drop, offset, group0 + (uint32_t)(at.t + i * at.width));
+      const int c = at.t + i * at.width;
+      if (c >= d8) {
+        y[i].clear();
+        r[i].clear();
+        if constexpr (ROWS) g[i].clear();
       }
-      if (gate != nullptr) {
-        Eight<T> g;
-        g.load(gate + (p.gate_rows ? base : 0) + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= g.get(e);
-      }
-      if (w1 != nullptr) {
-        Eight<T> w;
-        w.load(w1 + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= w.get(e) * inv1;
-      }
+      float k[8];
+      read8(f, (int)p.d, c < d8 ? c : 0, k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[i][e] = __builtin_fmaf(f[e], y[i].get(e), r[i].get(e));
+        const float v = y[i].get(e);
+        s[0] = __builtin_fmaf(v, v, s[0]);
+        b[i][e] = DROP && !((kept >> e) & 1u) ? 0.f : ROWS ? k[e] * g[i].get(e) * v : k[e] * v;
+        o[i][e] = r[i].get(e);
+      }
+    }
+    if (row0 + step < p.N) fetch(row0 + step);
+    float inv1 = 1.f;
+    if (p.w_post != nullptr) {
+      team_sums(s, team, red, half);
+      inv1 = 1.f / sqrtf(s[0] * inv_d + p.eps);
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = at.t + i * at.width;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o[i][e] = __builtin_fmaf(b[i][e], inv1, o[i][e]);
         s[0] = __builtin_fmaf(o[i][e], o[i][e], s[0]);
       }
       Eight<T> v;
       v.set(o[i]);
-      v.store((T*)p.r_out + base + 8 * c);
+      if (live && c < d8) v.store(row_at<T>(p.r_out, row0, p.d, offset_of<T>(row0, p.N, at.sub, (uint32_t)p.d, c, true)));
     }
     float inv2 = 1.f;
-    if (w2 != nullptr) {
+    if (p.w_pre != nullptr) {
       team_sums(s, team, red, half);
       inv2 = 1.f / sqrtf(s[0] * inv_d + p.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = t + i * width;
-        if (!live || c >= d8) continue;
-        Eight<T> w;
-        w.load(w2 + 8 * c);
-        float f[8];
+        const int c = at.t + i * at.width;
+        float k[8];
+        read8(w2, (int)p.d, c < d8 ? c : 0, k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = o[i][e] * inv2 * w.get(e);
-        w.set(f);
-        w.store((T*)p.x + base + 8 * c);
+        for (int e = 0; e < 8; ++e) o[i][e] *= inv2 * k[e];
+        Eight<T> v;
+        v.set(o[i]);
+        if (live && c < d8) v.store(row_at<T>(p.x, row0, p.d, offset_of<T>(row0, p.N, at.sub, (uint32_t)p.d, c, true)));
       }
     }
-    if (p.stats != nullptr && live && t == 0) {
-      p.stats[row] = inv1;
-      p.stats[p.N + row] = inv2;
+    if (p.stats != nullptr && live && at.t == 0) {
+      p.stats[row0 + at.sub] = inv1;
+      p.stats[p.N + row0 + at.sub] = inv2;
     }
   }
 }
 
-// Columns' sums of a workgroup's rows: part[block][which][d], which = dw_post,
-// dw_pre, dgate as far as they are asked for.
-template <typename T, int NV, int MT>
-__global__ void __launch_bounds__(MT) add_norm_bwd_kernel(NormArgs p, NormGrads q, Team team) {
+// Per workgroup, part[block][which][d]: sum m D n1 (m the kept ones, times a row's
+// gate) where `a`, from which dw_post and the gradient of a gate [d] follow by the
+// columns' factors, and sum dx n2 with w_pre.
+template <typename T, int NV, int MT, bool ROWS, bool DROP>
+__global__ void __launch_bounds__(MT) __attribute__((amdgpu_waves_per_eu(bwd_waves<T, NV, MT, ROWS>())))
+add_norm_bwd_kernel(NormArgs p, NormGrads q, Team team) {
   __shared__ float red[2 * 3 * 16];
+  extern __shared__ float columns[];
+  float *f = columns, *w2 = columns + p.d;
   int half = 0;
-  const int lane = threadIdx.x & 63;
-  const int t = team.waves > 1 ? threadIdx.x : lane & (team.lanes - 1);
-  const int width = team.waves > 1 ? team.waves * 64 : team.lanes;
-  const int sub = team.waves > 1 ? 0 : lane / team.lanes;
+  const Place at(team);
   const int d8 = (int)(p.d >> 3);
-  const uint64_t offset = p.drop.border ? drop_offset(p.drop) : 0;
-  const T* w1 = (const T*)p.w_post;
-  const T* w2 = (const T*)p.w_pre;
-  const T* gate = (const T*)p.gate;
-  const float factor = p.drop.border ? p.scale * p.drop.keep : p.scale;
+  const uint64_t offset = DROP ? drop_offset(p.drop) : 0;
   const float inv_d = 1.f / (float)p.d;
-  float aw1[NV][8], aw2[NV][8], ag[NV][8];
+  const bool post = p.w_post != nullptr, pre = q.dx != nullptr;
+  float aa[NV][8], a2[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aw1[i][e] = aw2[i][e] = ag[i][e] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * team.teams;
-  for (int64_t row0 = (int64_t)blockIdx.x * team.teams; row0 < p.N; row0 += step) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.N;
-    const int64_t base = row * p.d;
-    const float inv1 = live && w1 != nullptr ? p.stats_in[row] : 1.f;
-    const float inv2 = live && w2 != nullptr ? p.stats_in[p.N + row] : 1.f;
-    // per element: h = f gate, n1, n2 and the gradients
-    float n1[NV][8], n2[NV][8], a[NV][8], D[NV][8];
-    uint32_t kept[NV];  // bit e: element e of the vector is kept
+    for (int e = 0; e < 8; ++e) aa[i][e] = a2[i][e] = 0.f;
+  Eight<T> y[NV], r[NV], dx[NV], dro[NV], g[ROWS ? NV : 1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    dx[i].clear();
+    dro[i].clear();
+  }
+  float inv1 = 1.f, inv2 = 1.f;
+  const auto fetch = [&](int64_t row0) {
+    const void *ys = rows_of<T>(p.y, row0, p.d), *rs = rows_of<T>(p.r, row0, p.d);
+    const void *xs = rows_of<T>(q.dx, row0, p.d), *os = rows_of<T>(q.dr_in, row0, p.d);
+    const void* gs = ROWS ? rows_of<T>(p.gate, row0, p.d) : nullptr;
+    const bool live = row0 + at.sub < p.N;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = at.t + i * at.width;
+      const uint32_t off = offset_of<T>(row0, p.N, at.sub, (uint32_t)p.d, c, c < d8);
+      y[i].load((const T*)((const char*)ys + off));
+      r[i].load((const T*)((const char*)rs + off));
+      if constexpr (ROWS) g[i].load((const T*)((const char*)gs + off));
+      load_at<T>(dx[i], xs, off);
+      load_at<T>(dro[i], os, off);
+    }
+    const int64_t rc = live ? row0 + at.sub : p.N - 1;
+    if (post) inv1 = p.stats_in[rc];
+    if (pre) inv2 = p.stats_in[p.N + rc];
+  };
+  const int64_t step = (int64_t)gridDim.x * team.rows;
+  fetch((int64_t)blockIdx.x * team.rows);
+  column_weights<T, ROWS>(p, f, w2);
+  for (int64_t row0 = (int64_t)blockIdx.x * team.rows; row0 < p.N; row0 += step) {
+    const bool live = row0 + at.sub < p.N;
+    const uint64_t group0 = (uint64_t)row0 * (uint64_t)d8 + (uint64_t)(uint32_t)(at.sub * d8);
+    // the row's values move aside, so that the next row's are under way for all of this one's turn
+    const float i1 = inv1, i2 = inv2;
+    Eight<T> cy[NV], cr[NV], cx[NV], co[NV], cg[ROWS ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cy[i] = y[i];
+      cr[i] = r[i];
+      cx[i] = dx[i];
+      co[i] = dro[i];
+      if constexpr (ROWS) cg[i] = g[i];
+    }
+    if (row0 + step < p.N) fetch(row0 + step);
+    float n1[NV][8], n2[NV][8], D[NV][8], gr[ROWS ? NV : 1][8];
+    uint32_t kept[NV];
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * width;
-      if (!live || c >= d8) continue;
-      Eight<T> v;
-      v.load((const T*)p.y + base + 8 * c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n1[i][e] = v.get(e) * inv1;
-      float f[8];
+      __builtin_amdgcn_sched_barrier(0);  // one vector after the other: their weights together would not fit
       kept[i] = 0xFFu;
-      if (p.drop.border) {
-        const row_u32x4 w = philox((uint64_t)(base >> 3) + (uint64_t)c, offset, p.drop.seed);
-        kept[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) kept[i] |= (bits16(w, e) >= p.drop.border ? 1u : 0u) << e;
+      if constexpr (DROP) kept[i] = kept_bits(p.drop, offset, group0 + (uint32_t)(at.t + i * at.width));
+      const int c = at.t + i * at.width;
+      if (!live || c >= d8) {  // nothing of it enters a sum
+        cy[i].clear();
+        cr[i].clear();
+        cx[i].clear();
+        co[i].clear();
+        if constexpr (ROWS) cg[i].clear();
       }
+      float k[8], k2[8], b[8];
+      read8(f, (int)p.d, c < d8 ? c : 0, k);
+      read8(w2, (int)p.d, c < d8 ? c : 0, k2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = (kept[i] >> e) & 1u ? factor : 0.f;
-      if (gate != nullptr) {
-        v.load(gate + (p.gate_rows ? base : 0) + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= v.get(e);
+      for (int e = 0; e < 8; ++e) {
+        n1[i][e] = cy[i].get(e) * i1;
+        b[e] = k[e] * n1[i][e];
+        if constexpr (ROWS) b[e] *= gr[i][e] = cg[i].get(e);
+        if (DROP && !((kept[i] >> e) & 1u)) b[e] = 0.f;
+        D[i][e] = co[i].get(e);
       }
-      if (w1 != nullptr) {
-        v.load(w1 + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= v.get(e);
-      }
-      // f n1 = f gate u: the branch's share of r'
-      v.load((const T*)p.r + base + 8 * c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n2[i][e] = __builtin_fmaf(f[e], n1[i][e], v.get(e)) * inv2;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) D[i][e] = 0.f;
-      if (q.dr_in != nullptr) {
-        v.load((const T*)q.dr_in + base + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) D[i][e] = v.get(e);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a[i][e] = 0.f;
-      if (q.dx != nullptr) {
-        v.load((const T*)q.dx + base + 8 * c);
+      if (pre) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          a[i][e] = v.get(e);
-          aw2[i][e] = __builtin_fmaf(a[i][e], n2[i][e], aw2[i][e]);
+          n2[i][e] = (cr[i].get(e) + b[e]) * i2;
+          const float x = cx[i].get(e), a = x * k2[e];
+          a2[i][e] = __builtin_fmaf(x, n2[i][e], a2[i][e]);
+          D[i][e] = __builtin_fmaf(a, i2, D[i][e]);
+          s[0] = __builtin_fmaf(a, n2[i][e], s[0]);
+          s[2] = __builtin_fmaf(b[e], n2[i][e], s[2]);
         }
-        v.load(w2 + 8 * c);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[i][e] *= v.get(e);
+        for (int e = 0; e < 8; ++e) n2[i][e] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float b = f[e] * n1[i][e];
-        D[i][e] = __builtin_fmaf(a[i][e], inv2, D[i][e]);
-        s[0] = __builtin_fmaf(a[i][e], n2[i][e], s[0]);
-        s[1] = __builtin_fmaf(b, D[i][e], s[1]);
-        s[2] = __builtin_fmaf(b, n2[i][e], s[2]);
-      }
+      for (int e = 0; e < 8; ++e) s[1] = __builtin_fmaf(b[e], D[i][e], s[1]);
     }
     team_sums(s, team, red, half);
-    const float c2 = s[0] * inv_d * inv2;              // mean(a n2) / rms(r')
-    const float c1 = w1 != nullptr ? (s[1] - c2 * s[2]) * inv_d : 0.f;  // mean(e n1)
+    const float c2 = s[0] * inv_d * i2;                        // mean(a n2) / rms(r')
+    const float c1 = post ? (s[1] - c2 * s[2]) * inv_d : 0.f;  // mean(e n1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * width;
-      if (!live || c >= d8) continue;
+      const int c = at.t + i * at.width;
+      __builtin_amdgcn_sched_barrier(0);
+      const bool out = live && c < d8;
+      const uint32_t off = offset_of<T>(row0, p.N, at.sub, (uint32_t)p.d, c, true);
+      float o[8], og[8], k[8];
+      read8(f, (int)p.d, c < d8 ? c : 0, k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) D[i][e] = __builtin_fmaf(-c2, n2[i][e], D[i][e]);
       Eight<T> v;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) D[i][e] -= n2[i][e] * c2;
       v.set(D[i]);
-      v.store((T*)q.dr + base + 8 * c);
-      float f[8], o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = (kept[i] >> e) & 1u ? factor : 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= D[i][e];
-      float wp[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wp[e] = 1.f;
-      if (w1 != nullptr) {
-        v.load(w1 + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wp[e] = v.get(e);
-      }
-      if (gate != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = f[e] * n1[i][e] * wp[e];
-        if (p.gate_rows) {
-          v.set(o);
-          v.store((T*)q.dgate + base + 8 * c);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ag[i][e] += o[e];
-        }
-        v.load(gate + (p.gate_rows ? base : 0) + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= v.get(e);
-      }
+      if (out) v.store(row_at<T>(q.dr, row0, p.d, off));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        aw1[i][e] = __builtin_fmaf(f[e], n1[i][e], aw1[i][e]);
-        o[e] = (f[e] * wp[e] - n1[i][e] * c1) * inv1;
+        float m = DROP && !((kept[i] >> e) & 1u) ? 0.f : D[i][e];
+        if constexpr (ROWS) {
+          og[e] = k[e] * m * n1[i][e];
+          m *= gr[i][e];
+        }
+        aa[i][e] = __builtin_fmaf(m, n1[i][e], aa[i][e]);
+        o[e] = __builtin_fmaf(k[e], m, -n1[i][e] * c1) * i1;
       }
       v.set(o);
-      v.store((T*)q.dy + base + 8 * c);
+      if (out) v.store(row_at<T>(q.dy, row0, p.d, off));
+      if constexpr (ROWS) {
+        v.set(og);
+        if (out) v.store(row_at<T>(q.dgate, row0, p.d, off));
+      }
     }
   }
-  // rows side by side in the wave hold the same columns
-  if (team.teams > 1) {
+  float* to = q.part + (int64_t)blockIdx.x * q.sums * p.d;
+  float* to2 = q.a ? to + p.d : to;
+  if (team.rows == 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const int c = at.t + i * at.width;
+      if (c >= d8) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        for (int o = 32; o >= team.lanes; o >>= 1) {
-          aw1[i][e] += __shfl_xor(aw1[i][e], o);
-          aw2[i][e] += __shfl_xor(aw2[i][e], o);
-          ag[i][e] += __shfl_xor(ag[i][e], o);
+      for (int e = 0; e < 8; ++e) {
+        if (q.a) to[8 * c + e] = aa[i][e];
+        if (p.w_pre != nullptr) to2[8 * c + e] = a2[i][e];
+      }
+    }
+    return;
+  }
+  // rows side by side hold the same columns: within the wave first, then wave by wave
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      for (int o = 32; o >= team.lanes; o >>= 1) {
+        aa[i][e] += __shfl_xor(aa[i][e], o);
+        a2[i][e] += __shfl_xor(a2[i][e], o);
+      }
+  const int wave = threadIdx.x >> 6;
+  float* sums = columns;
+  __syncthreads();  // the weights are read no more
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+    if (w == wave && (int)(threadIdx.x & 63) < team.lanes) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = at.t + i * at.width;
+        if (c >= d8) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float* u = sums + 8 * c + e;
+          u[0] = w == 0 ? aa[i][e] : u[0] + aa[i][e];
+          u[p.d] = w == 0 ? a2[i][e] : u[p.d] + a2[i][e];
         }
-    if (sub != 0) return;
+      }
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = t + i * width;
-    if (c >= d8) continue;
-    float* to = q.part + (int64_t)blockIdx.x * q.sums * p.d + 8 * c;
-    if (w1 != nullptr) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) to[e] = aw1[i][e];
-      to += p.d;
-    }
-    if (w2 != nullptr) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) to[e] = aw2[i][e];
-      to += p.d;
-    }
-    if (gate != nullptr && !p.gate_rows) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) to[e] = ag[i][e];
-    }
+  for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) {
+    if (q.a) to[c] = sums[c];
+    if (p.w_pre != nullptr) to2[c] = sums[p.d + c];
   }
 }
 
-// out[c] = the sum of part[b][c] over the workgroups b, in a fixed order: 64
-// columns a workgroup, 16 threads a column.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int rows, int64_t cols,
-                                                         int64_t d, float* o0, float* o1, float* o2) {
+// The workgroups' sums of a column, in a fixed order: 64 columns a workgroup, 16
+// threads a column, 8 loads of each in flight.
+template <typename T>
+__global__ void __launch_bounds__(1024) column_sum_kernel(NormArgs p, NormGrads q, int rows) {
   __shared__ float red[16][64];
   const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const int64_t cols = q.sums * p.d;
   const int64_t c = (int64_t)blockIdx.x * 64 + x;
   float s = 0.f;
-  if (c < cols)
-    for (int b = y; b < rows; b += 16) s += part[(int64_t)b * cols + c];
+  if (c < cols) {
+    const float* from = q.part + c;
+    int b = y;
+    for (; b + 7 * 16 < rows; b += 8 * 16) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = from[(int64_t)(b + 16 * i) * cols];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; b < rows; b += 16) s += from[(int64_t)b * cols];
+  }
   red[y][x] = s;
   __syncthreads();
   if (y != 0 || c >= cols) return;
 #pragma unroll
   for (int i = 1; i < 16; ++i) s += red[i][x];
-  float* o = c < d ? o0 : c < 2 * d ? o1 : o2;
-  o[c % d] = s;
+  if (!q.a || c >= p.d) {
+    q.dw_pre[q.a ? c - p.d : c] = s;
+    return;
+  }
+  s *= p.drop.border ? p.scale * p.drop.keep : p.scale;
+  const bool vec = p.gate != nullptr && !p.gate_rows;
+  if (p.w_post != nullptr) q.dw_post[c] = vec ? s * (float)((const T*)p.gate)[c] : s;
+  if (vec) ((float*)q.dgate)[c] = p.w_post != nullptr ? s * (float)((const T*)p.w_post)[c] : s;
 }
 
-// Lanes, rows a wave and waves for rows of d elements with up to `most` vectors
-// a lane, and how many are used.  Workgroups are held to 512 threads, so that a
-// lane can have 256 registers; rows of more than 8 x 64 x 8 x 3 elements take
-// up to 1024 threads with two vectors each.
-constexpr int kNormVec = 3;
+// A row's lanes, and how many vectors of 8 each holds: up to `most` (two where a
+// workgroup would pass 512 threads, which leaves a lane 128 registers).
+constexpr int kFwdVec = 2, kBwdVec = 1;
 struct Shape {
   Team team;
-  int nv;
+  int nv, threads;
 };
-Shape shape_of(int64_t d) {
+Shape shape_of(int64_t d, int most) {
   const int64_t d8 = d / 8;
-  Shape r{{64, 1, 1}, 1};
-  if (d8 <= 64) {
-    while (r.team.lanes > 1 && r.team.lanes / 2 >= d8) r.team.lanes /= 2;
-    r.team.teams = 64 / r.team.lanes;
+  Shape r{{64, 4, 1}, 1, 256};
+  if (d8 <= 64 * most) {  // four waves, a row each, or several where it is short
+    if (d8 <= 64) {
+      while (r.team.lanes > 1 && r.team.lanes / 2 >= d8) r.team.lanes /= 2;
+      r.team.rows = 256 / r.team.lanes;
+    } else {
+      r.nv = (int)((d8 + 63) / 64);
+    }
     return r;
   }
-  int most = kNormVec;
   if (d8 > 8 * 64 * most) most = 2;
-  r.team.waves = (int)((d8 + 64 * most - 1) / (64 * most));
-  r.nv = (int)((d8 + 64 * r.team.waves - 1) / (64 * r.team.waves));
+  r.team.span = (int)((d8 + 64 * most - 1) / (64 * most));
+  r.team.rows = 1;
+  r.nv = (int)((d8 + 64 * r.team.span - 1) / (64 * r.team.span));
+  r.threads = 64 * r.team.span;
   return r;
 }
 
-// Workgroups of the backward pass, each with its partial sums.
-int bwd_blocks(int64_t N, const Team& t) {
-  const int64_t need = (N + t.teams - 1) / t.teams;
-  const int64_t most = t.waves == 1 ? 2048 : t.waves == 2 ? 1024 : 512;
+// Workgroups: as many as the 256 compute units hold at once with `waves` waves a
+// SIMD, since one more would run after all others.
+int blocks_of(int64_t N, const Shape& h, int waves) {
+  const int64_t need = (N + h.team.rows - 1) / h.team.rows;
+  const int64_t unit = 4 * waves / (h.threads / 64);
+  const int64_t most = 256 * (unit > 0 ? unit : 1);
   return (int)(need < most ? need : most);
+}
+template <typename T, bool ROWS>
+int fwd_blocks(int64_t N, const Shape& h) {
+  return blocks_of(N, h, h.threads > 512 ? fwd_waves<T, 2, 1024, ROWS>()
+                         : h.nv == 1    ? fwd_waves<T, 1, 512, ROWS>()
+                                        : fwd_waves<T, 2, 512, ROWS>());
+}
+// The backward pass's, each with its sums.
+template <typename T, bool ROWS>
+int bwd_blocks(int64_t N, const Shape& h) {
+  return blocks_of(N, h, h.threads > 512 ? bwd_waves<T, 2, 1024, ROWS>()
+                         : h.nv == 1    ? bwd_waves<T, 1, 512, ROWS>()
+                                        : bwd_waves<T, 2, 512, ROWS>());
+}
+
+template <typename T, int NV, int MT>
+void add_norm_as(const NormArgs& p, const Shape& h, dim3 grid, hipStream_t s) {
+  const dim3 block(h.threads);
+  const bool drop = p.drop.border != 0;
+  const size_t lds = (size_t)p.d * 8;
+  if (p.gate_rows && drop)
+    hipLaunchKernelGGL((add_norm_kernel<T, NV, MT, true, true>), grid, block, lds, s, p, h.team);
+  else if (p.gate_rows)
+    hipLaunchKernelGGL((add_norm_kernel<T, NV, MT, true, false>), grid, block, lds, s, p, h.team);
+  else if (drop)
+    hipLaunchKernelGGL((add_norm_kernel<T, NV, MT, false, true>), grid, block, lds, s, p, h.team);
+  else
+    hipLaunchKernelGGL((add_norm_kernel<T, NV, MT, false, false>), grid, block, lds, s, p, h.team);
 }
 
 template <typename T>
 hipError_t add_norm_of(const NormArgs& p, hipStream_t s) {
-  const Shape h = shape_of(p.d);
-  const int64_t need = (p.N + h.team.teams - 1) / h.team.teams;
-  const int64_t most = 256 * 32 / h.team.waves;
-  const dim3 grid((unsigned)(need < most ? need : most)), block(64 * h.team.waves);
-  if (block.x > 512)
-    hipLaunchKernelGGL((add_norm_kernel<T, 2, 1024>), grid, block, 0, s, p, h.team);
+  const Shape h = shape_of(p.d, kFwdVec);
+  const dim3 grid(p.gate_rows ? fwd_blocks<T, true>(p.N, h) : fwd_blocks<T, false>(p.N, h));
+  if (h.threads > 512)
+    add_norm_as<T, 2, 1024>(p, h, grid, s);
   else if (h.nv == 1)
-    hipLaunchKernelGGL((add_norm_kernel<T, 1, 512>), grid, block, 0, s, p, h.team);
-  else if (h.nv == 2)
-    hipLaunchKernelGGL((add_norm_kernel<T, 2, 512>), grid, block, 0, s, p, h.team);
+    add_norm_as<T, 1, 512>(p, h, grid, s);
   else
-    hipLaunchKernelGGL((add_norm_kernel<T, 3, 512>), grid, block, 0, s, p, h.team);
+    add_norm_as<T, 2, 512>(p, h, grid, s);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t add_norm_bwd_of(const NormArgs& p, const NormGrads& q, hipStream_t s) {
-  const Shape h = shape_of(p.d);
-  const int blocks = bwd_blocks(p.N, h.team);
-  const dim3 grid(blocks), block(64 * h.team.waves);
-  if (block.x > 512)
-    hipLaunchKernelGGL((add_norm_bwd_kernel<T, 2, 1024>), grid, block, 0, s, p, q, h.team);
-  else if (h.nv == 1)
-    hipLaunchKernelGGL((add_norm_bwd_kernel<T, 1, 512>), grid, block, 0, s, p, q, h.team);
-  else if (h.nv == 2)
-    hipLaunchKernelGGL((add_norm_bwd_kernel<T, 2, 512>), grid, block, 0, s, p, q, h.team);
+template <typename T, int NV, int MT>
+void add_norm_bwd_as(const NormArgs& p, const NormGrads& q, const Shape& h, dim3 grid, hipStream_t s) {
+  const dim3 block(h.threads);
+  const bool drop = p.drop.border != 0;
+  const size_t lds = (size_t)p.d * 8;
+  if (p.gate_rows && drop)
+    hipLaunchKernelGGL((add_norm_bwd_kernel<T, NV, MT, true, true>), grid, block, lds, s, p, q, h.team);
+  else if (p.gate_rows)
+    hipLaunchKernelGGL((add_norm_bwd_kernel<T, NV, MT, true, false>), grid, block, lds, s, p, q, h.team);
+  else if (drop)
+    hipLaunchKernelGGL((add_norm_bwd_kernel<T, NV, MT, false, true>), grid, block, lds, s, p, q, h.team);
   else
-    hipLaunchKernelGGL((add_norm_bwd_kernel<T, 3, 512>), grid, block, 0, s, p, q, h.team);
+    hipLaunchKernelGGL((add_norm_bwd_kernel<T, NV, MT, false, false>), grid, block, lds, s, p, q, h.team);
+}
+
+template <typename T>
+hipError_t add_norm_bwd_of(const NormArgs& p, NormGrads q, hipStream_t s) {
+  q.a = p.w_post != nullptr || (p.gate != nullptr && !p.gate_rows);
+  q.sums = (q.a ? 1 : 0) + (p.w_pre != nullptr ? 1 : 0);
+  const Shape h = shape_of(p.d, kBwdVec);
+  const int blocks = p.gate_rows ? bwd_blocks<T, true>(p.N, h) : bwd_blocks<T, false>(p.N, h);
+  const dim3 grid(blocks);
+  if (h.threads > 512)
+    add_norm_bwd_as<T, 2, 1024>(p, q, h, grid, s);
+  else if (h.nv == 1)
+    add_norm_bwd_as<T, 1, 512>(p, q, h, grid, s);
+  else
+    add_norm_bwd_as<T, 2, 512>(p, q, h, grid, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || q.sums == 0) return e;
-  float* outs[3] = {nullptr, nullptr, nullptr};
-  int n = 0;
-  if (p.w_post != nullptr) outs[n++] = q.dw_post;
-  if (p.w_pre != nullptr) outs[n++] = q.dw_pre;
-  if (p.gate != nullptr && !p.gate_rows) outs[n++] = (float*)q.dgate;
-  const int64_t cols = q.sums * p.d;
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, q.part, blocks, cols, p.d,
-                     outs[0], outs[1], outs[2]);
+  hipLaunchKernelGGL((column_sum_kernel<T>), dim3((unsigned)((q.sums * p.d + 63) / 64)), dim3(1024), 0, s, p, q, blocks);
   return hipGetLastError();
 }
 
@@ -484,7 +632,8 @@ hipError_t launch_add_norm(Dtype dt, const NormArgs& p, hipStream_t s) {
 }
 
 uint64_t add_norm_bwd_workspace(int64_t N, int64_t d, int sums) {
-  return N > 0 ? (uint64_t)bwd_blocks(N, shape_of(d).team) * (uint64_t)sums * (uint64_t)d * 4 : 0;
+  const Shape h = shape_of(d, kBwdVec);  // the most workgroups of all types
+  return N > 0 ? (uint64_t)bwd_blocks<__bf16, false>(N, h) * (uint64_t)sums * (uint64_t)d * 4 : 0;
 }
 
 hipError_t launch_add_norm_bwd(Dtype dt, const NormArgs& p, const NormGrads& q, hipStream_t s) {

@@ -165,8 +165,9 @@ struct NormGrads {
   float* dw_post;     // [d]
   float* dw_pre;      // [d]
   void* dgate;        // fp32 [d], or [N, d] in the path's type
-  int sums;           // how many of dw_post, dw_pre and a gate [d]'s gradient there are
   float* part;        // add_norm_bwd_workspace bytes
+  bool a;             // set by the launcher: whether dw_post or a gate [d]'s gradient is there
+  int sums;           // set by the launcher: sums a column
 };
 constexpr int64_t kMaxNormWidth = 16384;  // d: a row is held in one workgroup's registers
 hipError_t launch_add_norm(Dtype dt, const NormArgs& p, hipStream_t s);

@@ -23,6 +23,7 @@ struct Eight;
 template <>
 struct Eight<__bf16> {
   row_u32x4 a;
+  __device__ inline void clear() { a = row_u32x4{0, 0, 0, 0}; }
   __device__ inline void load(const __bf16* p) { a = ((const Raw16*)p)->v; }
   __device__ inline void store(__bf16* p) const { ((Raw16*)p)->v = a; }
   __device__ inline float get(int i) const {
@@ -39,6 +40,7 @@ struct Eight<__bf16> {
 template <>
 struct Eight<float> {
   row_u32x4 a, b;
+  __device__ inline void clear() { a = b = row_u32x4{0, 0, 0, 0}; }
   __device__ inline void load(const float* p) {
     a = ((const Raw16*)p)->v;
     b = ((const Raw16*)(p + 4))->v;
@@ -60,6 +62,14 @@ struct Eight<float> {
 __device__ inline float lanes_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
+}
+
+// A barrier that orders LDS only: __syncthreads also waits for every global load
+// and store of the wave, and with it for the next row's loads.
+__device__ inline void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // ------------------------------------------------------------------ random bits
