@@ -17,7 +17,7 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 PASSES = {"fused": 0, "fwd": 1, "bwd": 2}
 TIMING_KINDS = {"logits": 0, "rows": 1, "dh": 2, "dh_reduce": 3, "dw": 4, "other": 5, "topk": 6, "embed": 7,
-                "sample": 8, "fp8": 9, "norm": 10, "logprob": 11}
+                "sample": 8, "fp8": 9}
 
 _lib = None
 

@@ -291,7 +291,7 @@ struct TraceRange {
 };
 
 // ------------------------------------------------------------------ timing
-enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_NORM, T_LOGPROB, T_KINDS };
+enum Kind { T_LOGITS = 0, T_ROWS, T_DH, T_DHRED, T_DW, T_OTHER, T_TOPK, T_EMBED, T_SAMPLE, T_FP8, T_KINDS };
 struct TimingState {
   bool on = false;
   std::vector<std::pair<hipEvent_t, hipEvent_t>> pool;
@@ -937,7 +937,7 @@ int ckl_logprobs(int dtype, const void* logits, int64_t N, int64_t V, int64_t ro
   p.top_ids = top_ids;
   p.top_logp = top_logp;
   try {
-    Timed t(T_LOGPROB, stream);
+    Timed t(T_OTHER, stream);
     CKL_TRY(launch_logprob(to_dt(dtype), p, need ? workspace : nullptr, stream));
     return CKL_OK;
   } catch (...) {
@@ -973,7 +973,7 @@ int ckl_logprobs_bwd(int dtype, const void* logits, int64_t N, int64_t V, int64_
   p.dentropy = dentropy;
   p.out = dlogits;
   try {
-    Timed t(T_LOGPROB, stream);
+    Timed t(T_OTHER, stream);
     CKL_TRY(launch_logprob_grad(to_dt(dtype), p, stream));
     return CKL_OK;
   } catch (...) {
@@ -1018,7 +1018,7 @@ int ckl_head_logprobs(int dtype, const void* H, const void* W, const int32_t* id
     float* part_a = (float*)(ws + L.parta_off);
     TraceRange range("ckl head logprobs N=%lld d=%lld V=%lld T=%lld chunk=%lld", (long long)N, (long long)d, (long long)V,
                      (long long)T, (long long)L.C);
-    Timed t(T_LOGPROB, stream);
+    Timed t(T_OTHER, stream);
     if (T > 0) CKL_TRY(launch_given_logits(c.dt, p, stream));
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
       const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
@@ -1066,7 +1066,7 @@ int ckl_head_logprobs_bwd(int dtype, const void* H, const void* W, const int32_t
     const void* Wt = L.tiled ? ws + L.w_off : W;
     TraceRange range("ckl head logprobs backward N=%lld d=%lld V=%lld T=%lld chunk=%lld", (long long)N, (long long)d,
                      (long long)V, (long long)T, (long long)L.C);
-    Timed t(T_LOGPROB, stream);
+    Timed t(T_OTHER, stream);
     if (L.tiled) CKL_TRY(launch_tile_copy(c.dt, W, V, d, ws + L.w_off, stream));
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
       const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
@@ -1100,7 +1100,7 @@ int ckl_dropout(int dtype, const void* x, int64_t n, const ckl_drop* how, void* 
   const uintptr_t el = dtype == CKL_DTYPE_BF16 ? 2 : 4;
   if (!x || !out || !aligned(x, el) || !aligned(out, el)) return CKL_EINVAL;
   try {
-    Timed t(T_NORM, stream);
+    Timed t(T_OTHER, stream);
     CKL_TRY(launch_dropout(to_dt(dtype), x, n, r, out, stream));
     return CKL_OK;
   } catch (...) {
@@ -1124,7 +1124,7 @@ int ckl_add_norm(int dtype, const void* y, const void* r, const ckl_norm* how, i
   p.x = x;
   p.stats = stats;
   try {
-    Timed t(T_NORM, stream);
+    Timed t(T_OTHER, stream);
     CKL_TRY(launch_add_norm(to_dt(dtype), p, stream));
     return CKL_OK;
   } catch (...) {
@@ -1177,7 +1177,7 @@ int ckl_add_norm_bwd(int dtype, const void* y, const void* r, const ckl_norm* ho
     q.dw_pre = dw_pre;
     q.dgate = dgate;
     q.part = (float*)workspace;
-    Timed t(T_NORM, stream);
+    Timed t(T_OTHER, stream);
     CKL_TRY(launch_add_norm_bwd(to_dt(dtype), p, q, stream));
     return CKL_OK;
   } catch (...) {

@@ -505,15 +505,14 @@ int ckl_debug_rows(const float* Z, const int32_t* idx, const float* tlogit, cons
                    void* G_out, float* kl_out, float* lse_out, hipStream_t stream);
 
 /* Measurement support.  While enabled, every kernel launch of a loss call
- * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk), and all launches of one ckl_embed,
- * ckl_embed_bwd, ckl_sample, ckl_quantize_fp8, ckl_matmul_fp8, ckl_dropout,
- * ckl_add_norm*, ckl_logprobs* or ckl_head_logprobs* call together, are bracketed by
- * HIP events on the call's stream.  ckl_timing_query waits for the recorded events and returns
- * the summed milliseconds and launch count of one kernel kind: 0 logits GEMM,
- * 1 row pass, 2 dH GEMM, 3 dH split reduce, 4 dW GEMM, 5 other, 6 top-K
- * (ckl_topk), 7 embedding, 8 sampling, 9 8-bit products and quantisers,
- * 10 dropout and the residual's norms, 11 log-probabilities.  Not for concurrent use from several
- * threads. */
+ * (ckl_fwd_bwd*, ckl_fwd, ckl_bwd, ckl_topk), and all launches of one call of the
+ * other operators together, are bracketed by HIP events on the call's stream.
+ * ckl_timing_query waits for the recorded events and returns the summed
+ * milliseconds and launch count of one kernel kind: 0 logits GEMM, 1 row pass,
+ * 2 dH GEMM, 3 dH split reduce, 4 dW GEMM, 5 other (of a loss call, and the
+ * log-probabilities, the residual's norms and dropout), 6 top-K (ckl_topk),
+ * 7 embedding, 8 sampling, 9 8-bit products and quantisers.  Not for concurrent use
+ * from several threads. */
 int ckl_timing_enable(int on);
 int ckl_timing_query(int kind, double* total_ms, int64_t* launches);
 
