@@ -535,7 +535,9 @@ int logprob_shape(int dtype, const void* logits, int64_t N, int64_t V, int64_t l
 // Device workspace of a call on hidden states with chunks of C rows.
 struct HeadLayout {
   int64_t C = 0, pblk = 0;
-  int n_slices = 0, splits = 0;
+  int n_slices = 0;
+  HeadTile tile = TILE_256;  // forward: the contraction's
+  HeadSplit split{TILE_256, 0};
   bool tiled = false;  // backward: a tiled copy of W
   uint64_t live_off = 0, hc_off = 0, vidx_off = 0, pos_off = 0, part_off = 0, parta_off = 0, w_off = 0, g_off = 0,
            coef_off = 0, slab_off = 0, dw_off = 0, total = 0;
@@ -548,7 +550,8 @@ HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C
   HeadLayout L;
   L.C = C;
   L.pblk = tile_row_stride(V);
-  L.n_slices = (int)((V + 127) / 128);
+  L.tile = head_logits_tile(esz == 2 ? DT_BF16 : DT_F32, C, V);
+  L.n_slices = (int)((V + head_slice(L.tile) - 1) / head_slice(L.tile));
   uint64_t off = 0;
   const auto take = [&off](uint64_t bytes) {
     const uint64_t at = off;
@@ -565,10 +568,10 @@ HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C
   } else {
     L.tiled = N >= kTileCopyRows;
     if (L.tiled) L.w_off = take((uint64_t)((V + 63) / 64) * tile_row_stride(d) * esz);
-    L.splits = dh_splits(esz == 2 ? DT_BF16 : DT_F32, C, d, V);
+    L.split = head_dh_split(esz == 2 ? DT_BF16 : DT_F32, C, d, V);
     L.g_off = take((uint64_t)((C + 63) / 64) * L.pblk * esz);
     L.coef_off = take((uint64_t)C * 16);
-    L.slab_off = take((uint64_t)L.splits * C * d * 4);
+    L.slab_off = take((uint64_t)L.split.splits * C * d * 4);
     if (dw_sum && C < N) L.dw_off = take((uint64_t)V * d * 4);  // a bf16 dW's sums over chunks
   }
   L.total = off;
@@ -1019,13 +1022,12 @@ int ckl_head_logprobs(int dtype, const void* H, const void* W, const int32_t* id
     TraceRange range("ckl head logprobs N=%lld d=%lld V=%lld T=%lld chunk=%lld", (long long)N, (long long)d, (long long)V,
                      (long long)T, (long long)L.C);
     Timed t(T_OTHER, stream);
-    if (T > 0) CKL_TRY(launch_given_logits(c.dt, p, stream));
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
       const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
       Chunk k;
       CKL_TRY(head_chunk(c, L, H, d, r0, rows, entropy + r0, &k, stream));
-      CKL_TRY(launch_head_stats(c.dt, p, k.Hc, rows, part, part_a, L.n_slices, k.live, stream));
-      CKL_TRY(launch_head_rows(p, r0, rows, part, part_a, L.n_slices, k.pos, stream));
+      CKL_TRY(launch_head_stats(c.dt, L.tile, p, k.Hc, rows, part, part_a, L.n_slices, k.live, stream));
+      CKL_TRY(launch_head_rows(c.dt, p, r0, rows, part, part_a, L.n_slices, k.pos, stream));
     }
     return CKL_OK;
   } catch (...) {
@@ -1074,15 +1076,14 @@ int ckl_head_logprobs_bwd(int dtype, const void* H, const void* W, const int32_t
       // (the compaction writes a zero per masked row somewhere: the rows' coefficients, written after it)
       CKL_TRY(head_chunk(c, L, H, d, r0, rows, (float*)coef, &k, stream));
       CKL_TRY(launch_head_grad(c.dt, p, Wt, L.tiled, k.Hc, r0, rows, k.vidx, k.live, coef, G, L.pblk, stream));
-      int splits = dh_splits(c.dt, rows, d, V);
-      const int64_t cap = (int64_t)L.splits * L.C / rows;  // slab capacity in splits of this chunk
-      if (splits > cap) splits = dh_fit_splits(c.dt, V, (int)cap);
-      CKL_TRY(launch_dh(c.dt, G, L.pblk, Wt, V, d, rows, slab, splits, k.live, stream, L.tiled));
-      CKL_TRY(launch_dh_reduce(c.dt, slab, splits, rows, d, k.pos, (char*)dH + (size_t)r0 * d * c.esz, stream));
-      if (round && r0 + rows >= N)
-        CKL_TRY(launch_dw_round(G, L.pblk, k.Hc, V, d, rows, r0 > 0 ? sums : nullptr, dW, k.live, stream));
-      else
-        CKL_TRY(launch_dw(c.dt, G, L.pblk, k.Hc, V, d, rows, sums, r0 > 0 || accumulate ? 1 : 0, k.live, stream));
+      HeadSplit h = head_dh_split(c.dt, rows, d, V);
+      const int64_t cap = (int64_t)L.split.splits * L.C / rows;  // slab capacity in splits of this chunk
+      if (h.splits > cap) h.splits = dh_fit_splits(c.dt, V, (int)cap);
+      CKL_TRY(launch_head_dh(c.dt, h, G, L.pblk, Wt, L.tiled, V, d, rows, slab, k.live, stream));
+      CKL_TRY(launch_dh_reduce(c.dt, slab, h.splits, rows, d, k.pos, (char*)dH + (size_t)r0 * d * c.esz, stream));
+      const bool last = round && r0 + rows >= N;
+      CKL_TRY(launch_head_dw(c.dt, G, L.pblk, k.Hc, V, d, rows, last && r0 > 0 ? sums : nullptr, sums,
+                             r0 > 0 || accumulate ? 1 : 0, last ? dW : nullptr, k.live, stream));
     }
     return CKL_OK;
   } catch (...) {

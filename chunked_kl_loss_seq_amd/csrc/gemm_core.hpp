@@ -80,7 +80,7 @@ enum EpilogueKind : int {
   EPI_LOGITS = 0,  // per (n, 128-row slice of m): mx = max D, P[n][m] = exp(D[m][n] - mx), (mx, sum P)
   EPI_SLAB = 1,    // out[m][n] = D[m][n] (fp32), one slab per k-split
   EPI_ACCUM = 2,   // out[m][n] = D[m][n] (beta = 0) or out[m][n] += D[m][n] (beta = 1)
-  EPI_STATS = 3,   // per (n, 128-row slice of m): mx = max D, (mx, sum exp(D - mx)) and sum exp(D - mx) (D - mx)
+  EPI_STATS = 3,   // per (n, slice of a wave's rows of m): mx = max D, (mx, sum exp(D - mx)), sum exp(D - mx) (D - mx)
   EPI_GRAD = 4,    // out[n][m] = -p (c + u l), l = log p = D[m][n] - max - log sum, by the row's coefficients
   EPI_ROUND = 5,   // out[m][n] = D[m][n], plus old[m][n] where given, rounded to bf16
 };
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
   static_assert(WTM % MS == 0 && WTN % MS == 0, "wave tile must be a multiple of the MFMA block");
   static_assert(SUB % 2 == 0 && SUB >= 2, "the pipeline assumes an even sub-step count");
   static_assert(NS >= 2 && (NS - 1) * NIT < 64, "stages in flight must fit the vmcnt counter");
-  static_assert(!kLogits || WTM == 128, "logit partials are per 128-row slice");
+  static_assert(EPI != EPI_LOGITS || WTM == 128, "logit partials are per 128-row slice");
   constexpr int STAGE = DA::kBytes + DB::kBytes;
   constexpr int SPARE = DA::kSpare > DB::kSpare ? DA::kSpare : DB::kSpare;
   constexpr int XOFF = NS * STAGE + SPARE;  // id tables (logits only)
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
 #pragma unroll
           for (int q = 0; q < NMF; ++q)
             acc[q / FN][q % FN] = mfma_block(fa[fbuf][q / FN], fb[fbuf][q % FN], acc[q / FN][q % FN]);
-          if constexpr (MS == 16) {
+          if constexpr (MS == 16 && NMF >= 2 * (FM + FN)) {
             // one fragment read every two MFMAs (measured faster than the
             // scheduler's own order for this loop)
 #pragma unroll
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
     const bool mfull = mw + WTM <= p.valid_m;
     auto run0 = [&](int i, int q) { return MS == 32 ? 32 * i + 8 * q + 4 * sub : 16 * i + 4 * sub; };
     if constexpr (EPI == EPI_STATS) {
-      const int slice = (int)(mw / 128);
+      const int slice = (int)(mw / WTM);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int64_t n = nw + MS * j + cl;
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
             acc[i][j][r] = rok && (mfull || (int)mw + run0(i, r / 4) + r % 4 < vm) ? g : 0.f;
           }
       }
-      if constexpr (sizeof(T) == 2) {
+      if constexpr (sizeof(T) == 2 && WTM == 128) {
         // through the wave's 16 KiB of LDS, as 16 coalesced 1 KiB stores (see the logits epilogue below)
         static_assert(WTM == 128 && WTN == 64 && NW * 16384 <= NS * STAGE, "one wave = two 64 x 64 tiles");
         typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
@@ -809,9 +809,16 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
 #pragma unroll
             for (int q = 0; q < RUNS; ++q) {
               const int64_t m = mw + run0(i, q);
-              if (m < p.valid_m)
-                *(f32x4*)(prow + (m >> 6) * 4096 + (m & 63)) =
-                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+              // zeros up to the end of the last 16 bytes: dH's copies of G go by those
+              if (m >= ((p.valid_m + 7) & ~(int64_t)7)) continue;
+              T* to = prow + (m >> 6) * 4096 + (m & 63);
+              if constexpr (sizeof(T) == 2) {
+                typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
+                *(bf16x4*)to = bf16x4{(__bf16)acc[i][j][4 * q], (__bf16)acc[i][j][4 * q + 1],
+                                      (__bf16)acc[i][j][4 * q + 2], (__bf16)acc[i][j][4 * q + 3]};
+              } else {
+                *(f32x4*)to = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+              }
             }
         }
       }

@@ -22,78 +22,109 @@ namespace {
 
 constexpr float kFar = -1000.f;  // exp(kFar) is 0 in fp32
 
-// One wave per (row, given token): z = H_n . W_id in fp32, kept in logp until the
-// row's statistics are known.
+// z = H_n . W_id in fp32, by one wave.
 template <typename T>
-__global__ void __launch_bounds__(256) given_logits_kernel(HeadArgs p) {
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= p.N * p.T) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t n = i / p.T;
-  const int32_t id = p.ids[i];
-  if (id < 0 || id >= p.V || (p.mask != nullptr && p.mask[n] == 0)) return;
+__device__ inline float given_logit(const HeadArgs& p, int64_t n, int32_t id) {
   const T* h = (const T*)p.H + n * p.d;
   const T* w = (const T*)p.W + (int64_t)id * p.d;
   float s = 0.f;
-  for (int64_t k = 8 * lane; k < p.d; k += 512) {
+  int64_t k = 8 * (threadIdx.x & 63);
+  for (; k + 512 < p.d; k += 1024) {  // two vectors of each in flight
+    Eight<T> a, b, c, e;
+    a.load(h + k);
+    b.load(w + k);
+    c.load(h + k + 512);
+    e.load(w + k + 512);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(a.get(i), b.get(i), s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(c.get(i), e.get(i), s);
+  }
+  if (k < p.d) {
     Eight<T> a, b;
     a.load(h + k);
     b.load(w + k);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(a.get(e), b.get(e), s);
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(a.get(i), b.get(i), s);
   }
-  s = lanes_sum(s, 64);
-  if (lane == 0) p.logp[i] = s;
+  return lanes_sum(s, 64);
 }
 
-// Rows [r0, r0 + rows) of the call: the slices' statistics to the rows'.  With a
-// compacted chunk, pos gives each row's place in it, -1 for a masked one.
-__global__ void __launch_bounds__(256) head_rows_kernel(HeadArgs p, int64_t r0, const float2* __restrict__ part,
-                                                       const float* __restrict__ part_a, int n_slices,
-                                                       const int* __restrict__ pos) {
-  __shared__ float red[12];
+// Rows [r0, r0 + rows) of the call: the slices' statistics to the rows', and the
+// given tokens' log-probabilities.  With a compacted chunk, pos gives each row's
+// place in it, -1 for a masked one.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) head_rows_kernel(HeadArgs p, int64_t r0, const float2* __restrict__ part,
+                                                      const float* __restrict__ part_a, int n_slices,
+                                                      const int* __restrict__ pos) {
+  constexpr int NW = NT / 64, U = 8;  // slices in flight per thread
+  __shared__ float red[3 * NW];
   const int64_t row = r0 + blockIdx.x;
   const int t = threadIdx.x, w = t >> 6;
   const int64_t at = pos != nullptr ? pos[blockIdx.x] : (int64_t)blockIdx.x;
   if (at < 0) {
-    for (int i = t; i < p.T; i += 256) p.logp[row * p.T + i] = 0.f;
+    for (int i = t; i < p.T; i += NT) p.logp[row * p.T + i] = 0.f;
     if (t == 0) p.entropy[row] = p.stats[row] = p.stats[p.N + row] = 0.f;
     return;
   }
   const float2* q = part + at * n_slices;
   const float* qa = part_a + at * n_slices;
-  float M = -INFINITY;
-  for (int i = t; i < n_slices; i += 256) M = fmaxf(M, q[i].x);
+  float M = -INFINITY, s = 0.f, a = 0.f;
+  for (int i0 = t; i0 < n_slices; i0 += U * NT) {
+    float2 v[U];
+    float va[U];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
-  if ((t & 63) == 0) red[w] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float s = 0.f, a = 0.f;
-  for (int i = t; i < n_slices; i += 256) {
-    const float2 v = q[i];
-    const float dm = fmaxf(v.x - M, kFar), k = __expf(dm);
-    s = __builtin_fmaf(v.y, k, s);
-    a = __builtin_fmaf(__builtin_fmaf(v.y, dm, qa[i]), k, a);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * NT < n_slices ? i0 + u * NT : i0;
+      v[u] = q[i];
+      va[u] = qa[i];
+    }
+    float m = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = fmaxf(m, v[u].x);
+    const float d0 = fmaxf(M - m, kFar), k0 = __expf(d0);
+    a = __builtin_fmaf(s, d0, a) * k0;
+    s *= k0;
+    M = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * NT >= n_slices) continue;
+      const float dm = fmaxf(v[u].x - m, kFar), k = __expf(dm);
+      s = __builtin_fmaf(v[u].y, k, s);
+      a = __builtin_fmaf(__builtin_fmaf(v[u].y, dm, va[u]), k, a);
+    }
   }
-  s = lanes_sum(s, 64);
-  a = lanes_sum(a, 64);
+  float top = M;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if ((t & 63) == 0) red[w] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NW; ++i) top = fmaxf(top, red[i]);
+  const float d1 = fmaxf(M - top, kFar), k1 = __expf(d1);
+  a = lanes_sum(__builtin_fmaf(s, d1, a) * k1, 64);
+  s = lanes_sum(s * k1, 64);
   if ((t & 63) == 0) {
-    red[4 + w] = s;
-    red[8 + w] = a;
+    red[NW + w] = s;
+    red[2 * NW + w] = a;
   }
   __syncthreads();
-  s = (red[4] + red[5]) + (red[6] + red[7]);
-  a = (red[8] + red[9]) + (red[10] + red[11]);
+  s = a = 0.f;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    s += red[NW + i];
+    a += red[2 * NW + i];
+  }
   const float logs = logf(s), h = logs - a / s;
-  for (int i = t; i < p.T; i += 256) {
+  for (int i = w; i < p.T; i += NW) {
     const int32_t id = p.ids[row * p.T + i];
-    float* l = p.logp + row * p.T + i;
-    *l = id >= 0 && id < p.V ? (*l - M) - logs : 0.f;
+    const bool in = id >= 0 && id < p.V;
+    const float z = in ? given_logit<T>(p, row, id) : 0.f;
+    if ((t & 63) == 0) p.logp[row * p.T + i] = in ? (z - top) - logs : 0.f;
   }
   if (t == 0) {
     p.entropy[row] = h < 0.f ? 0.f : h;
-    p.stats[row] = M;
+    p.stats[row] = top;
     p.stats[p.N + row] = logs;
   }
 }
@@ -147,14 +178,49 @@ __global__ void __launch_bounds__(256) head_given_kernel(HeadGradArgs p, int64_t
   }
 }
 
+// Tiles of an m x n product: 256 x 256 (eight waves, the loss's), 128 x 128 and
+// 64 x 64 (four waves), the last two for products that would leave compute units
+// without a tile.
+int tile_edge(HeadTile t) { return t == TILE_256 ? 256 : t == TILE_128 ? 128 : 64; }
+int64_t tiles_of(int64_t m, int64_t n, HeadTile t) {
+  const int e = tile_edge(t);
+  return ((m + e - 1) / e) * ((n + e - 1) / e);
+}
+// The tile with the least time by this count: tiles a compute unit takes in turn x
+// a tile's work, over the rate that it reaches with all units busy (bf16: 1,305
+// TFLOP/s at 256 x 256, 1,021 at 128, 706 at 64; fp32: 130, 126 and 121).
+HeadTile tile_for(Dtype dt, int64_t m, int64_t n, int64_t splits) {
+  static const double work[2][3] = {{1.0, 0.25 / 0.78, 0.0625 / 0.54}, {1.0, 0.25 / 0.97, 0.0625 / 0.93}};
+  HeadTile best = TILE_256;
+  double least = 0;
+  for (int t = TILE_256; t <= TILE_64; ++t) {
+    const int64_t turns = (tiles_of(m, n, (HeadTile)t) * splits + 255) / 256;
+    const double cost = (double)turns * work[dt == DT_BF16 ? 0 : 1][t];
+    if (t == TILE_256 || cost < least) {
+      least = cost;
+      best = (HeadTile)t;
+    }
+  }
+  return best;
+}
+
+template <typename T, bool AK, bool BKM, int EPI, int MS, bool WITH_256 = true>
+hipError_t launch_tile(HeadTile t, const GemmParams& p, hipStream_t s) {
+  if constexpr (WITH_256) {
+    if (t == TILE_256) return launch_gemm<T, 256, 256, 2, 4, AK, BKM, EPI, 128, 2, MS>(p, s);
+  }
+  if (t == TILE_128) return launch_gemm<T, 128, 128, 2, 2, AK, BKM, EPI, 128, 2, MS>(p, s);
+  return launch_gemm<T, 64, 64, 2, 2, AK, BKM, EPI, 128, 3, MS>(p, s);
+}
+
 GemmParams logits_product(Dtype dt, const void* W, bool tiled, const void* Hc, int64_t V, int64_t d, int64_t rows,
-                          const int* live) {
+                          HeadTile t, const int* live) {
   GemmParams p{};
   p.live = live;
   p.a = tiled ? Operand{W, 0, V, d, tile_row_stride(d)} : Operand{W, d, V, d, 0};
   p.b = Operand{Hc, d, rows, d, 0};
-  p.tiles_m = cdiv64(V, 256);
-  p.tiles_n = cdiv64(rows, 256);
+  p.tiles_m = cdiv64(V, tile_edge(t));
+  p.tiles_n = cdiv64(rows, tile_edge(t));
   p.k_tiles = cdiv64(d, dt == DT_BF16 ? 64 : 32);
   p.splits = 1;
   p.k_tiles_per_split = p.k_tiles;
@@ -166,28 +232,34 @@ GemmParams logits_product(Dtype dt, const void* W, bool tiled, const void* Hc, i
 
 }  // namespace
 
-hipError_t launch_given_logits(Dtype dt, const HeadArgs& p, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N * p.T + 3) / 4));
-  if (dt == DT_BF16)
-    hipLaunchKernelGGL((given_logits_kernel<__bf16>), grid, dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((given_logits_kernel<float>), grid, dim3(256), 0, s, p);
-  return hipGetLastError();
-}
+HeadTile head_logits_tile(Dtype dt, int64_t rows, int64_t V) { return tile_for(dt, V, rows, 1); }
 
-hipError_t launch_head_stats(Dtype dt, const HeadArgs& a, const void* Hc, int64_t rows, float2* part, float* part_a,
-                             int n_slices, const int* live, hipStream_t s) {
-  GemmParams p = logits_product(dt, a.W, false, Hc, a.V, a.d, rows, live);
+// Ids of a slice of the statistics: what one wave of a tile covers.
+int head_slice(HeadTile t) { return tile_edge(t) / 2; }
+
+hipError_t launch_head_stats(Dtype dt, HeadTile t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
+                             float* part_a, int n_slices, const int* live, hipStream_t s) {
+  GemmParams p = logits_product(dt, a.W, false, Hc, a.V, a.d, rows, t, live);
   p.part = part;
   p.part_a = part_a;
   p.n_slices = n_slices;
-  if (dt == DT_BF16) return launch_gemm<__bf16, 256, 256, 2, 4, true, true, EPI_STATS, 128, 2, 16>(p, s);
-  return launch_gemm<float, 256, 256, 2, 4, true, true, EPI_STATS, 128, 2>(p, s);
+  if (dt == DT_BF16) return launch_tile<__bf16, true, true, EPI_STATS, 16>(t, p, s);
+  return launch_tile<float, true, true, EPI_STATS, 32>(t, p, s);
 }
 
-hipError_t launch_head_rows(const HeadArgs& p, int64_t r0, int64_t rows, const float2* part, const float* part_a,
-                            int n_slices, const int* pos, hipStream_t s) {
-  hipLaunchKernelGGL(head_rows_kernel, dim3((unsigned)rows), dim3(256), 0, s, p, r0, part, part_a, n_slices, pos);
+hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t rows, const float2* part,
+                            const float* part_a, int n_slices, const int* pos, hipStream_t s) {
+  // few rows of many slices: a workgroup of 1,024 threads a row
+  const bool wide = rows < 512 && n_slices > 2048;
+  const dim3 grid((unsigned)rows), block(wide ? 1024 : 256);
+  if (dt == DT_BF16 && wide)
+    hipLaunchKernelGGL((head_rows_kernel<__bf16, 1024>), grid, block, 0, s, p, r0, part, part_a, n_slices, pos);
+  else if (dt == DT_BF16)
+    hipLaunchKernelGGL((head_rows_kernel<__bf16, 256>), grid, block, 0, s, p, r0, part, part_a, n_slices, pos);
+  else if (wide)
+    hipLaunchKernelGGL((head_rows_kernel<float, 1024>), grid, block, 0, s, p, r0, part, part_a, n_slices, pos);
+  else
+    hipLaunchKernelGGL((head_rows_kernel<float, 256>), grid, block, 0, s, p, r0, part, part_a, n_slices, pos);
   return hipGetLastError();
 }
 
@@ -198,12 +270,13 @@ hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, bool
   hipLaunchKernelGGL(head_coef_kernel, grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  GemmParams p = logits_product(dt, W, tiled, Hc, a.V, a.d, rows, live);
+  const HeadTile t = head_logits_tile(dt, rows, a.V);
+  GemmParams p = logits_product(dt, W, tiled, Hc, a.V, a.d, rows, t, live);
   p.coef = coef;
   p.out = G;
   p.ldo = gblk;
-  e = dt == DT_BF16 ? launch_gemm<__bf16, 256, 256, 2, 4, true, true, EPI_GRAD, 128, 2, 16>(p, s)
-                    : launch_gemm<float, 256, 256, 2, 4, true, true, EPI_GRAD, 128, 2>(p, s);
+  e = dt == DT_BF16 ? launch_tile<__bf16, true, true, EPI_GRAD, 16>(t, p, s)
+                    : launch_tile<float, true, true, EPI_GRAD, 32>(t, p, s);
   if (e != hipSuccess || a.T == 0) return e;
   if (dt == DT_BF16)
     hipLaunchKernelGGL((head_given_kernel<__bf16>), grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef, (__bf16*)G, gblk);
@@ -212,24 +285,67 @@ hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, bool
   return hipGetLastError();
 }
 
-hipError_t launch_dw_round(const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
-                           const float* old, void* dW, const int* live, hipStream_t s) {
+// The split of dH's reduction over V and its tile: with enough 256 x 256 tiles, the
+// loss's (dh_splits); else 64 x 64 tiles in as many splits as give every compute
+// unit two, of at least 8 k-steps each.
+HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V) {
+  const int s256 = dh_splits(dt, rows, d, V);
+  if (tile_for(dt, rows, d, s256) == TILE_256) return HeadSplit{TILE_256, s256};
+  const int64_t tiles = tiles_of(rows, d, TILE_64), steps = (V + (dt == DT_BF16 ? 63 : 31)) / (dt == DT_BF16 ? 64 : 32);
+  int64_t n = (512 + tiles - 1) / tiles;
+  if (n > steps / 8) n = steps / 8;
+  if (n > 32) n = 32;
+  const int fit = n > 1 ? dh_fit_splits(dt, V, (int)n) : 1;
+  return HeadSplit{tile_for(dt, rows, d, fit), fit};
+}
+
+hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, bool tiled, int64_t V,
+                          int64_t d, int64_t rows, float* slab, const int* live, hipStream_t s) {
+  if (h.tile == TILE_256) return launch_dh(dt, G, gblk, W, V, d, rows, slab, h.splits, live, s, tiled);
+  GemmParams p{};
+  p.live = live;
+  p.a = Operand{G, 0, rows, V, gblk};  // tiled: storage row = token, column = vocabulary id
+  // storage row = vocabulary id (k), column = d (n)
+  p.b = tiled ? Operand{W, 0, d, V, tile_row_stride(d)} : Operand{W, d, d, V, 0};
+  p.tiles_m = cdiv64(rows, tile_edge(h.tile));
+  p.tiles_n = cdiv64(d, tile_edge(h.tile));
+  p.k_tiles = cdiv64(V, dt == DT_BF16 ? 64 : 32);
+  p.k_tiles_per_split = cdiv64(p.k_tiles, h.splits);
+  p.splits = cdiv64(p.k_tiles, p.k_tiles_per_split);
+  p.group_m = 4;
+  p.out = slab;
+  p.ldo = d;
+  p.split_stride = rows * d;
+  p.valid_m = rows;
+  p.valid_n = d;
+  if (p.splits != h.splits) return hipErrorInvalidValue;
+  if (dt == DT_BF16) return launch_tile<__bf16, true, false, EPI_SLAB, 32, false>(h.tile, p, s);
+  return launch_tile<float, true, false, EPI_SLAB, 32, false>(h.tile, p, s);
+}
+
+hipError_t launch_head_dw(Dtype dt, const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
+                          const float* old, float* sums, int beta, void* rounded, const int* live, hipStream_t s) {
+  const HeadTile t = tile_for(dt, V, d, 1);
+  if (rounded == nullptr && t == TILE_256) return launch_dw(dt, G, gblk, Hc, V, d, rows, sums, beta, live, s);
   GemmParams p{};
   p.live = live;
   p.a = Operand{G, 0, V, rows, gblk};  // tiled: storage row = token (k), column = vocabulary id (m)
   p.b = Operand{Hc, d, d, rows, 0};
-  p.tiles_m = cdiv64(V, 256);
-  p.tiles_n = cdiv64(d, 256);
-  p.k_tiles = cdiv64(rows, 64);
+  p.tiles_m = cdiv64(V, tile_edge(t));
+  p.tiles_n = cdiv64(d, tile_edge(t));
+  p.k_tiles = cdiv64(rows, dt == DT_BF16 ? 64 : 32);
   p.splits = 1;
   p.k_tiles_per_split = p.k_tiles;
   p.group_m = 1;
-  p.out = dW;
+  p.out = rounded != nullptr ? rounded : (void*)sums;
   p.ldo = d;
   p.old = old;
+  p.beta = beta;
   p.valid_m = V;
   p.valid_n = d;
-  return launch_gemm<__bf16, 256, 256, 2, 4, false, false, EPI_ROUND, 128, 2>(p, s);
+  if (rounded != nullptr) return launch_tile<__bf16, false, false, EPI_ROUND, 32>(t, p, s);
+  if (dt == DT_BF16) return launch_tile<__bf16, false, false, EPI_ACCUM, 32, false>(t, p, s);
+  return launch_tile<float, false, false, EPI_ACCUM, 32, false>(t, p, s);
 }
 
 }  // namespace ckl

@@ -223,14 +223,16 @@ struct HeadArgs {
   float* entropy;       // [N]
   float* stats;         // [2, N]
 };
-// logp[n][t] = H_n . W_id for ids in [0, V) of rows that count.
-hipError_t launch_given_logits(Dtype dt, const HeadArgs& p, hipStream_t s);
+// Edge of the square tiles of a product (see kernels_head.hip).
+enum HeadTile : int { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
+HeadTile head_logits_tile(Dtype dt, int64_t rows, int64_t V);
+int head_slice(HeadTile t);  // ids of a slice of the statistics
 // The slices' statistics of a chunk of rows Hc (all of them, or the *live compacted ones).
-hipError_t launch_head_stats(Dtype dt, const HeadArgs& a, const void* Hc, int64_t rows, float2* part, float* part_a,
-                             int n_slices, const int* live, hipStream_t s);
+hipError_t launch_head_stats(Dtype dt, HeadTile t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
+                             float* part_a, int n_slices, const int* live, hipStream_t s);
 // Entropy, stats and log-probabilities of rows [r0, r0 + rows); pos: of a compacted chunk, or null.
-hipError_t launch_head_rows(const HeadArgs& p, int64_t r0, int64_t rows, const float2* part, const float* part_a,
-                            int n_slices, const int* pos, hipStream_t s);
+hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t rows, const float2* part,
+                            const float* part_a, int n_slices, const int* pos, hipStream_t s);
 struct HeadGradArgs {
   int64_t N, d, V;
   const int32_t* ids;      // [N, T]
@@ -245,9 +247,18 @@ struct HeadGradArgs {
 hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, bool tiled, const void* Hc, int64_t r0,
                             int64_t rows, const int* vidx, const int* live, float4* coef, void* G, int64_t gblk,
                             hipStream_t s);
-// bf16 dW = G^T H_c, plus the fp32 `old` where given (bf16 operands).
-hipError_t launch_dw_round(const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
-                           const float* old, void* dW, const int* live, hipStream_t s);
+// dH's partial slabs as launch_dh leaves them, in the given tile and splits.
+struct HeadSplit {
+  HeadTile tile;
+  int splits;
+};
+HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V);
+hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, bool tiled, int64_t V,
+                          int64_t d, int64_t rows, float* slab, const int* live, hipStream_t s);
+// dW: fp32 `sums` (+)= G^T H_c; or, where `rounded` is not null, that bf16 array = G^T
+// H_c, plus the fp32 `old` where given (bf16 operands).
+hipError_t launch_head_dw(Dtype dt, const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
+                          const float* old, float* sums, int beta, void* rounded, const int* live, hipStream_t s);
 
 constexpr int kMaxK = 2048;
 constexpr int kMaxTop = 512;  // alternatives of a row

@@ -143,6 +143,13 @@ def test_many_rows(ckl, dtype):
     check(ckl, 9000, 130, 24, dtype, 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d", [(500, 8000, 72), (600, 40000, 64), (40, 40000, 1032), (5000, 200, 2056), (2500, 700, 1032)])
+def test_tiles(ckl, dtype, N, V, d):
+    # products of 64, 128 and 256 wide tiles: the logits', dH's and dW's
+    check(ckl, N, V, d, dtype, 1)
+
+
 @pytest.mark.parametrize("T", [64, 2048])
 def test_given_tokens(ckl, T):
     check(ckl, 5, 300, 64, "bf16", T)
