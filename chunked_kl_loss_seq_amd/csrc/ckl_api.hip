@@ -538,13 +538,8 @@ struct HeadLayout {
   int n_slices = 0;
   HeadTile tile = TILE_256;  // forward: the contraction's
   HeadSplit split{TILE_256, 0};
-  bool tiled = false;  // backward: a tiled copy of W
-  uint64_t live_off = 0, hc_off = 0, vidx_off = 0, pos_off = 0, part_off = 0, parta_off = 0, w_off = 0, g_off = 0,
-           coef_off = 0, slab_off = 0, dw_off = 0, total = 0;
+  uint64_t live_off = 0, hc_off = 0, vidx_off = 0, pos_off = 0, part_off = 0, parta_off = 0, g_off = 0, coef_off = 0, slab_off = 0, dw_off = 0, total = 0;
 };
-
-// Rows from which the backward call copies W into tiles.
-constexpr int64_t kTileCopyRows = 8192;
 
 HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C, size_t esz, bool dw_sum) {
   HeadLayout L;
@@ -566,8 +561,6 @@ HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C
     L.part_off = take((uint64_t)C * L.n_slices * 8);
     L.parta_off = take((uint64_t)C * L.n_slices * 4);
   } else {
-    L.tiled = N >= kTileCopyRows;
-    if (L.tiled) L.w_off = take((uint64_t)((V + 63) / 64) * tile_row_stride(d) * esz);
     L.split = head_dh_split(esz == 2 ? DT_BF16 : DT_F32, C, d, V);
     L.g_off = take((uint64_t)((C + 63) / 64) * L.pblk * esz);
     L.coef_off = take((uint64_t)C * 16);
@@ -1065,21 +1058,19 @@ int ckl_head_logprobs_bwd(int dtype, const void* H, const void* W, const int32_t
     float4* coef = (float4*)(ws + L.coef_off);
     float* slab = (float*)(ws + L.slab_off);
     float* sums = round ? (L.C < N ? (float*)(ws + L.dw_off) : nullptr) : (float*)dW;
-    const void* Wt = L.tiled ? ws + L.w_off : W;
     TraceRange range("ckl head logprobs backward N=%lld d=%lld V=%lld T=%lld chunk=%lld", (long long)N, (long long)d,
                      (long long)V, (long long)T, (long long)L.C);
     Timed t(T_OTHER, stream);
-    if (L.tiled) CKL_TRY(launch_tile_copy(c.dt, W, V, d, ws + L.w_off, stream));
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
       const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
       Chunk k;
       // (the compaction writes a zero per masked row somewhere: the rows' coefficients, written after it)
       CKL_TRY(head_chunk(c, L, H, d, r0, rows, (float*)coef, &k, stream));
-      CKL_TRY(launch_head_grad(c.dt, p, Wt, L.tiled, k.Hc, r0, rows, k.vidx, k.live, coef, G, L.pblk, stream));
+      CKL_TRY(launch_head_grad(c.dt, p, W, k.Hc, r0, rows, k.vidx, k.live, coef, G, L.pblk, stream));
       HeadSplit h = head_dh_split(c.dt, rows, d, V);
       const int64_t cap = (int64_t)L.split.splits * L.C / rows;  // slab capacity in splits of this chunk
       if (h.splits > cap) h.splits = dh_fit_splits(c.dt, V, (int)cap);
-      CKL_TRY(launch_head_dh(c.dt, h, G, L.pblk, Wt, L.tiled, V, d, rows, slab, k.live, stream));
+      CKL_TRY(launch_head_dh(c.dt, h, G, L.pblk, W, V, d, rows, slab, k.live, stream));
       CKL_TRY(launch_dh_reduce(c.dt, slab, h.splits, rows, d, k.pos, (char*)dH + (size_t)r0 * d * c.esz, stream));
       const bool last = round && r0 + rows >= N;
       CKL_TRY(launch_head_dw(c.dt, G, L.pblk, k.Hc, V, d, rows, last && r0 > 0 ? sums : nullptr, sums,

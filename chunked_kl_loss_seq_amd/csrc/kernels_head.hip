@@ -213,11 +213,15 @@ hipError_t launch_tile(HeadTile t, const GemmParams& p, hipStream_t s) {
   return launch_gemm<T, 64, 64, 2, 2, AK, BKM, EPI, 128, 3, MS>(p, s);
 }
 
-GemmParams logits_product(Dtype dt, const void* W, bool tiled, const void* Hc, int64_t V, int64_t d, int64_t rows,
-                          HeadTile t, const int* live) {
+// W is read as it lies: a copy in 64 x 64 tiles, as the loss makes for its three
+// contractions of every chunk, did not pay here at any length (both passes of 201,088 x
+// 2,880: 4,096 rows 14.93 ms without it and 15.27 with, 8,192 31.25 and 31.61, 32,768
+// 128.1 and 133.0).
+GemmParams logits_product(Dtype dt, const void* W, const void* Hc, int64_t V, int64_t d, int64_t rows, HeadTile t,
+                          const int* live) {
   GemmParams p{};
   p.live = live;
-  p.a = tiled ? Operand{W, 0, V, d, tile_row_stride(d)} : Operand{W, d, V, d, 0};
+  p.a = Operand{W, d, V, d, 0};
   p.b = Operand{Hc, d, rows, d, 0};
   p.tiles_m = cdiv64(V, tile_edge(t));
   p.tiles_n = cdiv64(rows, tile_edge(t));
@@ -239,7 +243,7 @@ int head_slice(HeadTile t) { return tile_edge(t) / 2; }
 
 hipError_t launch_head_stats(Dtype dt, HeadTile t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
                              float* part_a, int n_slices, const int* live, hipStream_t s) {
-  GemmParams p = logits_product(dt, a.W, false, Hc, a.V, a.d, rows, t, live);
+  GemmParams p = logits_product(dt, a.W, Hc, a.V, a.d, rows, t, live);
   p.part = part;
   p.part_a = part_a;
   p.n_slices = n_slices;
@@ -263,15 +267,14 @@ hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t row
   return hipGetLastError();
 }
 
-hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, bool tiled, const void* Hc, int64_t r0,
-                            int64_t rows, const int* vidx, const int* live, float4* coef, void* G, int64_t gblk,
-                            hipStream_t s) {
+hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, const void* Hc, int64_t r0, int64_t rows,
+                            const int* vidx, const int* live, float4* coef, void* G, int64_t gblk, hipStream_t s) {
   const dim3 grid((unsigned)((rows + 3) / 4));
   hipLaunchKernelGGL(head_coef_kernel, grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const HeadTile t = head_logits_tile(dt, rows, a.V);
-  GemmParams p = logits_product(dt, W, tiled, Hc, a.V, a.d, rows, t, live);
+  GemmParams p = logits_product(dt, W, Hc, a.V, a.d, rows, t, live);
   p.coef = coef;
   p.out = G;
   p.ldo = gblk;
@@ -299,14 +302,13 @@ HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V) {
   return HeadSplit{tile_for(dt, rows, d, fit), fit};
 }
 
-hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, bool tiled, int64_t V,
-                          int64_t d, int64_t rows, float* slab, const int* live, hipStream_t s) {
-  if (h.tile == TILE_256) return launch_dh(dt, G, gblk, W, V, d, rows, slab, h.splits, live, s, tiled);
+hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, int64_t V, int64_t d,
+                          int64_t rows, float* slab, const int* live, hipStream_t s) {
+  if (h.tile == TILE_256) return launch_dh(dt, G, gblk, W, V, d, rows, slab, h.splits, live, s, false);
   GemmParams p{};
   p.live = live;
   p.a = Operand{G, 0, rows, V, gblk};  // tiled: storage row = token, column = vocabulary id
-  // storage row = vocabulary id (k), column = d (n)
-  p.b = tiled ? Operand{W, 0, d, V, tile_row_stride(d)} : Operand{W, d, d, V, 0};
+  p.b = Operand{W, d, d, V, 0};        // storage row = vocabulary id (k), column = d (n)
   p.tiles_m = cdiv64(rows, tile_edge(h.tile));
   p.tiles_n = cdiv64(d, tile_edge(h.tile));
   p.k_tiles = cdiv64(V, dt == DT_BF16 ? 64 : 32);

@@ -243,18 +243,17 @@ struct HeadGradArgs {
   const float* dlogp;      // [N, T]
   const float* dentropy;   // [N] or null
 };
-// G of a chunk (tiled, tile rows gblk elements apart); W row-major, or its tiled copy; coef: [rows].
-hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, bool tiled, const void* Hc, int64_t r0,
-                            int64_t rows, const int* vidx, const int* live, float4* coef, void* G, int64_t gblk,
-                            hipStream_t s);
+// G of a chunk (tiled, tile rows gblk elements apart); coef: [rows].
+hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, const void* Hc, int64_t r0, int64_t rows,
+                            const int* vidx, const int* live, float4* coef, void* G, int64_t gblk, hipStream_t s);
 // dH's partial slabs as launch_dh leaves them, in the given tile and splits.
 struct HeadSplit {
   HeadTile tile;
   int splits;
 };
 HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V);
-hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, bool tiled, int64_t V,
-                          int64_t d, int64_t rows, float* slab, const int* live, hipStream_t s);
+hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, int64_t V, int64_t d,
+                          int64_t rows, float* slab, const int* live, hipStream_t s);
 // dW: fp32 `sums` (+)= G^T H_c; or, where `rounded` is not null, that bf16 array = G^T
 // H_c, plus the fp32 `old` where given (bf16 operands).
 hipError_t launch_head_dw(Dtype dt, const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,

@@ -11,9 +11,9 @@ from __future__ import annotations
 import ctypes
 from typing import Any, NamedTuple
 
-from .binding import DTYPE_BF16, DTYPE_F32, _check, _check_out, _ptr, lib
-from .residual import _no_capture
-from .vocab import _dtype, _gpu, _on, _stream
+from .binding import DTYPE_BF16, DTYPE_F32, _check, _check_out, lib
+from .residual import _at, _call, _no_capture
+from .vocab import _dtype, _gpu
 
 
 class LogProbs(NamedTuple):
@@ -49,7 +49,8 @@ def _given(torch, ids, mask, N, dev):
     if mask is not None:
         if tuple(mask.shape) != (N,) or mask.device != dev:
             raise ValueError(f"mask must be [N] on {dev}")
-        mask = mask.to(torch.uint8).contiguous()
+        mask = mask.contiguous()
+        mask = mask.view(torch.uint8) if mask.dtype == torch.bool else mask.to(torch.uint8)
     return T, mask
 
 
@@ -99,18 +100,17 @@ def logprobs(logits, ids=None, top=0, mask=None):
         raise ValueError("top must be in 0 .. V")
     T, mask = _given(torch, ids, mask, N, dev)
     need = ctypes.c_uint64(0)
-    _check(lib().ckl_logprobs_workspace(N, V, top, ctypes.byref(need)), "ckl_logprobs_workspace")
-    f32 = torch.float32
-    logp = torch.empty(ids.shape, dtype=f32, device=dev) if ids is not None else None
-    entropy = torch.empty((N,), dtype=f32, device=dev)
-    stats = torch.empty((2, N), dtype=f32, device=dev)
-    top_ids = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
-    top_logp = torch.empty((N, top), dtype=f32, device=dev) if top else None
-    with _on(torch, dev):
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        _check(lib().ckl_logprobs(dt, _ptr(logits), N, V, ld, _ptr(ids), T, _ptr(mask), top, _ptr(logp), _ptr(entropy),
-                                  _ptr(stats), _ptr(top_ids), _ptr(top_logp), _ptr(ws), need.value, _stream(torch, dev)),
-               "ckl_logprobs")
+    _check(lib().ckl_logprobs_workspace(N, V, top, need), "ckl_logprobs_workspace")
+    f32, empty = torch.float32, torch.empty
+    logp = empty(*ids.shape, dtype=f32, device=dev) if ids is not None else None
+    entropy = empty(N, dtype=f32, device=dev)
+    stats = empty(2, N, dtype=f32, device=dev)
+    top_ids = empty(N, top, dtype=torch.int32, device=dev) if top else None
+    top_logp = empty(N, top, dtype=f32, device=dev) if top else None
+    # from torch's allocator, so that calls on several streams, or captured into several graphs, never share it
+    ws = empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    _call(torch, dev, lib().ckl_logprobs, dt, logits.data_ptr(), N, V, ld, _at(ids), T, _at(mask), top, _at(logp),
+          entropy.data_ptr(), stats.data_ptr(), _at(top_ids), _at(top_logp), _at(ws), need.value)
     return LogProbs(logp, entropy, stats, top_ids, top_logp)
 
 
@@ -140,10 +140,8 @@ def logprobs_bwd(logits, ids, entropy, stats, dlogp=None, dentropy=None, mask=No
         ldo = V
     if out is None:
         out = torch.empty((N, V), dtype=logits.dtype, device=dev)
-    with _on(torch, dev):
-        _check(lib().ckl_logprobs_bwd(dt, _ptr(logits), N, V, ld, _ptr(ids), T, _ptr(mask), _ptr(stats), _ptr(entropy),
-                                      _ptr(dlogp), _ptr(dentropy), _ptr(out), ldo, _stream(torch, dev)),
-               "ckl_logprobs_bwd")
+    _call(torch, dev, lib().ckl_logprobs_bwd, dt, logits.data_ptr(), N, V, ld, _at(ids), T, _at(mask), stats.data_ptr(),
+          _at(entropy), _at(dlogp), _at(dentropy), out.data_ptr(), ldo)
     return out
 
 
@@ -238,11 +236,9 @@ def head_logprobs(H, W, ids=None, mask=None, chunk=0):
     logp = torch.empty(ids.shape, dtype=torch.float32, device=dev) if ids is not None else None
     entropy = torch.empty((N,), dtype=torch.float32, device=dev)
     stats = torch.empty((2, N), dtype=torch.float32, device=dev)
-    with _on(torch, dev):
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(lib().ckl_head_logprobs(dt, _ptr(H), _ptr(W), _ptr(ids), _ptr(mask), N, d, V, T, int(chunk), _ptr(logp),
-                                       _ptr(entropy), _ptr(stats), _ptr(ws), need, _stream(torch, dev)),
-               "ckl_head_logprobs")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call(torch, dev, lib().ckl_head_logprobs, dt, H.data_ptr(), W.data_ptr(), _at(ids), _at(mask), N, d, V, T, int(chunk),
+          _at(logp), entropy.data_ptr(), stats.data_ptr(), _at(ws), need)
     return HeadLogProbs(logp, entropy, stats)
 
 
@@ -279,12 +275,10 @@ def head_logprobs_bwd(H, W, ids, logp, entropy, stats, dlogp=None, dentropy=None
     dw_dt = DTYPE_BF16 if dW.dtype == torch.bfloat16 else DTYPE_F32
     need = _plan(1, dt, dw_dt, N, d, V, int(chunk))
     dH = torch.empty_like(H)
-    with _on(torch, dev):
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(lib().ckl_head_logprobs_bwd(dt, _ptr(H), _ptr(W), _ptr(ids), _ptr(mask), N, d, V, T, int(chunk),
-                                           _ptr(logp), _ptr(entropy), _ptr(stats), _ptr(dlogp), _ptr(dentropy), _ptr(dH),
-                                           dw_dt, 1 if accumulate else 0, _ptr(dW), _ptr(ws), need, _stream(torch, dev)),
-               "ckl_head_logprobs_bwd")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call(torch, dev, lib().ckl_head_logprobs_bwd, dt, H.data_ptr(), W.data_ptr(), _at(ids), _at(mask), N, d, V, T,
+          int(chunk), _at(logp), _at(entropy), stats.data_ptr(), _at(dlogp), _at(dentropy), dH.data_ptr(), dw_dt,
+          1 if accumulate else 0, dW.data_ptr(), _at(ws), need)
     return dH, dW
 
 

@@ -9,8 +9,25 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import Drop, Norm, _check, _check_out, _ptr, lib
-from .vocab import _dtype, _gpu, _on, _stream
+from .binding import Drop, Norm, _check, _check_out, lib
+from .vocab import _dtype, _gpu, _stream
+
+
+def _at(t):
+    """Address of a tensor, or None."""
+    return None if t is None else t.data_ptr()
+
+
+def _call(torch, device, fn, *args):
+    """fn(*args, the device's current stream), on that device: the library launches on
+    the current one."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(torch, device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(torch, device))
+    if st:
+        _check(st, fn.__name__)
 
 
 def _drop(torch, p, seed, offset, device):
@@ -21,7 +38,7 @@ def _drop(torch, p, seed, offset, device):
         raise ValueError("p must be in [0, 1]")
     if not 0 <= seed < 1 << 64:
         raise ValueError("seed must be in [0, 2^64)")
-    if torch.is_tensor(offset):
+    if isinstance(offset, torch.Tensor):
         if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
             raise ValueError(f"offset must be an int or an int64 tensor of one element on {device}")
         return Drop(p, seed, 0, offset.data_ptr())
@@ -50,12 +67,11 @@ def drop(x, p, seed, offset=0, out=None):
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     how = _drop(torch, p, seed, offset, dev)
-    _check_out(torch, out, x.shape, x.dtype, dev, "out")
     if out is None:
         out = torch.empty_like(x)
-    with _on(torch, dev):
-        _check(lib().ckl_dropout(dt, _ptr(x), x.numel(), ctypes.byref(how), _ptr(out), _stream(torch, dev)),
-               "ckl_dropout")
+    else:
+        _check_out(torch, out, x.shape, x.dtype, dev, "out")
+    _call(torch, dev, lib().ckl_dropout, dt, x.data_ptr(), x.numel(), how, out.data_ptr())
     return out
 
 
@@ -108,37 +124,29 @@ def dropout(x, p, seed, offset=0):
 
 
 def _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps):
-    """Checks what both directions share: (dtype code, device, N, d, ckl_norm, what it
-    points at)."""
+    """Checks what both directions share: (dtype code, device, N, d, ckl_norm)."""
     dev = _gpu(y, "y")
-    dt = _dtype(torch, y, "y")
-    if y.dim() < 1:
-        raise ValueError("y must be [..., d]")
-    if tuple(r.shape) != tuple(y.shape):
+    dt, kind, shape = _dtype(torch, y, "y"), y.dtype, y.shape
+    if y.dim() < 1 or shape[-1] == 0:
+        raise ValueError("y must be [..., d], d at least 1")
+    if r.shape != shape:
         raise ValueError("r must have the shape of y")
-    d = y.shape[-1]
-    n = y.numel()
-    if d == 0:
-        raise ValueError("d must be at least 1")
+    d = shape[-1]
+    rows = gate is not None and gate.dim() > 1 and gate.shape == shape
     for name, t in (("y", y), ("r", r), ("w_pre", w_pre), ("w_post", w_post), ("gate", gate)):
-        if t is not None and (t.dtype != y.dtype or t.device != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {y.dtype} tensor on {dev}")
-    for name, t in (("w_pre", w_pre), ("w_post", w_post)):
-        if t is not None and tuple(t.shape) != (d,):
-            raise ValueError(f"{name} must be [{d}]")
-    rows = False
-    if gate is not None:
-        rows = gate.dim() > 1 and tuple(gate.shape) == tuple(y.shape)
-        if not rows and tuple(gate.shape) != (d,):
-            raise ValueError(f"gate must be [{d}] or have the shape of y")
+        if t is None:
+            continue
+        if t.dtype != kind or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {kind} tensor on {dev}")
+        if t is not y and t is not r and not (rows and t is gate) and (t.dim() != 1 or t.shape[0] != d):
+            raise ValueError(f"{name} must be [{d}]" + (" or have the shape of y" if t is gate else ""))
     eps = float(eps)
     if not eps >= 0.0:
         raise ValueError("eps must be at least 0")
-    held = _drop(torch, p, seed, offset, dev)
-    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    how = Norm(ptr(w_post), ptr(w_pre), ptr(gate), 1 if rows else 0, float(scale), eps,
-               ctypes.pointer(held) if p else None)
-    return dt, dev, n // d, d, how, held
+    drops = _drop(torch, p, seed, offset, dev)
+    how = Norm(_at(w_post), _at(w_pre), _at(gate), 1 if rows else 0, float(scale), eps,
+               ctypes.pointer(drops) if p else None)
+    return dt, dev, y.numel() // d, d, how
 
 
 def add_norm(y, r, w_pre, w_post=None, gate=None, scale=1.0, p=0.0, seed=0, offset=0, eps=1e-6, stats=False,
@@ -160,20 +168,20 @@ def add_norm(y, r, w_pre, w_post=None, gate=None, scale=1.0, p=0.0, seed=0, offs
     """
     import torch
 
-    dt, dev, N, d, how, held = _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps)
-    _check_out(torch, r_out, y.shape, y.dtype, dev, "r_out")
-    _check_out(torch, x_out, y.shape, y.dtype, dev, "x_out")
+    dt, dev, N, d, how = _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps)
     if r_out is None:
         r_out = torch.empty_like(y)
-    if w_pre is None:
-        if x_out is not None:
+    else:
+        _check_out(torch, r_out, y.shape, y.dtype, dev, "r_out")
+    if x_out is not None:
+        if w_pre is None:
             raise ValueError("x_out needs w_pre")
-    elif x_out is None:
+        _check_out(torch, x_out, y.shape, y.dtype, dev, "x_out")
+    elif w_pre is not None:
         x_out = torch.empty_like(y)
     kept = torch.empty((2, N), dtype=torch.float32, device=dev) if stats else None
-    with _on(torch, dev):
-        _check(lib().ckl_add_norm(dt, _ptr(y), _ptr(r), ctypes.byref(how), N, d, _ptr(r_out), _ptr(x_out), _ptr(kept),
-                                  _stream(torch, dev)), "ckl_add_norm")
+    _call(torch, dev, lib().ckl_add_norm, dt, y.data_ptr(), r.data_ptr(), how, N, d, r_out.data_ptr(), _at(x_out),
+          _at(kept))
     return r_out, x_out, kept
 
 
@@ -188,7 +196,7 @@ def add_norm_bwd(y, r, w_pre, w_post, stats, dx, dr_out, gate=None, scale=1.0, p
     """
     import torch
 
-    dt, dev, N, d, how, held = _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps)
+    dt, dev, N, d, how = _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps)
     _check_out(torch, stats, (2, N), torch.float32, dev, "stats")
     _check_out(torch, dx, y.shape, y.dtype, dev, "dx")
     _check_out(torch, dr_out, y.shape, y.dtype, dev, "dr_out")
@@ -205,12 +213,11 @@ def add_norm_bwd(y, r, w_pre, w_post, stats, dx, dr_out, gate=None, scale=1.0, p
     dgate = None if gate is None else torch.empty_like(gate) if how.gate_rows else vec()
     sums = (w_post is not None) + (w_pre is not None) + (gate is not None and not how.gate_rows)
     need = ctypes.c_uint64(0)
-    _check(lib().ckl_add_norm_bwd_workspace(N, d, sums, ctypes.byref(need)), "ckl_add_norm_bwd_workspace")
-    with _on(torch, dev):
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        _check(lib().ckl_add_norm_bwd(dt, _ptr(y), _ptr(r), ctypes.byref(how), N, d, _ptr(stats), _ptr(dx), _ptr(dr_out),
-                                      _ptr(dy), _ptr(dr), _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(ws),
-                                      need.value, _stream(torch, dev)), "ckl_add_norm_bwd")
+    _check(lib().ckl_add_norm_bwd_workspace(N, d, sums, need), "ckl_add_norm_bwd_workspace")
+    # from torch's allocator, so that calls on several streams, or captured into several graphs, never share it
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    _call(torch, dev, lib().ckl_add_norm_bwd, dt, y.data_ptr(), r.data_ptr(), how, N, d, stats.data_ptr(), _at(dx),
+          _at(dr_out), dy.data_ptr(), dr.data_ptr(), _at(dw_post), _at(dw_pre), _at(dgate), _at(ws), need.value)
     return dy, dr, dw_post, dw_pre, dgate
 
 
