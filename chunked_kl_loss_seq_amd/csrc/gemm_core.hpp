@@ -500,8 +500,12 @@ struct AccOf<16> {
 // At most 256 VGPRs per lane (two waves per SIMD), so that either one 8-wave
 // or two 4-wave workgroups fit a compute unit; with two workgroups their
 // barriers and epilogues overlap each other's MFMA work.  MS is the MFMA
-// block (32, or 16 for bf16 with both operands k-major).
-template <typename T, int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int KB, int NS, int MS = 32>
+// block (32, or 16 for bf16 with both operands k-major).  TWO: a slab's products are
+// summed by themselves and then added to the tile's sums, which shortens the chain
+// of roundings from the whole of k to a slab's and the slabs' number (fp32, whose
+// results keep those bits), for tiles whose sums fit the registers twice.
+template <typename T, int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int KB, int NS, int MS = 32,
+          bool TWO = false>
 __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_eu(2))) gemm_kernel(GemmParams p) {
   constexpr int NW = WM * WN;
   constexpr int BK = KB / (int)sizeof(T);
@@ -555,6 +559,12 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int r = 0; r < NR; ++r) acc[i][j][r] = 0.f;
+  static_assert(!TWO || NMF * NR <= 64, "the sums are held twice");
+  typename AccOf<MS>::type sum[TWO ? FM : 1][TWO ? FN : 1];
+  if constexpr (TWO) {
+#pragma unroll
+    for (int q = 0; q < NMF; ++q) sum[q / FN][q % FN] = acc[q / FN][q % FN];
+  }
 
   typedef typename Frag<T>::type FragT;
   FragT fa[2][FM], fb[2][FN];
@@ -693,7 +703,20 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
             acc[q / FN][q % FN] = mfma_block(fa[fbuf][q / FN], fb[fbuf][q % FN], acc[q / FN][q % FN]);
         }
       }
+      if constexpr (TWO) {
+#pragma unroll
+        for (int q = 0; q < NMF; ++q)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            sum[q / FN][q % FN][r] += acc[q / FN][q % FN][r];
+            acc[q / FN][q % FN][r] = 0.f;
+          }
+      }
     }
+  }
+  if constexpr (TWO) {
+#pragma unroll
+    for (int q = 0; q < NMF; ++q) acc[q / FN][q % FN] = sum[q / FN][q % FN];
   }
   wait_vmcnt<0>();  // no LDS copy outlives the workgroup
 
@@ -1200,11 +1223,12 @@ inline int cdiv64(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // One launch over every tile of p; the grid is rounded up to a multiple of
 // the 8 XCDs so that each XCD gets the same share of the tile order.
-template <typename T, int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int KB, int NS, int MS = 32>
+template <typename T, int BM, int BN, int WM, int WN, bool AK, bool BKM, int EPI, int KB, int NS, int MS = 32,
+          bool TWO = false>
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s) {
   const int total = p.tiles_m * p.tiles_n * p.splits;
   const int grid = ((total + 7) / 8) * 8;
-  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, AK, BKM, EPI, KB, NS, MS>), dim3(grid), dim3(WM * WN * 64), 0,
+  hipLaunchKernelGGL((gemm_kernel<T, BM, BN, WM, WN, AK, BKM, EPI, KB, NS, MS, TWO>), dim3(grid), dim3(WM * WN * 64), 0,
                      s, p);
   return hipGetLastError();
 }

@@ -188,29 +188,33 @@ int64_t tiles_of(int64_t m, int64_t n, HeadTile t) {
 }
 // The tile with the least time by this count: tiles a compute unit takes in turn x
 // a tile's work, over the rate that it reaches with all units busy (bf16: 1,305
-// TFLOP/s at 256 x 256, 1,021 at 128, 706 at 64; fp32: 130, 126 and 121).
+// TFLOP/s at 256 x 256, 1,021 at 128, 706 at 64; fp32: 126 at 128 and 121 at 64).
+// fp32 takes no 256 x 256 tile (130 TFLOP/s): its sums would not fit twice.
 HeadTile tile_for(Dtype dt, int64_t m, int64_t n, int64_t splits) {
-  static const double work[2][3] = {{1.0, 0.25 / 0.78, 0.0625 / 0.54}, {1.0, 0.25 / 0.97, 0.0625 / 0.93}};
-  HeadTile best = TILE_256;
+  static const double work[2][3] = {{1.0, 0.25 / 0.78, 0.0625 / 0.54}, {0.0, 0.25 / 0.97, 0.0625 / 0.93}};
+  const int first = dt == DT_BF16 ? TILE_256 : TILE_128;
+  int best = first;
   double least = 0;
-  for (int t = TILE_256; t <= TILE_64; ++t) {
+  for (int t = first; t <= TILE_64; ++t) {
     const int64_t turns = (tiles_of(m, n, (HeadTile)t) * splits + 255) / 256;
     const double cost = (double)turns * work[dt == DT_BF16 ? 0 : 1][t];
-    if (t == TILE_256 || cost < least) {
+    if (t == first || cost < least) {
       least = cost;
-      best = (HeadTile)t;
+      best = t;
     }
   }
-  return best;
+  return (HeadTile)best;
 }
 
-template <typename T, bool AK, bool BKM, int EPI, int MS, bool WITH_256 = true>
+// WITH_256: whether a 256 x 256 tile may be asked for here.
+template <typename T, bool AK, bool BKM, int EPI, int MS, bool WITH_256 = sizeof(T) == 2>
 hipError_t launch_tile(HeadTile t, const GemmParams& p, hipStream_t s) {
+  constexpr bool TWO = sizeof(T) == 4;
   if constexpr (WITH_256) {
     if (t == TILE_256) return launch_gemm<T, 256, 256, 2, 4, AK, BKM, EPI, 128, 2, MS>(p, s);
   }
-  if (t == TILE_128) return launch_gemm<T, 128, 128, 2, 2, AK, BKM, EPI, 128, 2, MS>(p, s);
-  return launch_gemm<T, 64, 64, 2, 2, AK, BKM, EPI, 128, 3, MS>(p, s);
+  if (t == TILE_128) return launch_gemm<T, 128, 128, 2, 2, AK, BKM, EPI, 128, 2, MS, TWO>(p, s);
+  return launch_gemm<T, 64, 64, 2, 2, AK, BKM, EPI, 128, 3, MS, TWO>(p, s);
 }
 
 // W is read as it lies: a copy in 64 x 64 tiles, as the loss makes for its three
@@ -292,8 +296,10 @@ hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, cons
 // loss's (dh_splits); else 64 x 64 tiles in as many splits as give every compute
 // unit two, of at least 8 k-steps each.
 HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V) {
-  const int s256 = dh_splits(dt, rows, d, V);
-  if (tile_for(dt, rows, d, s256) == TILE_256) return HeadSplit{TILE_256, s256};
+  if (dt == DT_BF16) {
+    const int s256 = dh_splits(dt, rows, d, V);
+    if (tile_for(dt, rows, d, s256) == TILE_256) return HeadSplit{TILE_256, s256};
+  }
   const int64_t tiles = tiles_of(rows, d, TILE_64), steps = (V + (dt == DT_BF16 ? 63 : 31)) / (dt == DT_BF16 ? 64 : 32);
   int64_t n = (512 + tiles - 1) / tiles;
   if (n > steps / 8) n = steps / 8;
