@@ -85,6 +85,17 @@ enum EpilogueKind : int {
   EPI_ROUND = 5,   // out[m][n] = D[m][n], plus old[m][n] where given, rounded to bf16
 };
 
+// A row's coefficients of the gradient's epilogue where one token is given a row:
+// from the call's arrays, at g_rowmap's row where that is not null.
+struct GradRow {
+  const int32_t* ids;      // null: the coefficients are in `coef`
+  const float* dlogp;
+  const float* dentropy;   // or null
+  const float* entropy;
+  const float* stats;      // [2, n]
+  int64_t n;
+};
+
 struct GemmParams {
   Operand a, b;
   int tiles_m, tiles_n;  // output tiles
@@ -127,9 +138,11 @@ struct GemmParams {
   const float* g_gscale;
   // EPI_STATS: the third sum, per [n][slice] beside part
   float* part_a;
-  // EPI_GRAD: (max, log sum, c, u) of row n; rows at and past valid_n (and
-  // *live) and ids at and past valid_m get zeros
+  // EPI_GRAD: (max, log sum, c, u) of row n, or with one given token a row its
+  // own arrays (GradRow); rows at and past valid_n (and *live) and ids at and past
+  // valid_m get zeros
   const float4* coef;
+  GradRow one;
   // EPI_ROUND: fp32 values to add, laid out as out, or null
   const float* old;
 };
@@ -780,7 +793,20 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
       for (int j = 0; j < FN; ++j) {
         const int64_t n = nw + MS * j + cl;
         const bool rok = n < p.valid_n && n < live;
-        const float4 c = rok ? p.coef[n] : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+        int32_t given = -1;
+        float w = 0.f;
+        if (p.one.ids == nullptr) {
+          if (rok) c = p.coef[n];
+        } else if (rok) {
+          const int64_t at = p.g_rowmap != nullptr ? p.g_rowmap[n] : n;
+          given = p.one.ids[at];
+          if (given < 0 || given >= p.valid_m) given = -1;
+          if (given >= 0) w = p.one.dlogp[at];
+          const float u = p.one.dentropy != nullptr ? p.one.dentropy[at] : 0.f;
+          c = make_float4(p.one.stats[at], p.one.stats[p.one.n + at],
+                          __builtin_fmaf(u, u != 0.f ? p.one.entropy[at] : 0.f, w), u);
+        }
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -789,6 +815,15 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
             const float g = -__builtin_amdgcn_exp2f(l * kLog2e) * __builtin_fmaf(c.w, l, c.z);
             acc[i][j][r] = rok && (mfull || (int)mw + run0(i, r / 4) + r % 4 < vm) ? g : 0.f;
           }
+        // the given token's own element, in the one wave that holds it
+        const int own = given - (int)mw;
+        if (given >= 0 && own >= 0 && own < WTM) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+              if (run0(i, r / 4) + r % 4 == own) acc[i][j][r] += w;
+        }
       }
       if constexpr (sizeof(T) == 2 && WTM == 128) {
         // through the wave's 16 KiB of LDS, as 16 coalesced 1 KiB stores (see the logits epilogue below)

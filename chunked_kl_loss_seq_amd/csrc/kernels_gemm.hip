@@ -142,7 +142,15 @@ __global__ void __launch_bounds__(256) dh_reduce_kernel(const float* __restrict_
   }
   if (live) {
     acc = *(const f32x4*)(slab + src);
-    for (int s = 1; s < splits; ++s) acc += *(const f32x4*)(slab + (int64_t)s * count + src);
+    int s = 1;
+    for (; s + 3 < splits; s += 4) {  // four loads under way, added in the splits' order
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *(const f32x4*)(slab + (int64_t)(s + i) * count + src);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc += v[i];
+    }
+    for (; s < splits; ++s) acc += *(const f32x4*)(slab + (int64_t)s * count + src);
   }
   if constexpr (sizeof(TO) == 4) {
     *(f32x4*)((float*)out + i4) = acc;

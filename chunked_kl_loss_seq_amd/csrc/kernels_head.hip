@@ -274,17 +274,30 @@ hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t row
 hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, const void* Hc, int64_t r0, int64_t rows,
                             const int* vidx, const int* live, float4* coef, void* G, int64_t gblk, hipStream_t s) {
   const dim3 grid((unsigned)((rows + 3) / 4));
-  hipLaunchKernelGGL(head_coef_kernel, grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const HeadTile t = head_logits_tile(dt, rows, a.V);
   GemmParams p = logits_product(dt, W, Hc, a.V, a.d, rows, t, live);
-  p.coef = coef;
   p.out = G;
   p.ldo = gblk;
+  hipError_t e;
+  if (a.T == 1) {  // the epilogue reads the rows' arrays and adds the given token's share itself
+    p.one = GradRow{a.ids, a.dlogp, a.dentropy, a.entropy, a.stats, a.N};
+    p.g_rowmap = vidx;
+    p.one.ids += r0;
+    p.one.dlogp += r0;
+    if (a.dentropy != nullptr) {
+      p.one.dentropy += r0;
+      p.one.entropy += r0;
+    }
+    p.one.stats += r0;
+  } else {
+    hipLaunchKernelGGL(head_coef_kernel, grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.coef = coef;
+  }
   e = dt == DT_BF16 ? launch_tile<__bf16, true, true, EPI_GRAD, 16>(t, p, s)
                     : launch_tile<float, true, true, EPI_GRAD, 32>(t, p, s);
-  if (e != hipSuccess || a.T == 0) return e;
+  if (e != hipSuccess || a.T <= 1) return e;
   if (dt == DT_BF16)
     hipLaunchKernelGGL((head_given_kernel<__bf16>), grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef, (__bf16*)G, gblk);
   else
