@@ -581,9 +581,9 @@ int head_plan(bool backward, int dtype, int dw_dtype, int64_t N, int64_t d, int6
   budget = budget_from_env(budget);
   const size_t esz = dtype == CKL_DTYPE_BF16 ? 2 : 4;
   const bool sum = backward && dw_dtype == CKL_DTYPE_BF16;
-  // rows per chunk at most: 2^22 tiles of 256 x 256, so that a launch stays below 2^32 threads
-  const int64_t most_tiles = ((int64_t)1 << 22) / ((V + 255) / 256);
-  const int64_t most = most_tiles >= kMaxChunk / 256 ? kMaxChunk : most_tiles * 256;
+  // rows per chunk at most: below 2^24 tiles of 64 x 64, the smallest, of 256 threads each
+  const int64_t most_tiles = (((int64_t)1 << 24) - 1) / ((V + 63) / 64);
+  const int64_t most = most_tiles >= kMaxChunk / 64 ? kMaxChunk : most_tiles / 4 * 256;
   if (chunk > 0) {
     const int64_t C = chunk < N ? chunk : N;
     if (C > most) return CKL_EUNSUPPORTED;
@@ -1064,7 +1064,7 @@ int ckl_head_logprobs_bwd(int dtype, const void* H, const void* W, const int32_t
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
       const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
       Chunk k;
-      // (the compaction writes a zero per masked row somewhere: the rows' coefficients, written after it)
+      // the compaction writes a zero per masked row somewhere: the coefficients' place, which holds nothing yet
       CKL_TRY(head_chunk(c, L, H, d, r0, rows, (float*)coef, &k, stream));
       CKL_TRY(launch_head_grad(c.dt, p, W, k.Hc, r0, rows, k.vidx, k.live, coef, G, L.pblk, stream));
       HeadSplit h = head_dh_split(c.dt, rows, d, V);

@@ -15,11 +15,11 @@
 // passes through to the row's results.
 //
 // Alternatives: the K-th largest of the maxima of 64 groups of threads (or of
-// the threads themselves) is a bound that at least K logits reach.  Threads
-// whose maximum reaches it read their logits again and collect those that do;
-// each one's place is the number of larger (logit, lower id) pairs.  Where more
-// than 1,024 reach the bound (equal logits), a binary search over the pairs
-// narrows it first.
+// the threads themselves), cut to 16 bits, is a bound that at least K logits
+// reach.  Threads whose maximum reaches it read their logits again and collect
+// those that do; up to 128 are placed by the number of larger (logit, lower id)
+// pairs, more are sorted.  Where more than 1,024 reach the bound (equal logits), a
+// binary search over the pairs narrows it first.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -37,6 +37,7 @@ constexpr float kFar = -1000.f;  // exp(kFar) is 0 in fp32
 constexpr int kList = 1024;      // pairs held in LDS
 constexpr int kGroups = 64;
 constexpr int kGroupTop = 48;    // up to this many alternatives the bound comes from the groups' maxima
+constexpr int kWideTop = 128;    // beyond, rows are taken by 1,024 threads, whose maxima give a bound up to 512
 
 __device__ inline float exp_fast(float t) { return __builtin_amdgcn_exp2f(t * kLog2); }
 // the larger of t and kFar; NaN stays NaN
@@ -133,11 +134,97 @@ struct RowResult {
 // ------------------------------------------------------------------ alternatives
 template <int NT>
 struct TopLds {
-  u64 list[kList];
+  u64 list[kList], other[kList];
   uint32_t keys[NT > kGroups ? NT : kGroups];
   int n, count[2];
   uint32_t bound;
 };
+
+// By one wave: the largest 16-bit prefix that at least K of n <= 1,024 keys reach, as
+// a key (0 if fewer than K keys are above 0).
+template <typename F>
+__device__ inline uint32_t prefix_bound(F key, int n, int K) {
+  const int lane = threadIdx.x & 63;
+  uint32_t v[kList / 64];
+#pragma unroll
+  for (int i = 0; i < kList / 64; ++i) v[i] = lane + 64 * i < n ? key(lane + 64 * i) >> 16 : 0u;
+  uint32_t best = 0;
+  for (int b = 15; b >= 0; --b) {
+    const uint32_t next = best | (1u << b);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kList / 64; ++i)
+      if (64 * i < n) c += __builtin_popcountll(__ballot(v[i] >= next));
+    if (c >= K) best = next;
+  }
+  return best << 16;
+}
+
+// The number of larger pairs in the list (kList long; entries past n may hold anything).
+__device__ inline int rank_in(const u64* list, int n, u64 pair) {
+  int rank = 0;
+  for (int j = 0; j < n; j += 8) {
+    u64 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = list[j + i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rank += j + i < n && o[i] > pair;
+  }
+  return rank;
+}
+
+// The K largest of n <= kList pairs in `list` (all of them if there are fewer), in
+// order; `other` is scratch.  Returns where they are.  The workgroup comes here
+// together, and goes on with the result in sight of all.
+template <int NT>
+__device__ inline const u64* order_top(u64* list, u64* other, int& n, int K, int* count, uint32_t* bound) {
+  const int t = threadIdx.x;
+  if (n > 128 && n > 2 * K) {  // fewer first: those that reach the K-th largest's prefix
+    if (t < 64) {
+      const uint32_t b = prefix_bound([&](int i) { return (uint32_t)(list[i] >> 32); }, n, K);
+      if (t == 0) {
+        *bound = b;
+        *count = 0;
+      }
+    }
+    __syncthreads();
+    const uint32_t b = *bound;
+    for (int i = t; i < n; i += NT) {
+      const u64 pair = list[i];
+      if ((uint32_t)(pair >> 32) >= b) other[atomicAdd(count, 1)] = pair;
+    }
+    __syncthreads();
+    n = *count;
+    u64* const swap = list;
+    list = other;
+    other = swap;
+  }
+  if (n <= 128) {  // each pair's place is the number of larger ones
+    for (int i = t; i < n; i += NT) {
+      const u64 pair = list[i];
+      other[rank_in(list, n, pair)] = pair;
+    }
+    __syncthreads();
+    return other;
+  }
+  int m = 256;
+  while (m < n) m <<= 1;
+  for (int i = n + t; i < m; i += NT) list[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= m; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = t; i < m / 2; i += NT) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const u64 x = list[lo], y = list[hi];
+        if ((lo & k) == 0 ? x < y : x > y) {
+          list[lo] = y;
+          list[hi] = x;
+        }
+      }
+      __syncthreads();
+    }
+  return list;
+}
 
 // Number of (key, id) pairs at or above `from` among the elements [lo, hi) of a row.
 template <typename T, int NT>
@@ -191,39 +278,43 @@ __device__ inline int collect_top(const T* row, int64_t lo, int64_t hi, float mx
   } else if (K <= NT / 2) {
     sh.keys[t] = mine;
     __syncthreads();
-    int rank = 0;
-    for (int j = 0; j < NT; ++j) {
-      const uint32_t o = sh.keys[j];
-      rank += o > mine || (o == mine && j < t);
+    if (t < 64) {
+      const uint32_t b = prefix_bound([&](int i) { return sh.keys[i]; }, NT, K);
+      if (t == 0) sh.bound = b;
     }
-    if (rank == K - 1) sh.bound = mine;
     __syncthreads();
   } else {
     __syncthreads();
   }
   const uint32_t bound = sh.bound > 1u ? sh.bound : 1u;
   if (mine >= bound) {
+    const float least = bound > 1u ? key_value(bound) : kLowest;  // NaN and -inf do not reach it
+    const auto take = [&](float z, int64_t id) {
+      if (z >= least) {
+        const int at = atomicAdd(&sh.n, 1);
+        if (at < kList) sh.list[at] = pair_of(key_of(z), id);
+      }
+    };
     const int64_t n8 = (hi - lo) / 8;
-    for (int64_t i = t; i < n8; i += NT) {
-      Eight<T> v;
-      v.load(row + lo + 8 * i);
+    constexpr int U = sizeof(T) == 2 ? 6 : 3;  // vectors under way
+    for (int64_t i = t; i < n8; i += U * NT) {
+      Eight<T> v[U];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t k = key_of(v.get(e));
-        if (k >= bound) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < kList) sh.list[at] = pair_of(k, lo + 8 * i + e);
+      for (int u = 0; u < U; ++u) v[u].load(row + lo + 8 * (i + u * NT < n8 ? i + u * NT : i));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i + u * NT >= n8) continue;
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = v[u].get(e);
+        if (fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))) >= least) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) take(z[e], lo + 8 * (i + u * NT) + e);
         }
       }
     }
     if (t == n8 % NT)
-      for (int64_t i = lo + 8 * n8; i < hi; ++i) {
-        const uint32_t k = key_of((float)row[i]);
-        if (k >= bound) {
-          const int at = atomicAdd(&sh.n, 1);
-          if (at < kList) sh.list[at] = pair_of(k, i);
-        }
-      }
+      for (int64_t i = lo + 8 * n8; i < hi; ++i) take((float)row[i], i);
   }
   __syncthreads();
   int n = sh.n;
@@ -316,33 +407,19 @@ __device__ inline void write_row(const LogprobArgs& p, int64_t row, const RowRes
   }
 }
 
-// Writes alternative `rank` of a row, or -1 where the row has no more.
-__device__ inline void write_top(const LogprobArgs& p, int64_t row, int rank, u64 pair, const RowResult& r) {
-  p.top_ids[row * p.top + rank] = pair_id(pair);
-  p.top_logp[row * p.top + rank] = r.logp(key_value((uint32_t)(pair >> 32)));
-}
-__device__ inline void write_top_rest(const LogprobArgs& p, int64_t row, int n, int t, int nt) {
-  for (int i = n + t; i < p.top; i += nt) {
-    p.top_ids[row * p.top + i] = -1;
-    p.top_logp[row * p.top + i] = -INFINITY;
+// A row's alternatives from its n largest pairs in order; -1 where there are no more.
+__device__ inline void write_top(const LogprobArgs& p, int64_t row, const u64* sorted, int n, const RowResult& r, int t,
+                                 int nt) {
+  for (int i = t; i < p.top; i += nt) {
+    const u64 pair = i < n ? sorted[i] : 0;
+    p.top_ids[row * p.top + i] = i < n ? pair_id(pair) : -1;
+    p.top_logp[row * p.top + i] = i < n ? r.logp(key_value((uint32_t)(pair >> 32))) : -INFINITY;
   }
 }
 
-// The number of larger pairs in the list (kList long; entries past n may hold anything).
-__device__ inline int rank_in(const u64* list, int n, u64 pair) {
-  int rank = 0;
-  for (int j = 0; j < n; j += 8) {
-    u64 o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = list[j + i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rank += j + i < n && o[i] > pair;
-  }
-  return rank;
-}
-
+// (two workgroups of 1,024 threads a compute unit: 64 registers a lane)
 template <typename T, int NT, bool TOP>
-__global__ void __launch_bounds__(NT) logprob_kernel(LogprobArgs p) {
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) logprob_kernel(LogprobArgs p) {
   __shared__ float red[48];
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x;
@@ -359,19 +436,15 @@ __global__ void __launch_bounds__(NT) logprob_kernel(LogprobArgs p) {
   write_row<T>(p, row, r, t, NT);
   if constexpr (TOP) {
     __shared__ TopLds<NT> sh;
-    const int n = collect_top<T, NT>(x, 0, p.V, mine, v.mx, p.top, sh);
-    for (int i = t; i < n; i += NT) {
-      const u64 pair = sh.list[i];
-      const int rank = rank_in(sh.list, n, pair);
-      if (rank < p.top) write_top(p, row, rank, pair, r);
-    }
-    write_top_rest(p, row, n < p.top ? n : p.top, t, NT);
+    int n = collect_top<T, NT>(x, 0, p.V, mine, v.mx, p.top, sh);
+    const u64* sorted = order_top<NT>(sh.list, sh.other, n, p.top, &sh.count[0], &sh.bound);
+    write_top(p, row, sorted, n, r, t, NT);
   }
 }
 
 // A slice of a row (few rows): its sums, and its `top` largest pairs in order.
 template <typename T, int NT, bool TOP>
-__global__ void __launch_bounds__(NT) logprob_slice_kernel(LogprobArgs p) {
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) logprob_slice_kernel(LogprobArgs p) {
   __shared__ float red[48];
   const int64_t row = blockIdx.x / (unsigned)p.slices;
   const int sl = (int)(blockIdx.x % (unsigned)p.slices), t = threadIdx.x;
@@ -386,23 +459,20 @@ __global__ void __launch_bounds__(NT) logprob_slice_kernel(LogprobArgs p) {
   if constexpr (TOP) {
     __shared__ TopLds<NT> sh;
     u64* out = (u64*)p.pairs + (int64_t)blockIdx.x * p.top;
-    const int n = collect_top<T, NT>(x, lo, hi, mine, v.mx, p.top, sh);
-    for (int i = t; i < n; i += NT) {
-      const u64 pair = sh.list[i];
-      const int rank = rank_in(sh.list, n, pair);
-      if (rank < p.top) out[rank] = pair;
-    }
-    for (int i = n + t; i < p.top; i += NT) out[i] = 0;
+    int n = collect_top<T, NT>(x, lo, hi, mine, v.mx, p.top, sh);
+    const u64* sorted = order_top<NT>(sh.list, sh.other, n, p.top, &sh.count[0], &sh.bound);
+    for (int i = t; i < p.top; i += NT) out[i] = i < n ? sorted[i] : 0;
   }
 }
 
 // Joins a row's slices (2 to 64, and at most kList pairs).
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT) logprob_join_kernel(LogprobArgs p) {
-  __shared__ u64 list[kList];
+  __shared__ u64 list[kList], other[kList];
   __shared__ u64 least;
   __shared__ float got[3];
-  __shared__ int n;
+  __shared__ int found, count;
+  __shared__ uint32_t reach;
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x;
   if (masked(p, row)) {
@@ -442,7 +512,7 @@ __global__ void __launch_bounds__(NT) logprob_join_kernel(LogprobArgs p) {
       got[0] = v.mx;
       got[1] = v.s;
       got[2] = v.a;
-      n = 0;
+      found = 0;
     }
   }
   __syncthreads();
@@ -456,15 +526,12 @@ __global__ void __launch_bounds__(NT) logprob_join_kernel(LogprobArgs p) {
   const u64 bound = least;
   for (int i = t; i < p.slices * p.top; i += NT) {
     const u64 pair = pairs[i];
-    if (pair >= bound) list[atomicAdd(&n, 1)] = pair;
+    if (pair >= bound) list[atomicAdd(&found, 1)] = pair;
   }
   __syncthreads();
-  for (int i = t; i < n; i += NT) {
-    const u64 pair = list[i];
-    const int rank = rank_in(list, n, pair);
-    if (rank < p.top) write_top(p, row, rank, pair, r);
-  }
-  write_top_rest(p, row, n < p.top ? n : p.top, t, NT);
+  int n = found;
+  const u64* sorted = order_top<NT>(list, other, n, p.top, &count, &reach);
+  write_top(p, row, sorted, n, r, t, NT);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -587,7 +654,9 @@ template <typename T>
 hipError_t logprob_of(const LogprobArgs& p, hipStream_t s) {
   if (p.slices > 1) {
     const dim3 grid((unsigned)(p.N * p.slices));
-    if (p.top)
+    if (p.top > kWideTop)
+      hipLaunchKernelGGL((logprob_slice_kernel<T, 1024, true>), grid, dim3(1024), 0, s, p);
+    else if (p.top)
       hipLaunchKernelGGL((logprob_slice_kernel<T, 256, true>), grid, dim3(256), 0, s, p);
     else
       hipLaunchKernelGGL((logprob_slice_kernel<T, 256, false>), grid, dim3(256), 0, s, p);
@@ -598,7 +667,7 @@ hipError_t logprob_of(const LogprobArgs& p, hipStream_t s) {
   }
   if (p.V <= 1024)
     logprob_rows<T, 64>(p, s);
-  else if (p.V <= 8192)
+  else if (p.V <= 8192 && p.top <= kWideTop)
     logprob_rows<T, 256>(p, s);
   else
     logprob_rows<T, 1024>(p, s);
