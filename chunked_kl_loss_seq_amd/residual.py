@@ -30,20 +30,21 @@ def _call(torch, device, fn, *args):
         _check(st, fn.__name__)
 
 
+_WORD = (1 << 64) - 1
+
+
 def _drop(torch, p, seed, offset, device):
     """ckl_drop of a probability, a seed in [0, 2^64) and an offset: an int in
     [0, 2^64) or an int64 GPU tensor of one element, read when the kernels run."""
-    p, seed = float(p), int(seed)
     if not 0.0 <= p <= 1.0:
         raise ValueError("p must be in [0, 1]")
-    if not 0 <= seed < 1 << 64:
+    if not 0 <= seed <= _WORD:
         raise ValueError("seed must be in [0, 2^64)")
     if isinstance(offset, torch.Tensor):
         if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
             raise ValueError(f"offset must be an int or an int64 tensor of one element on {device}")
         return Drop(p, seed, 0, offset.data_ptr())
-    offset = int(offset)
-    if not 0 <= offset < 1 << 64:
+    if not 0 <= offset <= _WORD:
         raise ValueError("offset must be in [0, 2^64)")
     return Drop(p, seed, offset, None)
 
@@ -132,20 +133,23 @@ def _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps):
     if r.shape != shape:
         raise ValueError("r must have the shape of y")
     d = shape[-1]
-    rows = gate is not None and gate.dim() > 1 and gate.shape == shape
     for name, t in (("y", y), ("r", r), ("w_pre", w_pre), ("w_post", w_post), ("gate", gate)):
-        if t is None:
-            continue
-        if t.dtype != kind or t.device != dev or not t.is_contiguous():
+        if t is not None and (t.dtype != kind or t.device != dev or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {kind} tensor on {dev}")
-        if t is not y and t is not r and not (rows and t is gate) and (t.dim() != 1 or t.shape[0] != d):
-            raise ValueError(f"{name} must be [{d}]" + (" or have the shape of y" if t is gate else ""))
+    if w_pre is not None and (w_pre.dim() != 1 or w_pre.shape[0] != d):
+        raise ValueError(f"w_pre must be [{d}]")
+    if w_post is not None and (w_post.dim() != 1 or w_post.shape[0] != d):
+        raise ValueError(f"w_post must be [{d}]")
+    rows = False
+    if gate is not None and (gate.dim() != 1 or gate.shape[0] != d):
+        if gate.shape != shape:
+            raise ValueError(f"gate must be [{d}] or have the shape of y")
+        rows = True
     eps = float(eps)
     if not eps >= 0.0:
         raise ValueError("eps must be at least 0")
     drops = _drop(torch, p, seed, offset, dev)
-    how = Norm(_at(w_post), _at(w_pre), _at(gate), 1 if rows else 0, float(scale), eps,
-               ctypes.pointer(drops) if p else None)
+    how = Norm(_at(w_post), _at(w_pre), _at(gate), 1 if rows else 0, scale, eps, ctypes.pointer(drops) if p else None)
     return dt, dev, y.numel() // d, d, how
 
 

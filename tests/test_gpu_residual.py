@@ -208,6 +208,22 @@ def test_in_place_and_same_bits(ckl):
     assert torch.equal(full[1][17:18], part[1])
 
 
+def test_an_input_given_twice(ckl):
+    """The block's output as its own gate, and one weight in both places."""
+    y, r, w = (torch.randn(*s, device="cuda:0") for s in ((7, 40), (7, 40), (40,)))
+    for g in (y, r):
+        a = ckl.add_norm(y, r, w, w, gate=g, stats=True)
+        b = ckl.add_norm(y, r, w, w.clone(), gate=g.clone(), stats=True)
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+        ga = ckl.add_norm_bwd(y, r, w, w, a[2], y, r, gate=g)
+        gb = ckl.add_norm_bwd(y, r, w, w.clone(), a[2], y.clone(), r.clone(), gate=g.clone())
+        assert all(torch.equal(u, v) for u, v in zip(ga, gb)) and ga[4].shape == y.shape
+    leaf = y.clone().requires_grad_()
+    ro, x = ckl.residual_norm(leaf, r, w, gate=leaf, scale=0.5)
+    ro.sum().backward()  # ro = r + y^2 / 2
+    assert bool((leaf.grad - y).abs().max() <= 4 * 2.0 ** -24 * y.abs().max())  # two halves of y, each rounded once
+
+
 def test_no_rows(ckl):
     e, w = torch.empty(0, 64, device="cuda:0"), torch.ones(64, device="cuda:0")
     ro, x, stats = ckl.add_norm(e, e, w, w, gate=w, stats=True)
