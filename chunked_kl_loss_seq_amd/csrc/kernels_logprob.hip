@@ -676,11 +676,11 @@ hipError_t logprob_of(const LogprobArgs& p, hipStream_t s) {
 
 }  // namespace
 
-// Slices of a row: enough for two workgroups a compute unit, at least 2,048
+// Slices of a row: enough for four workgroups a compute unit, at least 2,048
 // logits each, at most 64, and no more pairs than the join holds.
 int logprob_slices(int64_t N, int64_t V, int top) {
   if (N <= 0 || N >= 256 || V < 8192) return 1;
-  int64_t s = 512 / N;
+  int64_t s = 1024 / N;
   if (s > 64) s = 64;
   if (s > V / 2048) s = V / 2048;
   if (top > 0 && s > kList / top) s = kList / top;

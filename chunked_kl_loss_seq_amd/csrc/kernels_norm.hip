@@ -172,10 +172,9 @@ constexpr int fwd_waves() {
   if (MT > 512) return 4;
   return sizeof(T) == 2 ? (NV == 1 ? (ROWS ? 6 : 7) : 4) : (NV == 1 ? (ROWS ? 5 : 6) : (ROWS ? 3 : 4));
 }
-template <typename T, int NV, int MT, bool ROWS>
+template <typename T, int MT>
 constexpr int bwd_waves() {
-  if (MT > 512) return 4;
-  return sizeof(T) == 2 ? (NV == 1 ? 4 : 2) : (NV == 1 ? 3 : 2);
+  return MT > 512 || sizeof(T) == 2 ? 4 : 3;
 }
 
 template <typename T, int NV, int MT, bool ROWS, bool DROP>
@@ -277,7 +276,7 @@ add_norm_kernel(NormArgs p, Team team) {
 // gate) where `a`, from which dw_post and the gradient of a gate [d] follow by the
 // columns' factors, and sum dx n2 with w_pre.
 template <typename T, int NV, int MT, bool ROWS, bool DROP>
-__global__ void __launch_bounds__(MT) __attribute__((amdgpu_waves_per_eu(bwd_waves<T, NV, MT, ROWS>())))
+__global__ void __launch_bounds__(MT) __attribute__((amdgpu_waves_per_eu(bwd_waves<T, MT>())))
 add_norm_bwd_kernel(NormArgs p, NormGrads q, Team team) {
   __shared__ float red[2 * 3 * 16];
   extern __shared__ float columns[];
@@ -319,12 +318,15 @@ add_norm_bwd_kernel(NormArgs p, NormGrads q, Team team) {
     if (post) inv1 = p.stats_in[rc];
     if (pre) inv2 = p.stats_in[p.N + rc];
   };
+  // rows so wide that 1,024 threads hold two vectors each have no registers for the next one's values
+  constexpr bool AHEAD = MT <= 512 || NV == 1;
   const int64_t step = (int64_t)gridDim.x * team.rows;
-  fetch((int64_t)blockIdx.x * team.rows);
+  if (AHEAD) fetch((int64_t)blockIdx.x * team.rows);
   column_weights<T, ROWS>(p, f, w2);
   for (int64_t row0 = (int64_t)blockIdx.x * team.rows; row0 < p.N; row0 += step) {
     const bool live = row0 + at.sub < p.N;
     const uint64_t group0 = (uint64_t)row0 * (uint64_t)d8 + (uint64_t)(uint32_t)(at.sub * d8);
+    if (!AHEAD) fetch(row0);
     // the row's values move aside, so that the next row's are under way for all of this one's turn
     const float i1 = inv1, i2 = inv2;
     Eight<T> cy[NV], cr[NV], cx[NV], co[NV], cg[ROWS ? NV : 1];
@@ -336,7 +338,7 @@ add_norm_bwd_kernel(NormArgs p, NormGrads q, Team team) {
       co[i] = dro[i];
       if constexpr (ROWS) cg[i] = g[i];
     }
-    if (row0 + step < p.N) fetch(row0 + step);
+    if (AHEAD && row0 + step < p.N) fetch(row0 + step);
     float n1[NV][8], n2[NV][8], D[NV][8], gr[ROWS ? NV : 1][8];
     uint32_t kept[NV];
     float s[3] = {0.f, 0.f, 0.f};
@@ -500,8 +502,9 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(NormArgs p, NormGrads 
   if (vec) ((float*)q.dgate)[c] = p.w_post != nullptr ? s * (float)((const T*)p.w_post)[c] : s;
 }
 
-// A row's lanes, and how many vectors of 8 each holds: up to `most` (two where a
-// workgroup would pass 512 threads, which leaves a lane 128 registers).
+// A row's lanes, and how many vectors of 8 each holds: up to `most`, or two where 16
+// waves would not do.  Forward two (32,768 x 2,880 bf16 146 us, with one 190), backward
+// one (272 us, with two 330): fewer registers, more rows under way.
 constexpr int kFwdVec = 2, kBwdVec = 1;
 struct Shape {
   Team team;
@@ -519,7 +522,7 @@ Shape shape_of(int64_t d, int most) {
     }
     return r;
   }
-  if (d8 > 8 * 64 * most) most = 2;
+  if (d8 > 16 * 64 * most) most = 2;
   r.team.span = (int)((d8 + 64 * most - 1) / (64 * most));
   r.team.rows = 1;
   r.nv = (int)((d8 + 64 * r.team.span - 1) / (64 * r.team.span));
@@ -542,11 +545,9 @@ int fwd_blocks(int64_t N, const Shape& h) {
                                         : fwd_waves<T, 2, 512, ROWS>());
 }
 // The backward pass's, each with its sums.
-template <typename T, bool ROWS>
+template <typename T>
 int bwd_blocks(int64_t N, const Shape& h) {
-  return blocks_of(N, h, h.threads > 512 ? bwd_waves<T, 2, 1024, ROWS>()
-                         : h.nv == 1    ? bwd_waves<T, 1, 512, ROWS>()
-                                        : bwd_waves<T, 2, 512, ROWS>());
+  return blocks_of(N, h, h.threads > 512 ? bwd_waves<T, 1024>() : bwd_waves<T, 512>());
 }
 
 template <typename T, int NV, int MT>
@@ -597,14 +598,14 @@ hipError_t add_norm_bwd_of(const NormArgs& p, NormGrads q, hipStream_t s) {
   q.a = p.w_post != nullptr || (p.gate != nullptr && !p.gate_rows);
   q.sums = (q.a ? 1 : 0) + (p.w_pre != nullptr ? 1 : 0);
   const Shape h = shape_of(p.d, kBwdVec);
-  const int blocks = p.gate_rows ? bwd_blocks<T, true>(p.N, h) : bwd_blocks<T, false>(p.N, h);
+  const int blocks = bwd_blocks<T>(p.N, h);
   const dim3 grid(blocks);
-  if (h.threads > 512)
+  if (h.threads > 512 && h.nv == 1)
+    add_norm_bwd_as<T, 1, 1024>(p, q, h, grid, s);
+  else if (h.threads > 512)
     add_norm_bwd_as<T, 2, 1024>(p, q, h, grid, s);
-  else if (h.nv == 1)
-    add_norm_bwd_as<T, 1, 512>(p, q, h, grid, s);
   else
-    add_norm_bwd_as<T, 2, 512>(p, q, h, grid, s);
+    add_norm_bwd_as<T, 1, 512>(p, q, h, grid, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || q.sums == 0) return e;
   hipLaunchKernelGGL((column_sum_kernel<T>), dim3((unsigned)((q.sums * p.d + 63) / 64)), dim3(1024), 0, s, p, q, blocks);
@@ -633,7 +634,7 @@ hipError_t launch_add_norm(Dtype dt, const NormArgs& p, hipStream_t s) {
 
 uint64_t add_norm_bwd_workspace(int64_t N, int64_t d, int sums) {
   const Shape h = shape_of(d, kBwdVec);  // the most workgroups of all types
-  return N > 0 ? (uint64_t)bwd_blocks<__bf16, false>(N, h) * (uint64_t)sums * (uint64_t)d * 4 : 0;
+  return N > 0 ? (uint64_t)bwd_blocks<__bf16>(N, h) * (uint64_t)sums * (uint64_t)d * 4 : 0;
 }
 
 hipError_t launch_add_norm_bwd(Dtype dt, const NormArgs& p, const NormGrads& q, hipStream_t s) {

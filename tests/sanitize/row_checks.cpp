@@ -32,7 +32,7 @@ static void check_logprobs_workspace(int64_t N, int64_t V, int64_t top) {
     CHECK(st == CKL_EUNSUPPORTED);
   } else {
     CHECK(st == CKL_OK && b % 256 == 0);
-    CHECK(b <= (uint64_t)512 * 16 + (uint64_t)256 * 1024 * 8 + 256);  // 512 slices at most, 1,024 pairs a row
+    CHECK(b <= (uint64_t)1024 * 16 + (uint64_t)256 * 1024 * 8 + 256);  // 1,024 slices at most, 1,024 pairs a row
     if (N == 0 || N >= 256 || V < 8192) CHECK(b == 0);
   }
 }
