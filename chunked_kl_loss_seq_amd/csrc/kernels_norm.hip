@@ -145,14 +145,27 @@ __device__ inline void read8(float* w, int d, int c, float (&v)[8]) {
 template <typename T, bool ROWS>
 __device__ inline void column_weights(const NormArgs& p, float* f, float* w2) {
   const float k = p.drop.border ? p.scale * p.drop.keep : p.scale;
-  const int d = (int)p.d;
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    float v = k;
-    if (p.w_post != nullptr) v *= (float)((const T*)p.w_post)[c];
-    if (!ROWS && p.gate != nullptr) v *= (float)((const T*)p.gate)[c];
-    const int at = ((c >> 2) & 1) * (d >> 1) + (c >> 3) * 4 + (c & 3);
-    f[at] = v;
-    w2[at] = p.w_pre != nullptr ? (float)((const T*)p.w_pre)[c] : 0.f;
+  const int d = (int)p.d, d8 = d >> 3;
+  const bool gated = !ROWS && p.gate != nullptr;
+  for (int c = threadIdx.x; c < d8; c += blockDim.x) {
+    Eight<T> a, g, b;
+    if (p.w_post != nullptr) a.load((const T*)p.w_post + 8 * c);
+    if (gated) g.load((const T*)p.gate + 8 * c);
+    b.clear();
+    if (p.w_pre != nullptr) b.load((const T*)p.w_pre + 8 * c);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      row_f32x4 v, w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = k;
+        if (p.w_post != nullptr) v[j] *= a.get(4 * h + j);
+        if (gated) v[j] *= g.get(4 * h + j);
+        w[j] = b.get(4 * h + j);
+      }
+      *(row_f32x4*)half_at(f, d, c, h) = v;
+      *(row_f32x4*)half_at(w2, d, c, h) = w;
+    }
   }
   __syncthreads();
 }
