@@ -1,5 +1,5 @@
 // MFMA GEMM engine for gfx950 (CDNA4), shared by the three contractions of the
-// fused chunked KL loss:
+// fused chunked KL loss and of the log-probabilities from hidden states:
 //   logits    Z^T tile = W . H_c^T   (both operands contiguous along d)
 //   dH        dH_c     = G . W       (G contiguous along V, W contiguous along d)
 //   dW        dW      += G^T . H_c   (both operands contiguous along the token axis)
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
             for (int r = 0; r < NR; ++r)
               if ((int)mw + run0(i, r / 4) + r % 4 >= vm) acc[i][j][r] = -INFINITY;
         }
-        float mx = -INFINITY, s = 0.f, a = 0.f;
+        float mx = -3.402823466e38f, s = 0.f, a = 0.f;  // finite, also for a slice of -inf
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int64_t n = nw + MS * j + cl;
-        const bool rok = n < p.valid_n && n < live;
+        bool rok = n < p.valid_n && n < live;
         float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
         int32_t given = -1;
         float w = 0.f;
@@ -806,6 +806,10 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
           const float u = p.one.dentropy != nullptr ? p.one.dentropy[at] : 0.f;
           c = make_float4(p.one.stats[at], p.one.stats[p.one.n + at],
                           __builtin_fmaf(u, u != 0.f ? p.one.entropy[at] : 0.f, w), u);
+        }
+        if (c.x == -INFINITY) {  // no logit above -inf: no gradient
+          rok = false;
+          given = -1;
         }
 #pragma unroll
         for (int i = 0; i < FM; ++i)

@@ -138,7 +138,7 @@ def test_chunks_and_masks(ckl, dtype, base):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_rows(ckl, dtype):
-    # a sequence long enough for a tiled copy of W in the backward pass
+    # two and more chunks of thousands of rows, the last one short; many rows under few columns
     check(ckl, 8200, 200, 16, dtype, 1, chunk=4096)
     check(ckl, 9000, 130, 24, dtype, 2)
 
@@ -195,6 +195,61 @@ def test_nan_stays_in_its_row(ckl):
     out = ckl.head_logprobs(tH, tW, ids, mask=mask)
     dH, dW = ckl.head_logprobs_bwd(tH, tW, ids, *out, one, one, mask=mask)
     assert all(bool(t.isfinite().all()) for t in (*out, dH, dW)) and not dH[4].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [3, 600])
+def test_weights_of_minus_infinity(ckl, dtype, N):
+    """Ids whose logits are all -inf, whole slices of them, weigh nothing, as if they were not there."""
+    V, cut, d = 9000, 300, 64
+    rng = np.random.default_rng(N)
+    H, W = rng.standard_normal((N, d)), rng.standard_normal((V, d))
+    H[:, 0] = 1.0
+    W[:cut, 0] = -np.inf
+    tH, tW = dev(H, dtype), dev(W, dtype)
+    ids = rng.integers(0, V, (N, 2)).astype(np.int32)
+    ids[:, 1] = rng.integers(0, cut, N)
+    out = ckl.head_logprobs(tH, tW, torch.from_numpy(ids).to("cuda:0"))
+    H, W = host(tH), host(tW)[cut:]
+    z = H @ W.T
+    tz = (d + 8) * H24 * (np.abs(H) @ np.abs(W).T)
+    E = tz.max(1)
+    b = Bounds(z)
+    same(host(out.entropy), b.H, b.th + E * (b.p * np.abs(b.logp + b.H[:, None])).sum(1), "entropy")
+    same(host(out.stats)[0], b.M, E, "M")
+    rest = np.where(ids >= cut, ids - cut, -1)
+    want = O.given(b.logp, rest)
+    bound = b.of_logp(O.given(b.d, rest), want) + O.given(tz, rest) + E[:, None]
+    same(host(out.logp), np.where(ids >= cut, want, -np.inf), bound, "logp")
+    one = torch.ones(N, device="cuda:0")
+    _, dW = ckl.head_logprobs_bwd(tH, tW, None, None, out.entropy, out.stats, None, one)
+    assert not dW[:cut].any() and bool(dW.isfinite().all()) and bool(dW[cut:].any())
+    # no token at all
+    W = tW[:cut].clone()
+    for T in (1, 2):
+        tid = torch.zeros((N, T), dtype=torch.int32, device="cuda:0")
+        tid[:, -1] = -1
+        out = ckl.head_logprobs(tH, W, tid)
+        want = torch.full((N, T), -float("inf"), device="cuda:0")
+        want[:, -1] = 0
+        assert torch.equal(out.logp, want) and not out.entropy.any()
+        assert bool((out.stats[0] == -float("inf")).all()) and not out.stats[1].any()
+        tid.zero_()
+        out = ckl.head_logprobs(tH, W, tid)
+        _, dW = ckl.head_logprobs_bwd(tH, W, tid, *out, torch.ones(N, T, device="cuda:0"), one)
+        assert not dW.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_certain_token_is_not_above_one(ckl, dtype):
+    rng = np.random.default_rng(3)
+    W = rng.standard_normal((700, 520))
+    ids = rng.integers(0, 700, 300).astype(np.int32)
+    tW = dev(W, dtype)
+    out = ckl.head_logprobs(dev(W[ids], dtype), tW, torch.from_numpy(ids).to("cuda:0"))
+    # its logit, sum W^2, is some 400 above any other, so logp is 0 but for its two sums' errors
+    least = -2 * (520 + 8) * H24 * (host(tW) ** 2).sum(1).max()
+    assert bool((out.logp <= 0).all()) and bool((out.logp >= least).all()) and bool((out.entropy >= 0).all())
 
 
 def test_no_rows(ckl):
