@@ -1111,7 +1111,7 @@ int ckl_add_norm(int dtype, const void* y, const void* r, const ckl_norm* how, i
   const uintptr_t el = dtype == CKL_DTYPE_BF16 ? 2 : 4;
   if (!aligned(r_out, el) || !aligned(x, el) || !aligned(stats, 4)) return CKL_EINVAL;
   if (N == 0) return CKL_OK;
-  if (!y || !r || !r_out || (p.w_pre != nullptr) != (x != nullptr)) return CKL_EINVAL;
+  if (!y || !r || !r_out || r_out == x || (p.w_pre != nullptr) != (x != nullptr)) return CKL_EINVAL;
   p.r_out = r_out;
   p.x = x;
   p.stats = stats;
@@ -1159,6 +1159,7 @@ int ckl_add_norm_bwd(int dtype, const void* y, const void* r, const ckl_norm* ho
       return CKL_OK;
     }
     if (!y || !r || !stats || !dy || !dr || (!dx && !dr_in) || (dx && !p.w_pre)) return CKL_EINVAL;
+    if (dy == dr || dgate == dy || dgate == dr) return CKL_EINVAL;  // dgate may be null, these are not
     if (n_sums && (!workspace || workspace_bytes < add_norm_bwd_workspace(N, d, n_sums))) return CKL_EINVAL;
     p.stats_in = stats;
     q.dx = dx;

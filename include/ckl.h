@@ -420,7 +420,7 @@ int ckl_dropout(int dtype, const void* x, int64_t n, const ckl_drop* how, void* 
  *   w_post    [d] or NULL;  w_pre [d], or NULL: x (then NULL) is not computed
  *   gate      [d], or [N, d] with gate_rows = 1, or NULL for 1
  *   drop      NULL: nothing is dropped
- *   r_out     [N, d], may be r (a gradient needs r as it was); x [N, d]
+ *   r_out     [N, d], may be r (a gradient needs r as it was); x [N, d], not r_out
  *   stats     fp32 [2, N] or NULL: 1 / rms(y) and 1 / rms(r') (1 where not
  *             computed), for the gradient
  * d % 8 == 0, d <= 16384, N <= 2^31; arrays aligned to an element.  A row of
@@ -441,7 +441,7 @@ int ckl_add_norm(int dtype, const void* y, const void* r, const ckl_norm* how, i
  * forward call's.
  *   dx, dr_in   gradients of x and of r_out; either may be NULL for zeros (dx is
  *               NULL without w_pre), not both
- *   dy, dr      [N, d] in dtype; dr may be dr_in, dy may be dx
+ *   dy, dr      [N, d] in dtype; dr may be dr_in, dy may be dx; one array each
  *   dw_post, dw_pre  fp32 [d], each NULL exactly where the weight is
  *   dgate       fp32 [d], or [N, d] in dtype with gate_rows, NULL without a gate
  *   workspace   at least ckl_add_norm_bwd_workspace(N, d, sums) bytes, sums = how

@@ -127,9 +127,10 @@ def check(ckl, dtype, N, d, post, pre, gate, p, **kw):
     assert (dw_post is None) == (not post) and (dw_pre is None) == (not pre) and (dgate is None) == (gate == "none")
 
 
-# rows of one lane up to the widest, both sides of every change of shape: 8 x 64, 8 x 64 x 3, 8 x 512 x 3 elements
-SIZES = [(1, 8), (5, 16), (67, 24), (130, 64), (9, 512), (9, 520), (3, 1536), (3, 1544), (257, 2880), (2, 4104),
-         (2, 12288), (2, 12296), (3, 16384)]
+# rows of one lane up to the widest, both sides of every change of shape: rows side by side up to 512 elements, one or
+# two vectors a lane from 1,024, workgroups of more than 512 threads from 4,096 or 8,192, two vectors of those from 8,192
+SIZES = [(1, 8), (5, 16), (67, 24), (130, 64), (9, 512), (9, 520), (7, 1024), (7, 1032), (3, 1536), (3, 1544), (257, 2880),
+         (3, 4096), (2, 4104), (3, 8192), (600, 8200), (2, 12288), (2, 12296), (3, 16384)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -145,6 +146,19 @@ def test_sizes(ckl, dtype, N, d):
 @pytest.mark.parametrize("p", [0.0, 0.3])
 def test_forms(ckl, dtype, post, pre, gate, p):
     check(ckl, dtype, 37, 200, post, pre, gate, p)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [1032, 4104, 8200])
+def test_wide_rows_with_their_own_gates(ckl, dtype, d):
+    check(ckl, dtype, 5, d, True, True, "full", 0.2)
+    check(ckl, dtype, 5, d, False, True, "none", 0.0)
+
+
+@pytest.mark.parametrize("p", [1.0, 1 - 2.0 ** -18, 2.0 ** -18])
+def test_everything_or_nothing_dropped(ckl, p):
+    check(ckl, "f32", 21, 72, True, True, "vector", p)
+    check(ckl, "bf16", 21, 72, True, True, "full", p)
 
 
 @pytest.mark.parametrize("grads", [("dx",), ("dr",)])

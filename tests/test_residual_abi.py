@@ -35,7 +35,8 @@ def norm(w_post, w_pre, gate, rows, eps, p):
     return B.Norm(w_post, w_pre, gate, rows, 1.0, eps, ctypes.pointer(d) if d else None)
 
 
-def add_norm(dt=0, y=G, r=G, N=4, d=64, w_post=G, w_pre=G, gate=G, rows=0, eps=1e-6, p=None, ro=G, x=G, stats=G, how=True):
+def add_norm(dt=0, y=G, r=G, N=4, d=64, w_post=G, w_pre=G, gate=G, rows=0, eps=1e-6, p=None, ro=G, x=2 * G, stats=G,
+             how=True):
     h = norm(w_post, w_pre, gate, rows, eps, p)
     return B.lib().ckl_add_norm(dt, y, r, ctypes.byref(h) if how else None, N, d, ro, x, stats, None)
 
@@ -51,14 +52,14 @@ COMMON = [
 
 @pytest.mark.parametrize("bad,want", COMMON + [
     ({"ro": None}, EINVAL), ({"x": None}, EINVAL), ({"w_pre": None}, EINVAL), ({"ro": G + 1}, EINVAL), ({"x": G + 1}, EINVAL),
-    ({"N": 0, "y": None, "r": None, "ro": None, "x": None}, OK),
+    ({"x": G}, EINVAL), ({"N": 0, "y": None, "r": None, "ro": None, "x": None}, OK),
 ])
 def test_add_norm(bad, want):
     assert add_norm(**bad) == want
 
 
-def bwd(dt=0, y=G, r=G, N=4, d=64, w_post=G, w_pre=G, gate=G, rows=0, eps=1e-6, p=None, stats=G, dx=G, dr_in=G, dy=G, dr=G,
-        dw_post=G, dw_pre=G, dgate=G, ws=G, bytes_=1 << 30, how=True):
+def bwd(dt=0, y=G, r=G, N=4, d=64, w_post=G, w_pre=G, gate=G, rows=0, eps=1e-6, p=None, stats=G, dx=G, dr_in=G, dy=2 * G,
+        dr=3 * G, dw_post=G, dw_pre=G, dgate=4 * G, ws=G, bytes_=1 << 30, how=True):
     h = norm(w_post, w_pre, gate, rows, eps, p)
     return B.lib().ckl_add_norm_bwd(dt, y, r, ctypes.byref(h) if how else None, N, d, stats, dx, dr_in, dy, dr, dw_post,
                                     dw_pre, dgate, ws, bytes_, None)
@@ -70,6 +71,7 @@ def bwd(dt=0, y=G, r=G, N=4, d=64, w_post=G, w_pre=G, gate=G, rows=0, eps=1e-6, 
     ({"dgate": None}, EINVAL), ({"gate": None}, EINVAL), ({"ws": None}, EINVAL), ({"ws": G + 128}, EINVAL),
     ({"bytes_": 3 * 64 * 4 - 1}, EINVAL), ({"dx": G + 1}, EINVAL), ({"dr_in": G + 1}, EINVAL), ({"dy": G + 1}, EINVAL),
     ({"dr": G + 1}, EINVAL), ({"dw_post": G + 2}, EINVAL), ({"dw_pre": G + 2}, EINVAL), ({"dgate": G + 2}, EINVAL),
+    ({"dy": 3 * G}, EINVAL), ({"dgate": 2 * G}, EINVAL), ({"rows": 1, "dgate": 3 * G}, EINVAL),
 ])
 def test_add_norm_bwd(bad, want):
     assert bwd(**bad) == want
