@@ -101,9 +101,7 @@ __global__ void __launch_bounds__(NT) head_rows_kernel(HeadArgs p, int64_t r0, c
       a = __builtin_fmaf(__builtin_fmaf(v[u].y, dm, va[u]), k, a);
     }
   }
-  float top = M;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  float top = wave_max(M);
   if ((t & 63) == 0) red[w] = top;
   __syncthreads();
 #pragma unroll

@@ -20,6 +20,15 @@
 // those that do; up to 128 are placed by the number of larger (logit, lower id)
 // pairs, more are sorted.  Where more than 1,024 reach the bound (equal logits), a
 // binary search over the pairs narrows it first.
+//
+// Bound by reading the logits.  Measured (MI355X):
+//  1,024 x 201,088 bf16: 74 us, 5.6 TB/s (with 100 given tokens a row as well); 20
+//    alternatives 100 us, 128 132 us.  fp32 140 us, 5.9 TB/s.
+//  2,048 x 128,256 bf16 forward and gradient, a tenth of the rows masked: 284 us,
+//    5.2 TB/s of 1.47 GB.
+//  1 x 201,088 bf16, 20 alternatives: 7.9 us for the slices and 4.8 for joining them.
+// A workgroup of 1,024 threads a row: with 512 and 256 the second of these took 292
+// and 294 us.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -79,12 +88,6 @@ struct Sums {
     }
   }
 };
-
-__device__ inline float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
 
 // (M, S, A) of all threads of the workgroup, in every thread.
 template <int NT>
