@@ -14,21 +14,23 @@
 // held at -1000, whose exponential is 0, so that 0 x -inf never arises); NaN
 // passes through to the row's results.
 //
-// Alternatives: the K-th largest of the maxima of 64 groups of threads (or of
-// the threads themselves), cut to 16 bits, is a bound that at least K logits
-// reach.  Threads whose maximum reaches it read their logits again and collect
-// those that do; up to 128 are placed by the number of larger (logit, lower id)
-// pairs, more are sorted.  Where more than 1,024 reach the bound (equal logits), a
-// binary search over the pairs narrows it first.
+// Alternatives: a thread keeps the largest logit of each half of its share.  The
+// K-th largest of those (or of the maxima of 64 groups of threads), cut to 16 bits,
+// is a bound that at least K logits reach.  The halves whose maximum reaches it are
+// read again, each by several lanes at once, and what reaches it is collected; up
+// to 128 are placed by the number of larger (logit, lower id) pairs, more are
+// sorted.  Where more than 1,024 reach the bound (equal logits), a binary search over
+// the pairs narrows it first.  All of it is inlined: as calls, which the compiler
+// made of what two kernels share, the registers saved around them cost 20 to 50 us
+// of every case with alternatives below.
 //
 // Bound by reading the logits.  Measured (MI355X):
-//  1,024 x 201,088 bf16: 74 us, 5.6 TB/s (with 100 given tokens a row as well); 20
-//    alternatives 100 us, 128 132 us.  fp32 140 us, 5.9 TB/s.
+//  1,024 x 201,088 bf16: 72 us, 5.7 TB/s (with 100 given tokens a row 74); 20
+//    alternatives 75 us, 128 110 us, 400 154 us.  fp32 140 us, with 20 148 us.
+//  3,000 x 40,001 bf16, 20 alternatives: 51 us for 46 without.
 //  2,048 x 128,256 bf16 forward and gradient, a tenth of the rows masked: 284 us,
 //    5.2 TB/s of 1.47 GB.
-//  1 x 201,088 bf16, 20 alternatives: 7.9 us for the slices and 4.8 for joining them.
-// A workgroup of 1,024 threads a row: with 512 and 256 the second of these took 292
-// and 294 us.
+//  1 x 201,088 bf16, 20 alternatives: 7.7 us for the slices and 4.6 for joining them.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -45,8 +47,11 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = -1000.f;  // exp(kFar) is 0 in fp32
 constexpr int kList = 1024;      // pairs held in LDS
 constexpr int kGroups = 64;
-constexpr int kGroupTop = 48;    // up to this many alternatives the bound comes from the groups' maxima
-constexpr int kWideTop = 128;    // beyond, rows are taken by 1,024 threads, whose maxima give a bound up to 512
+// Up to this many alternatives the bound comes from the groups' maxima (2,048 x 128,256
+// bf16, 20: 139 us and 140 with the threads' own; 48: 167 and 155, the coarser bound
+// lets more through).
+constexpr int kGroupTop = 24;
+constexpr int kWideTop = 128;    // beyond, 256 threads' maxima are too few for a bound
 
 __device__ inline float exp_fast(float t) { return __builtin_amdgcn_exp2f(t * kLog2); }
 // the larger of t and kFar; NaN stays NaN
@@ -138,7 +143,7 @@ struct RowResult {
 template <int NT>
 struct TopLds {
   u64 list[kList], other[kList];
-  uint32_t keys[NT > kGroups ? NT : kGroups];
+  uint32_t keys[2 * NT];
   int n, count[2];
   uint32_t bound;
 };
@@ -146,7 +151,7 @@ struct TopLds {
 // By one wave: the largest 16-bit prefix that at least K of n <= 1,024 keys reach, as
 // a key (0 if fewer than K keys are above 0).
 template <typename F>
-__device__ inline uint32_t prefix_bound(F key, int n, int K) {
+__device__ __forceinline__ uint32_t prefix_bound(F key, int n, int K) {
   const int lane = threadIdx.x & 63;
   uint32_t v[kList / 64];
 #pragma unroll
@@ -164,7 +169,7 @@ __device__ inline uint32_t prefix_bound(F key, int n, int K) {
 }
 
 // The number of larger pairs in the list (kList long; entries past n may hold anything).
-__device__ inline int rank_in(const u64* list, int n, u64 pair) {
+__device__ __forceinline__ int rank_in(const u64* list, int n, u64 pair) {
   int rank = 0;
   for (int j = 0; j < n; j += 8) {
     u64 o[8];
@@ -180,7 +185,7 @@ __device__ inline int rank_in(const u64* list, int n, u64 pair) {
 // order; `other` is scratch.  Returns where they are.  The workgroup comes here
 // together, and goes on with the result in sight of all.
 template <int NT>
-__device__ inline const u64* order_top(u64* list, u64* other, int& n, int K, int* count, uint32_t* bound) {
+__device__ __forceinline__ const u64* order_top(u64* list, u64* other, int& n, int K, int* count, uint32_t* bound) {
   const int t = threadIdx.x;
   if (n > 128 && n > 2 * K) {  // fewer first: those that reach the K-th largest's prefix
     if (t < 64) {
@@ -231,7 +236,7 @@ __device__ inline const u64* order_top(u64* list, u64* other, int& n, int K, int
 
 // Number of (key, id) pairs at or above `from` among the elements [lo, hi) of a row.
 template <typename T, int NT>
-__device__ inline int count_from(const T* row, int64_t lo, int64_t hi, u64 from, TopLds<NT>& sh, int turn) {
+__device__ __forceinline__ int count_from(const T* row, int64_t lo, int64_t hi, u64 from, TopLds<NT>& sh, int turn) {
   if (threadIdx.x == 0) sh.count[turn] = 0;
   __syncthreads();
   int c = 0;
@@ -246,19 +251,27 @@ __device__ inline int count_from(const T* row, int64_t lo, int64_t hi, u64 from,
   return sh.count[turn];
 }
 
+// A thread takes the vectors t + k NT of a run of n8; k < first_half(n8) are its first half.
+template <int NT>
+__device__ inline int64_t first_half(int64_t n8) {
+  const int64_t h = (n8 + NT - 1) / NT / 2;
+  return h >= 8 ? h / 4 * 4 : h > 0 ? h : 1;  // whole turns of the scan
+}
+
 // Collects into sh.list at least the K largest pairs of the row's elements
-// [lo, hi) (all of them if there are fewer), at most kList; mx is the largest of
-// the elements this thread took (8 in turn with the others), M the row's.
+// [lo, hi) (all of them if there are fewer), at most kList; mx0 and mx1 are the
+// largest of the two halves of the elements that this thread took, M the row's.
 template <typename T, int NT>
-__device__ inline int collect_top(const T* row, int64_t lo, int64_t hi, float mx, float M, int K, TopLds<NT>& sh) {
+__device__ __forceinline__ int collect_top(const T* row, int64_t lo, int64_t hi, float mx0, float mx1, float M, int K,
+                                  TopLds<NT>& sh) {
   const int t = threadIdx.x;
-  const uint32_t mine = key_of(mx);
+  const uint32_t key0 = key_of(mx0), key1 = key_of(mx1);
   if (t == 0) {
-    sh.n = 0;
+    sh.n = sh.count[0] = 0;
     sh.bound = 0u;
   }
-  if (K <= kGroupTop) {
-    uint32_t g = mine;
+  if (K <= kGroupTop && NT > 64) {
+    uint32_t g = key0 > key1 ? key0 : key1;
 #pragma unroll
     for (int o = 1; o < NT / kGroups; o <<= 1) {
       const uint32_t h = (uint32_t)__shfl_xor((int)g, o);
@@ -277,48 +290,58 @@ __device__ inline int collect_top(const T* row, int64_t lo, int64_t hi, float mx
       }
       if (t == 0) sh.bound = best << 16;
     }
-    __syncthreads();
-  } else if (K <= NT / 2) {
-    sh.keys[t] = mine;
+  } else if (K <= NT) {
+    sh.keys[t] = key0;
+    sh.keys[NT + t] = key1;
     __syncthreads();
     if (t < 64) {
-      const uint32_t b = prefix_bound([&](int i) { return sh.keys[i]; }, NT, K);
+      const uint32_t b = prefix_bound([&](int i) { return sh.keys[i]; }, 2 * NT, K);
       if (t == 0) sh.bound = b;
     }
-    __syncthreads();
-  } else {
-    __syncthreads();
   }
+  __syncthreads();
   const uint32_t bound = sh.bound > 1u ? sh.bound : 1u;
-  if (mine >= bound) {
-    const float least = bound > 1u ? key_value(bound) : kLowest;  // NaN and -inf do not reach it
-    const auto take = [&](float z, int64_t id) {
-      if (z >= least) {
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < kList) sh.list[at] = pair_of(key_of(z), id);
-      }
-    };
-    const int64_t n8 = (hi - lo) / 8;
-    constexpr int U = sizeof(T) == 2 ? 6 : 3;  // vectors under way
-    for (int64_t i = t; i < n8; i += U * NT) {
+  // The halves that hold such a maximum; g lanes (a power of two) read each one's logits again.
+  if (key0 >= bound) sh.keys[atomicAdd(&sh.count[0], 1)] = (uint32_t)t;
+  if (key1 >= bound) sh.keys[atomicAdd(&sh.count[0], 1)] = (uint32_t)(NT + t);
+  __syncthreads();
+  const int owners = sh.count[0];
+  const float least = bound > 1u ? key_value(bound) : kLowest;  // NaN and -inf do not reach it
+  const auto take = [&](float z, int64_t id) {
+    if (z >= least) {
+      const int i = atomicAdd(&sh.n, 1);
+      if (i < kList) sh.list[i] = pair_of(key_of(z), id);
+    }
+  };
+  const int64_t n8 = (hi - lo) / 8, half = first_half<NT>(n8), rest = (n8 + NT - 1) / NT - half;
+  const int64_t most = rest > half ? rest : half;
+  int g = 1;
+  while (g < 64 && g < most) g <<= 1;
+  const int teams = NT / g;
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // vectors under way
+  for (int o = t / g; o < owners && n8 > 0; o += U * teams)
+    for (int64_t j = t & (g - 1); j < most; j += g) {
       Eight<T> v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u].load(row + lo + 8 * (i + u * NT < n8 ? i + u * NT : i));
+      int64_t at[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (i + u * NT >= n8) continue;
+        const uint32_t q = o + u * teams < owners ? sh.keys[o + u * teams] : 2 * NT;
+        at[u] = q < NT && j < half ? q + j * NT : q >= NT && q < 2 * NT ? q - NT + (half + j) * NT : n8;
+        v[u].load(row + lo + 8 * (at[u] < n8 ? at[u] : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (at[u] >= n8) continue;
         float z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = v[u].get(e);
         if (fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7]))) >= least) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) take(z[e], lo + 8 * (i + u * NT) + e);
+          for (int e = 0; e < 8; ++e) take(z[e], lo + 8 * at[u] + e);
         }
       }
     }
-    if (t == n8 % NT)
-      for (int64_t i = lo + 8 * n8; i < hi; ++i) take((float)row[i], i);
-  }
+  if (lo + 8 * n8 + t < hi) take((float)row[lo + 8 * n8 + t], lo + 8 * n8 + t);
   __syncthreads();
   int n = sh.n;
   if (n <= kList) return n;
@@ -350,7 +373,7 @@ __device__ inline int collect_top(const T* row, int64_t lo, int64_t hi, float mx
 // ------------------------------------------------------------------ forward
 // The sums of the row's elements [lo, hi), this thread's share: vectors of 8 in turn.
 template <typename T, int NT>
-__device__ inline void scan(const T* row, int64_t lo, int64_t hi, Sums& v) {
+__device__ __forceinline__ void scan(const T* row, int64_t lo, int64_t hi, Sums& v) {
   constexpr int U = 4;  // vectors in flight
   const int64_t n8 = (hi - lo) / 8;
   const T* p = row + lo;
@@ -381,6 +404,23 @@ __device__ inline void scan(const T* row, int64_t lo, int64_t hi, Sums& v) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = e < rest ? (float)p[8 * n8 + e] : -INFINITY;
     v.add8(z);
+  }
+}
+
+// The same, with the largest logit of each half of the thread's share for the alternatives.
+template <typename T, int NT, bool TOP>
+__device__ __forceinline__ void scan_halves(const T* row, int64_t lo, int64_t hi, Sums& v, float& mx0, float& mx1) {
+  if constexpr (TOP) {
+    int64_t mid = lo + 8 * NT * first_half<NT>((hi - lo) / 8);
+    if (mid > hi) mid = hi;
+    scan<T, NT>(row, lo, mid, v);
+    mx0 = v.mx;
+    v.mx = -INFINITY;
+    scan<T, NT>(row, mid, hi, v);
+    mx1 = v.mx;
+    v.mx = fmaxf(mx0, mx1);
+  } else {
+    scan<T, NT>(row, lo, hi, v);
   }
 }
 
@@ -432,14 +472,14 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) lo
   }
   const T* x = (const T*)p.x + row * p.ld;
   Sums v;
-  scan<T, NT>(x, 0, p.V, v);
-  const float mine = v.mx;
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+  scan_halves<T, NT, TOP>(x, 0, p.V, v, mx0, mx1);
   block_sums<NT>(v, red);
   const RowResult r(v);
   write_row<T>(p, row, r, t, NT);
   if constexpr (TOP) {
     __shared__ TopLds<NT> sh;
-    int n = collect_top<T, NT>(x, 0, p.V, mine, v.mx, p.top, sh);
+    int n = collect_top<T, NT>(x, 0, p.V, mx0, mx1, v.mx, p.top, sh);
     const u64* sorted = order_top<NT>(sh.list, sh.other, n, p.top, &sh.count[0], &sh.bound);
     write_top(p, row, sorted, n, r, t, NT);
   }
@@ -455,14 +495,14 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) lo
   const T* x = (const T*)p.x + row * p.ld;
   const int64_t lo = sl * p.per, hi = lo + p.per < p.V ? lo + p.per : p.V;
   Sums v;
-  scan<T, NT>(x, lo, hi, v);
-  const float mine = v.mx;
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+  scan_halves<T, NT, TOP>(x, lo, hi, v, mx0, mx1);
   block_sums<NT>(v, red);
   if (t == 0) p.part[blockIdx.x] = make_float4(v.mx, v.m, v.s, v.a);
   if constexpr (TOP) {
     __shared__ TopLds<NT> sh;
     u64* out = (u64*)p.pairs + (int64_t)blockIdx.x * p.top;
-    int n = collect_top<T, NT>(x, lo, hi, mine, v.mx, p.top, sh);
+    int n = collect_top<T, NT>(x, lo, hi, mx0, mx1, v.mx, p.top, sh);
     const u64* sorted = order_top<NT>(sh.list, sh.other, n, p.top, &sh.count[0], &sh.bound);
     for (int i = t; i < p.top; i += NT) out[i] = i < n ? sorted[i] : 0;
   }
@@ -658,7 +698,7 @@ hipError_t logprob_of(const LogprobArgs& p, hipStream_t s) {
   if (p.slices > 1) {
     const dim3 grid((unsigned)(p.N * p.slices));
     if (p.top > kWideTop)
-      hipLaunchKernelGGL((logprob_slice_kernel<T, 1024, true>), grid, dim3(1024), 0, s, p);
+      hipLaunchKernelGGL((logprob_slice_kernel<T, 512, true>), grid, dim3(512), 0, s, p);
     else if (p.top)
       hipLaunchKernelGGL((logprob_slice_kernel<T, 256, true>), grid, dim3(256), 0, s, p);
     else
@@ -672,6 +712,8 @@ hipError_t logprob_of(const LogprobArgs& p, hipStream_t s) {
     logprob_rows<T, 64>(p, s);
   else if (p.V <= 8192 && p.top <= kWideTop)
     logprob_rows<T, 256>(p, s);
+  else if (p.top)
+    logprob_rows<T, 512>(p, s);
   else
     logprob_rows<T, 1024>(p, s);
   return hipGetLastError();
