@@ -13,18 +13,19 @@
 //   sum e n1 = sum q (dr' + a / rms(r')) - (mean(a n2) / rms(r')) sum q n2,
 // so one round of three sums serves a row.
 //
-// Bound by HBM: forward two arrays read and two written, backward four and two, and
-// the numbers' generator (about 30 us of vector instructions for 94 M elements,
-// hidden but in the backward pass at 2,880 columns, whose six waves a row leave a
-// quarter of a compute unit's wave slots empty).
+// Bound by HBM: forward two arrays read and two written, backward four and two.  The
+// numbers' generator (about 30 us of vector instructions for 94 M elements) hides
+// behind them.
 // Measured (MI355X, bf16): 32,768 x 2,880 with both weights, a gate [d] and p = 0.1:
-// forward 144 us (5.2 TB/s), backward 270 us (4.2 TB/s; without dropout 231), sums of
-// columns 5 us.  16,384 x 4,096 backward 167 us (4.8 TB/s).  One row of 2,880: 4.2 us.
-// dropout of 94 M bf16 elements 66 us (5.7 TB/s).
+// forward 140 us (5.4 TB/s), backward 240 us (4.7 TB/s), of which the sums of columns
+// take 5.  8,192 x 8,192 backward 163 us (4.9 TB/s).  One row of 2,880: 4.0 us.
+// dropout of 94 M bf16 elements 67 us (5.6 TB/s).
+// Rows wider than 8,192 are far from that backward (4,096 x 12,288: 254 us, 117 at the
+// copy's rate): 1,024 threads hold two vectors each, which do not fit 128 registers.
 // What carried it: loads of the next row under way for a whole turn (a select right
 // after each load had made every load wait for the one before), a barrier for LDS
 // alone (the ordinary one waits for all loads), the columns' weights in LDS instead
-// of registers, as many workgroups as fit at once.
+// of registers, as many workgroups as fit at once, sums over lanes in registers.
 #include <hip/hip_runtime.h>
 
 #include "row_io.hpp"
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(NormArgs p, NormGrads 
 
 // A row's lanes, and how many vectors of 8 each holds: up to `most`, or two where 16
 // waves would not do.  Forward two (32,768 x 2,880 bf16 146 us, with one 190), backward
-// one (272 us, with two 330): fewer registers, more rows under way.
+// one (272 us, with two 330; both before sums over lanes stayed in registers): fewer registers, more rows under way.
 constexpr int kFwdVec = 2, kBwdVec = 1;
 struct Shape {
   Team team;
