@@ -536,7 +536,7 @@ int logprob_shape(int dtype, const void* logits, int64_t N, int64_t V, int64_t l
 struct HeadLayout {
   int64_t C = 0, pblk = 0;
   int n_slices = 0;
-  HeadTile tile = TILE_256;  // forward: the contraction's
+  HeadTiling tiling{TILE_256, TILE_256, 0};  // forward: the contraction's
   HeadSplit split{TILE_256, 0};
   uint64_t live_off = 0, hc_off = 0, vidx_off = 0, pos_off = 0, part_off = 0, parta_off = 0, g_off = 0, coef_off = 0, slab_off = 0, dw_off = 0, total = 0;
 };
@@ -545,8 +545,8 @@ HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C
   HeadLayout L;
   L.C = C;
   L.pblk = tile_row_stride(V);
-  L.tile = head_logits_tile(esz == 2 ? DT_BF16 : DT_F32, C, V);
-  L.n_slices = (int)((V + head_slice(L.tile) - 1) / head_slice(L.tile));
+  L.tiling = head_logits_tiling(esz == 2 ? DT_BF16 : DT_F32, C, V, d);
+  L.n_slices = head_slices(L.tiling, V);
   uint64_t off = 0;
   const auto take = [&off](uint64_t bytes) {
     const uint64_t at = off;
@@ -1019,7 +1019,7 @@ int ckl_head_logprobs(int dtype, const void* H, const void* W, const int32_t* id
       const int64_t rows = N - r0 < L.C ? N - r0 : L.C;
       Chunk k;
       CKL_TRY(head_chunk(c, L, H, d, r0, rows, entropy + r0, &k, stream));
-      CKL_TRY(launch_head_stats(c.dt, L.tile, p, k.Hc, rows, part, part_a, L.n_slices, k.live, stream));
+      CKL_TRY(launch_head_stats(c.dt, L.tiling, p, k.Hc, rows, part, part_a, L.n_slices, k.live, stream));
       CKL_TRY(launch_head_rows(c.dt, p, r0, rows, part, part_a, L.n_slices, k.pos, stream));
     }
     return CKL_OK;

@@ -94,6 +94,7 @@ struct GradRow {
   const float* entropy;
   const float* stats;      // [2, n]
   int64_t n;
+  int64_t vocab, base;     // all ids, and the first of this launch
 };
 
 struct GemmParams {
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
           s += __shfl_xor(s, o);
           a += __shfl_xor(a, o);
         }
-        if (sub == 0 && n < p.valid_n && slice < p.n_slices) {
+        if (sub == 0 && n < p.valid_n && mw < p.valid_m) {
           p.part[n * p.n_slices + slice] = make_float2(mx, s);
           p.part_a[n * p.n_slices + slice] = a;
         }
@@ -801,8 +802,9 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
         } else if (rok) {
           const int64_t at = p.g_rowmap != nullptr ? p.g_rowmap[n] : n;
           given = p.one.ids[at];
-          if (given < 0 || given >= p.valid_m) given = -1;
+          if (given < 0 || given >= p.one.vocab) given = -1;
           if (given >= 0) w = p.one.dlogp[at];
+          given -= (int32_t)p.one.base;
           const float u = p.one.dentropy != nullptr ? p.one.dentropy[at] : 0.f;
           c = make_float4(p.one.stats[at], p.one.stats[p.one.n + at],
                           __builtin_fmaf(u, u != 0.f ? p.one.entropy[at] : 0.f, w), u);
@@ -821,7 +823,7 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
           }
         // the given token's own element, in the one wave that holds it
         const int own = given - (int)mw;
-        if (given >= 0 && own >= 0 && own < WTM) {
+        if (given >= 0 && given < vm && own >= 0 && own < WTM) {
 #pragma unroll
           for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -886,21 +888,45 @@ __global__ void __launch_bounds__(WM* WN * 64) __attribute__((amdgpu_waves_per_e
       }
     }
   } else if constexpr (EPI == EPI_ROUND) {
+    // Through the wave's part of LDS, as 16-byte stores (2-byte ones from the accumulators cost
+    // a 201,088 x 2,880 dW of one row 461 us, these 350).  Neighbouring lanes hold neighbouring
+    // columns: of two rows the even lane packs the first one's pair, the odd lane the second's.
+    constexpr int RB = WTN * 2, CH = RB / 16;  // bytes and 16-byte chunks of a row
+    static_assert(NW * WTM * RB <= NS * STAGE, "the tile in bf16 has to fit");
     __bf16* out = (__bf16*)p.out;
+    __syncthreads();
+    char* wl = smem + wave * (WTM * RB);
+    const bool odd = lane & 1;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int64_t n = nw + j * 32 + col;
-        if (!full && n >= p.valid_n) continue;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t m = mw + i * 32 + (r >> 2) * 8 + h * 4 + (r & 3);
-          if (!full && m >= p.valid_m) continue;
-          const float v = acc[i][j][r];
-          out[m * p.ldo + n] = (__bf16)(p.old != nullptr ? p.old[m * p.ldo + n] + v : v);
+        for (int r = 0; r < 16; r += 2) {
+          const int row = i * 32 + (r >> 2) * 8 + h * 4 + (r & 3);
+          float v0 = acc[i][j][r], v1 = acc[i][j][r + 1];
+          if (p.old != nullptr && n < p.valid_n) {
+            const int64_t m = mw + row;
+            if (m < p.valid_m) v0 += p.old[m * p.ldo + n];
+            if (m + 1 < p.valid_m) v1 += p.old[(m + 1) * p.ldo + n];
+          }
+          const int give = __builtin_bit_cast(int, odd ? v0 : v1);
+          const float got = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(give, give, 0xB1, 0xF, 0xF, true));
+          typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+          const bf16x2 w = {(__bf16)(odd ? got : v0), (__bf16)(odd ? v1 : got)};
+          const int at = row + (odd ? 1 : 0), byte = 2 * (j * 32 + (col & ~1));
+          *(bf16x2*)(wl + at * RB + (((byte >> 4) ^ (at & (CH - 1))) << 4) + (byte & 15)) = w;
         }
       }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < WTM * CH / 64; ++k) {
+      const int idx = k * 64 + lane, row = idx / CH, c = idx % CH;
+      const int64_t m = mw + row, n = nw + 8 * c;
+      if (m < p.valid_m && n < p.valid_n)
+        *(u32x4*)(out + m * p.ldo + n) = *(const u32x4*)(wl + row * RB + ((c ^ (row & (CH - 1))) << 4));
+    }
   } else if constexpr (MS == 16) {
     // Logits from 16 x 16 blocks: lane l, slot r of block (i, j) holds the
     // logit of id mw + 16 i + 4 g + r (g = l / 16) and token nw + 16 j + c

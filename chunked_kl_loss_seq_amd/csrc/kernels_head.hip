@@ -16,7 +16,8 @@
 // Many rows are bound by the matrix cores, few by reading W.  Measured (MI355X):
 //  4,096 rows (3,686 count) x 201,088 x 2,880 bf16: forward 3.37 ms (1,267 TFLOP/s),
 //    gradient's logits 3.50, dH 3.75, dW 3.84 ms; both passes 14.5 ms.
-//  1 row of the same: 191 us for W's 1.16 GB (6.1 TB/s), 7 for the merge.
+//  256 rows of the same: forward 310 us, backward 1,245 (dW 616 of it, 1.16 GB written).
+//  1 row: 191 us for W's 1.16 GB (6.1 TB/s), 7 for the merge; backward 773 us.
 //  256 x 4,096 x 256 fp32, both passes: 46 us, seven launches of 3 to 13 us.
 #include <math.h>
 
@@ -195,26 +196,32 @@ int64_t tiles_of(int64_t m, int64_t n, HeadTile t) {
   const int e = tile_edge(t);
   return ((m + e - 1) / e) * ((n + e - 1) / e);
 }
-// The tile with the least time by this count: tiles a compute unit takes in turn x
-// a tile's work, over the rate that it reaches with all units busy (bf16: 1,305
-// TFLOP/s at 256 x 256, 1,021 at 128, 706 at 64; fp32: 126 at 128 and 121 at 64).
-// fp32 takes no 256 x 256 tile (130 TFLOP/s): its sums would not fit twice.
-HeadTile tile_for(Dtype dt, int64_t m, int64_t n, int64_t splits) {
-  static const double work[2][3] = {{1.0, 0.25 / 0.78, 0.0625 / 0.54}, {0.0, 0.25 / 0.97, 0.0625 / 0.93}};
-  const int first = dt == DT_BF16 ? TILE_256 : TILE_128;
-  int best = first;
-  double least = 0;
-  for (int t = first; t <= TILE_64; ++t) {
-    const int64_t turns = (tiles_of(m, n, (HeadTile)t) * splits + 255) / 256;
-    const double cost = (double)turns * work[dt == DT_BF16 ? 0 : 1][t];
-    if (t == first || cost < least) {
-      least = cost;
-      best = t;
-    }
-  }
-  return (HeadTile)best;
+// The time of n tiles on 256 compute units, in that of one turn of 256 x 256 tiles.  A
+// compute unit holds one such tile, two of 128 or three of 64; by the rates with all
+// of them busy (bf16: 1,305 TFLOP/s at 256 x 256, 1,021 at 128, 706 at 64; fp32: 126 at
+// 128 and 121 at 64) and, of a last turn, with fewer (one bf16 tile of 128 a unit takes 2,805 us
+// where one of 256 takes 6,195).  fp32 takes no 256 x 256 tile (130 TFLOP/s): its sums
+// would not fit twice.
+double tile_time(Dtype dt, HeadTile t, int64_t n) {
+  static const double busy[2][3][3] = {{{1.0}, {0.45, 0.64}, {0.20, 0.27, 0.347}}, {{}, {0.36, 0.516}, {0.11, 0.155, 0.202}}};
+  const auto& of = busy[dt == DT_BF16 ? 0 : 1][t];
+  const int held = t == TILE_256 ? 1 : t == TILE_128 ? 2 : 3;
+  const int64_t turns = n / (256 * held), rest = n - turns * 256 * held;
+  return (double)turns * of[held - 1] + (rest > 0 ? of[(rest - 1) / 256] : 0.0);
 }
-
+struct TileCost {
+  HeadTile tile;
+  double cost;
+};
+TileCost best_tile(Dtype dt, int64_t m, int64_t n) {
+  const int first = dt == DT_BF16 ? TILE_256 : TILE_128;
+  TileCost best{TILE_64, 0};
+  for (int t = first; t <= TILE_64; ++t) {
+    const double cost = tile_time(dt, (HeadTile)t, tiles_of(m, n, (HeadTile)t));
+    if (t == first || cost < best.cost) best = TileCost{(HeadTile)t, cost};
+  }
+  return best;
+}
 // WITH_256: whether a 256 x 256 tile may be asked for here.
 template <typename T, bool AK, bool BKM, int EPI, int MS, bool WITH_256 = sizeof(T) == 2>
 hipError_t launch_tile(HeadTile t, const GemmParams& p, hipStream_t s) {
@@ -230,38 +237,74 @@ hipError_t launch_tile(HeadTile t, const GemmParams& p, hipStream_t s) {
 // contractions of every chunk, did not pay here at any length (both passes of 201,088 x
 // 2,880: 4,096 rows 14.93 ms without it and 15.27 with, 8,192 31.25 and 31.61, 32,768
 // 128.1 and 133.0).
-GemmParams logits_product(Dtype dt, const void* W, const void* Hc, int64_t V, int64_t d, int64_t rows, HeadTile t,
-                          const int* live) {
+// Ids [lo, hi).
+GemmParams logits_product(Dtype dt, const void* W, const void* Hc, int64_t lo, int64_t hi, int64_t d, int64_t rows,
+                          HeadTile t, const int* live) {
   GemmParams p{};
   p.live = live;
-  p.a = Operand{W, d, V, d, 0};
+  p.a = Operand{(const char*)W + lo * d * (dt == DT_BF16 ? 2 : 4), d, hi - lo, d, 0};
   p.b = Operand{Hc, d, rows, d, 0};
-  p.tiles_m = cdiv64(V, tile_edge(t));
+  p.tiles_m = cdiv64(hi - lo, tile_edge(t));
   p.tiles_n = cdiv64(rows, tile_edge(t));
   p.k_tiles = cdiv64(d, dt == DT_BF16 ? 64 : 32);
   p.splits = 1;
   p.k_tiles_per_split = p.k_tiles;
   p.group_m = 4;
-  p.valid_m = V;
+  p.valid_m = hi - lo;
   p.valid_n = rows;
   return p;
 }
 
+// Ids of a slice of the statistics: what one wave of a tile covers.
+int slice_of(HeadTile t) { return tile_edge(t) / 2; }
+
 }  // namespace
 
-HeadTile head_logits_tile(Dtype dt, int64_t rows, int64_t V) { return tile_for(dt, V, rows, 1); }
+// Whole turns of large tiles, and the ids that would make a last turn of a few in
+// smaller ones, where that pays for the second launch, taken as 5 us, 195 / d turns
+// (256 rows of 201,088 x 2,880: 348 us forward in one launch, 310 in two; 1,000 of
+// 50,257 x 768 89 and 78).  fp32 tiles of 64 are as good as those of 128.
+HeadTiling head_logits_tiling(Dtype dt, int64_t rows, int64_t V, int64_t d) {
+  const TileCost plain = best_tile(dt, V, rows);
+  HeadTiling best{plain.tile, plain.tile, V};
+  if (dt != DT_BF16) return best;
+  double least = 0.96 * plain.cost;
+  for (int t = TILE_256; t < TILE_64; ++t) {
+    const int e = tile_edge((HeadTile)t);
+    const int64_t tn = (rows + e - 1) / e, main = tiles_of(V, rows, (HeadTile)t) / 256 * 256 / tn * e;
+    if (main == 0 || main >= V) continue;
+    const TileCost rest = best_tile(dt, V - main, rows);
+    const double cost = tile_time(dt, (HeadTile)t, main / e * tn) + rest.cost + 195.0 / (double)d;
+    if (cost < least) {
+      least = cost;
+      best = HeadTiling{(HeadTile)t, rest.tile, main};
+    }
+  }
+  return best;
+}
 
-// Ids of a slice of the statistics: what one wave of a tile covers.
-int head_slice(HeadTile t) { return tile_edge(t) / 2; }
+int head_slices(const HeadTiling& t, int64_t V) {
+  const int64_t a = (t.main + slice_of(t.tile) - 1) / slice_of(t.tile);
+  return (int)(a + (V - t.main + slice_of(t.rest) - 1) / slice_of(t.rest));
+}
 
-hipError_t launch_head_stats(Dtype dt, HeadTile t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
+hipError_t launch_head_stats(Dtype dt, const HeadTiling& t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
                              float* part_a, int n_slices, const int* live, hipStream_t s) {
-  GemmParams p = logits_product(dt, a.W, Hc, a.V, a.d, rows, t, live);
-  p.part = part;
-  p.part_a = part_a;
-  p.n_slices = n_slices;
-  if (dt == DT_BF16) return launch_tile<__bf16, true, true, EPI_STATS, 16>(t, p, s);
-  return launch_tile<float, true, true, EPI_STATS, 32>(t, p, s);
+  int at = 0;  // slices before this launch's
+  for (int64_t lo = 0; lo < a.V;) {
+    const HeadTile tile = lo == 0 ? t.tile : t.rest;
+    const int64_t hi = lo == 0 ? t.main : a.V;
+    GemmParams p = logits_product(dt, a.W, Hc, lo, hi, a.d, rows, tile, live);
+    p.part = part + at;
+    p.part_a = part_a + at;
+    p.n_slices = n_slices;
+    const hipError_t e = dt == DT_BF16 ? launch_tile<__bf16, true, true, EPI_STATS, 16>(tile, p, s)
+                                       : launch_tile<float, true, true, EPI_STATS, 32>(tile, p, s);
+    if (e != hipSuccess) return e;
+    at += (int)((hi - lo + slice_of(tile) - 1) / slice_of(tile));
+    lo = hi;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t rows, const float2* part,
@@ -283,30 +326,32 @@ hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t row
 hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, const void* Hc, int64_t r0, int64_t rows,
                             const int* vidx, const int* live, float4* coef, void* G, int64_t gblk, hipStream_t s) {
   const dim3 grid((unsigned)((rows + 3) / 4));
-  const HeadTile t = head_logits_tile(dt, rows, a.V);
-  GemmParams p = logits_product(dt, W, Hc, a.V, a.d, rows, t, live);
-  p.out = G;
-  p.ldo = gblk;
+  const HeadTiling t = head_logits_tiling(dt, rows, a.V, a.d);
   hipError_t e;
-  if (a.T == 1) {  // the epilogue reads the rows' arrays and adds the given token's share itself
-    p.one = GradRow{a.ids, a.dlogp, a.dentropy, a.entropy, a.stats, a.N};
-    p.g_rowmap = vidx;
-    p.one.ids += r0;
-    p.one.dlogp += r0;
-    if (a.dentropy != nullptr) {
-      p.one.dentropy += r0;
-      p.one.entropy += r0;
-    }
-    p.one.stats += r0;
-  } else {
+  if (a.T != 1) {
     hipLaunchKernelGGL(head_coef_kernel, grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    p.coef = coef;
   }
-  e = dt == DT_BF16 ? launch_tile<__bf16, true, true, EPI_GRAD, 16>(t, p, s)
-                    : launch_tile<float, true, true, EPI_GRAD, 32>(t, p, s);
-  if (e != hipSuccess || a.T <= 1) return e;
+  for (int64_t lo = 0; lo < a.V;) {
+    const HeadTile tile = lo == 0 ? t.tile : t.rest;
+    const int64_t hi = lo == 0 ? t.main : a.V;
+    GemmParams p = logits_product(dt, W, Hc, lo, hi, a.d, rows, tile, live);
+    p.out = (char*)G + (lo >> 6) * 4096 * (dt == DT_BF16 ? 2 : 4);
+    p.ldo = gblk;
+    if (a.T == 1) {  // the epilogue reads the rows' arrays and adds the given token's share itself
+      p.one = GradRow{a.ids + r0,  a.dlogp + r0, a.dentropy != nullptr ? a.dentropy + r0 : nullptr,
+                      a.entropy != nullptr ? a.entropy + r0 : nullptr, a.stats + r0, a.N, a.V, lo};
+      p.g_rowmap = vidx;
+    } else {
+      p.coef = coef;
+    }
+    e = dt == DT_BF16 ? launch_tile<__bf16, true, true, EPI_GRAD, 16>(tile, p, s)
+                      : launch_tile<float, true, true, EPI_GRAD, 32>(tile, p, s);
+    if (e != hipSuccess) return e;
+    lo = hi;
+  }
+  if (a.T <= 1) return hipSuccess;
   if (dt == DT_BF16)
     hipLaunchKernelGGL((head_given_kernel<__bf16>), grid, dim3(256), 0, s, a, r0, rows, vidx, live, coef, (__bf16*)G, gblk);
   else
@@ -314,20 +359,26 @@ hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, cons
   return hipGetLastError();
 }
 
-// The split of dH's reduction over V and its tile: with enough 256 x 256 tiles, the
-// loss's (dh_splits); else 64 x 64 tiles in as many splits as give every compute
-// unit two, of at least 8 k-steps each.
+// The split of dH's reduction over V and its tile: the least of the tiles' time and
+// that of the partial slabs, written and read again at 5 TB/s; runs of at least 8
+// k-steps.
 HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V) {
-  if (dt == DT_BF16) {
-    const int s256 = dh_splits(dt, rows, d, V);
-    if (tile_for(dt, rows, d, s256) == TILE_256) return HeadSplit{TILE_256, s256};
-  }
-  const int64_t tiles = tiles_of(rows, d, TILE_64), steps = (V + (dt == DT_BF16 ? 63 : 31)) / (dt == DT_BF16 ? 64 : 32);
-  int64_t n = (512 + tiles - 1) / tiles;
-  if (n > steps / 8) n = steps / 8;
-  if (n > 32) n = 32;
-  const int fit = n > 1 ? dh_fit_splits(dt, V, (int)n) : 1;
-  return HeadSplit{tile_for(dt, rows, d, fit), fit};
+  const int64_t steps = (V + (dt == DT_BF16 ? 63 : 31)) / (dt == DT_BF16 ? 64 : 32);
+  // one turn of 256 x 256 tiles over all of V at the rates above, in seconds
+  const double turn = 2.0 * 65536 * 256 * (double)V / (dt == DT_BF16 ? 1305e12 : 130e12);
+  HeadSplit best{TILE_64, 1};
+  double least = -1;
+  for (int t = dt == DT_BF16 ? TILE_256 : TILE_128; t <= TILE_64; ++t)
+    for (int n = 1; n <= 32 && (n == 1 || steps / n >= 8); ++n) {
+      if (dh_fit_splits(dt, V, n) != n) continue;
+      const double cost = tile_time(dt, (HeadTile)t, tiles_of(rows, d, (HeadTile)t) * n) / n +
+                          (double)n * (double)rows * (double)d * 8 / 5e12 / turn;
+      if (least < 0 || cost < least) {
+        least = cost;
+        best = HeadSplit{(HeadTile)t, n};
+      }
+    }
+  return best;
 }
 
 hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, int64_t V, int64_t d,
@@ -355,7 +406,7 @@ hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t g
 
 hipError_t launch_head_dw(Dtype dt, const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
                           const float* old, float* sums, int beta, void* rounded, const int* live, hipStream_t s) {
-  const HeadTile t = tile_for(dt, V, d, 1);
+  const HeadTile t = best_tile(dt, V, d).tile;
   if (rounded == nullptr && t == TILE_256) return launch_dw(dt, G, gblk, Hc, V, d, rows, sums, beta, live, s);
   GemmParams p{};
   p.live = live;

@@ -225,10 +225,15 @@ struct HeadArgs {
 };
 // Edge of the square tiles of a product (see kernels_head.hip).
 enum HeadTile : int { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
-HeadTile head_logits_tile(Dtype dt, int64_t rows, int64_t V);
-int head_slice(HeadTile t);  // ids of a slice of the statistics
+// The logits product's: ids [0, main) in `tile`, the others in `rest`, by a launch of their own.
+struct HeadTiling {
+  HeadTile tile, rest;
+  int64_t main;
+};
+HeadTiling head_logits_tiling(Dtype dt, int64_t rows, int64_t V, int64_t d);
+int head_slices(const HeadTiling& t, int64_t V);  // slices of a row's statistics
 // The slices' statistics of a chunk of rows Hc (all of them, or the *live compacted ones).
-hipError_t launch_head_stats(Dtype dt, HeadTile t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
+hipError_t launch_head_stats(Dtype dt, const HeadTiling& t, const HeadArgs& a, const void* Hc, int64_t rows, float2* part,
                              float* part_a, int n_slices, const int* live, hipStream_t s);
 // Entropy, stats and log-probabilities of rows [r0, r0 + rows); pos: of a compacted chunk, or null.
 hipError_t launch_head_rows(Dtype dt, const HeadArgs& p, int64_t r0, int64_t rows, const float2* part,

@@ -150,6 +150,21 @@ def test_tiles(ckl, dtype, N, V, d):
     check(ckl, N, V, d, dtype, 1)
 
 
+@pytest.mark.parametrize("T", [0, 1, 2])
+def test_a_last_turn_of_smaller_tiles(ckl, T):
+    # 256 tiles of 256 x 256 and 300 ids more, which go in tiles of 64 by a launch of their own
+    mask = np.ones(256, np.uint8)
+    mask[100:140] = 0
+    check(ckl, 256, 65836, 520, "bf16", T, mask=mask if T == 2 else None)
+
+
+def test_few_rows_past_a_tile(ckl):
+    # dH in tiles of 128 and many splits; dW rounded by all three tiles' epilogues, added over chunks
+    check(ckl, 300, 20000, 520, "bf16", 1)
+    check(ckl, 300, 700, 136, "bf16", 1, chunk=256)
+    check(ckl, 600, 9000, 2056, "bf16", 1, chunk=256)
+
+
 @pytest.mark.parametrize("T", [64, 2048])
 def test_given_tokens(ckl, T):
     check(ckl, 5, 300, 64, "bf16", T)
