@@ -15,10 +15,10 @@
 //
 // Many rows are bound by the matrix cores, few by reading W.  Measured (MI355X):
 //  4,096 rows (3,686 count) x 201,088 x 2,880 bf16: forward 3.37 ms (1,267 TFLOP/s),
-//    gradient's logits 3.50, dH 3.75, dW 3.84 ms; both passes 14.5 ms.
+//    gradient's logits 3.49, dH 3.75, dW 3.74 ms; both passes 14.6 ms.
 //  256 rows of the same: forward 310 us, backward 1,245 (dW 616 of it, 1.16 GB written).
 //  1 row: 191 us for W's 1.16 GB (6.1 TB/s), 7 for the merge; backward 773 us.
-//  256 x 4,096 x 256 fp32, both passes: 46 us, seven launches of 3 to 13 us.
+//  256 x 4,096 x 256 fp32, both passes: 46 us, six launches of 3 to 13 us.
 #include <math.h>
 
 #include "gemm_core.hpp"
