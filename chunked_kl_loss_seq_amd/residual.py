@@ -34,8 +34,8 @@ _WORD = (1 << 64) - 1
 
 
 def _drop(torch, p, seed, offset, device):
-    """ckl_drop of a probability, a seed in [0, 2^64) and an offset: an int in
-    [0, 2^64) or an int64 GPU tensor of one element, read when the kernels run."""
+    """The fields of ckl_drop for a probability, a seed in [0, 2^64) and an offset: an int
+    in [0, 2^64) or an int64 GPU tensor of one element, read when the kernels run."""
     if not 0.0 <= p <= 1.0:
         raise ValueError("p must be in [0, 1]")
     if not 0 <= seed <= _WORD:
@@ -43,10 +43,10 @@ def _drop(torch, p, seed, offset, device):
     if isinstance(offset, torch.Tensor):
         if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
             raise ValueError(f"offset must be an int or an int64 tensor of one element on {device}")
-        return Drop(p, seed, 0, offset.data_ptr())
+        return p, seed, 0, offset.data_ptr()
     if not 0 <= offset <= _WORD:
         raise ValueError("offset must be in [0, 2^64)")
-    return Drop(p, seed, offset, None)
+    return p, seed, offset, None
 
 
 def drop(x, p, seed, offset=0, out=None):
@@ -67,7 +67,7 @@ def drop(x, p, seed, offset=0, out=None):
     dt = _dtype(torch, x, "x")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    how = _drop(torch, p, seed, offset, dev)
+    how = Drop(*_drop(torch, p, seed, offset, dev))
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -149,7 +149,8 @@ def _norm_args(torch, y, r, w_pre, w_post, gate, scale, p, seed, offset, eps):
     if not eps >= 0.0:
         raise ValueError("eps must be at least 0")
     drops = _drop(torch, p, seed, offset, dev)
-    how = Norm(_at(w_post), _at(w_pre), _at(gate), 1 if rows else 0, scale, eps, ctypes.pointer(drops) if p else None)
+    how = Norm(_at(w_post), _at(w_pre), _at(gate), 1 if rows else 0, scale, eps,
+               ctypes.pointer(Drop(*drops)) if p else None)
     return dt, dev, y.numel() // d, d, how
 
 
