@@ -369,3 +369,30 @@ def test_refusals(ckl):
     with pytest.raises(RuntimeError, match="captured"):
         with torch.cuda.graph(g):
             ckl.token_logprobs(leaf, ids)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["rising", "falling", "one slice", "level", "few above -inf"])
+@pytest.mark.parametrize("top", [20, 128, 400])
+def test_alternatives_of_few_rows_in_few_slices(ckl, dtype, kind, top):
+    """Rows split over workgroups whose alternatives lie side by side, are all equal, or are too few."""
+    N, V = 3, 100003
+    say(f"[case] few rows {dtype} {kind} top={top}")
+    rng = np.random.default_rng(top)
+    z = {"rising": lambda: np.tile(np.linspace(-3, 8, V), (N, 1)), "falling": lambda: np.tile(np.linspace(8, -3, V), (N, 1)),
+         "one slice": lambda: rng.standard_normal((N, V)), "level": lambda: np.full((N, V), 1.5),
+         "few above -inf": lambda: np.full((N, V), -np.inf)}[kind]()
+    if kind == "one slice":
+        z[:, 50000:50600] += 20
+    if kind == "few above -inf":
+        z[:, rng.permutation(V)[:top - 1]] = rng.standard_normal(top - 1)
+    x = dev(z, dtype)
+    out = ckl.logprobs(x, None, top=top)
+    h = host(x)
+    b = Bounds(h)
+    for n in range(N):
+        order = np.lexsort((np.arange(V), -h[n]))[:top]
+        ids = np.where(np.isfinite(h[n][order]), order, -1)
+        np.testing.assert_array_equal(host(out.top_ids)[n], ids)
+        want = np.where(ids >= 0, b.logp[n][order], -np.inf)
+        same(host(out.top_logp)[n], want, b.of_logp(b.d[n][order], want)[n], "top_logp")
