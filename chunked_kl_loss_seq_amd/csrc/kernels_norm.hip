@@ -18,7 +18,7 @@
 // behind them.
 // Measured (MI355X, bf16): 32,768 x 2,880 with both weights, a gate [d] and p = 0.1:
 // forward 140 us (5.4 TB/s), backward 240 us (4.7 TB/s), of which the sums of columns
-// take 5.  8,192 x 8,192 backward 163 us (4.9 TB/s).  One row of 2,880: 4.0 us.
+// take 5.  8,192 x 8,192 backward 163 us (4.9 TB/s).  One row of 2,880: 3.7 us.
 // dropout of 94 M bf16 elements 67 us (5.6 TB/s).
 // Rows wider than 8,192 are far from that backward (4,096 x 12,288: 254 us, 117 at the
 // copy's rate): 1,024 threads hold two vectors each, which do not fit 128 registers.
