@@ -47,8 +47,27 @@ int dh_fit_splits(Dtype dt, int64_t V, int s) {
   return (int)((ksteps + per - 1) / per);  // at most s, and cuts the k-steps into exactly that many runs
 }
 
+// A tile's copies of G address it by 32-bit offsets from its first row within a
+// buffer of 2^31 - 16 bytes, and G's blocks of 64 rows lie tile_row_stride(V)
+// elements apart: 256 rows fit up to 5.59 M ids in bf16 and 2.79 M in fp32, 128 up to
+// 16.7 M and 8.3 M, the 64 of one block always.  Beyond, rows would read as zeros or
+// as other rows.
+int dh_tile_rows(Dtype dt, int64_t rows, int64_t V) {
+  const int64_t esz = dt == DT_BF16 ? 2 : 4;
+  int edge = 256;
+  for (; edge > 64; edge /= 2) {
+    const int64_t blocks = ((rows < edge ? rows : edge) + 63) / 64;
+    if (((blocks - 1) * tile_row_stride(V) + 4096) * esz <= 0x7FFFFFF0) break;
+  }
+  return edge;
+}
+
 hipError_t launch_dh(Dtype dt, const void* G, int64_t gblk, const void* Wt, int64_t V, int64_t d, int64_t rows,
                      float* slab, int splits, const int* live, hipStream_t s, bool tiled) {
+  const int edge = dh_tile_rows(dt, rows, V);
+  if (edge < 256)
+    return launch_head_dh(dt, HeadSplit{edge == 128 ? TILE_128 : TILE_64, splits}, G, gblk, Wt, V, d, rows, slab, live, s,
+                          tiled);
   const int bn = d_tile(dt, d);
   const int bk = dt == DT_BF16 ? 64 : 32;
   GemmParams p{};

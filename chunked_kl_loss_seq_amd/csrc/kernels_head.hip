@@ -361,15 +361,17 @@ hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, cons
 
 // The split of dH's reduction over V and its tile: the least of the tiles' time and
 // that of the partial slabs, written and read again at 5 TB/s; runs of at least 8
-// k-steps.
+// k-steps.  No tile of more rows than the copies of G reach.
 HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V) {
   const int64_t steps = (V + (dt == DT_BF16 ? 63 : 31)) / (dt == DT_BF16 ? 64 : 32);
   // one turn of 256 x 256 tiles over all of V at the rates above, in seconds
   const double turn = 2.0 * 65536 * 256 * (double)V / (dt == DT_BF16 ? 1305e12 : 130e12);
+  const int reach = dh_tile_rows(dt, rows, V);
   HeadSplit best{TILE_64, 1};
   double least = -1;
   for (int t = dt == DT_BF16 ? TILE_256 : TILE_128; t <= TILE_64; ++t)
     for (int n = 1; n <= 32 && (n == 1 || steps / n >= 8); ++n) {
+      if (tile_edge((HeadTile)t) > reach) break;
       if (dh_fit_splits(dt, V, n) != n) continue;
       const double cost = tile_time(dt, (HeadTile)t, tiles_of(rows, d, (HeadTile)t) * n) / n +
                           (double)n * (double)rows * (double)d * 8 / 5e12 / turn;
@@ -382,12 +384,13 @@ HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V) {
 }
 
 hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, int64_t V, int64_t d,
-                          int64_t rows, float* slab, const int* live, hipStream_t s) {
-  if (h.tile == TILE_256) return launch_dh(dt, G, gblk, W, V, d, rows, slab, h.splits, live, s, false);
+                          int64_t rows, float* slab, const int* live, hipStream_t s, bool tiled) {
+  if (h.tile == TILE_256) return launch_dh(dt, G, gblk, W, V, d, rows, slab, h.splits, live, s, tiled);
   GemmParams p{};
   p.live = live;
   p.a = Operand{G, 0, rows, V, gblk};  // tiled: storage row = token, column = vocabulary id
-  p.b = Operand{W, d, d, V, 0};        // storage row = vocabulary id (k), column = d (n)
+  // storage row = vocabulary id (k), column = d (n)
+  p.b = tiled ? Operand{W, 0, d, V, tile_row_stride(d)} : Operand{W, d, d, V, 0};
   p.tiles_m = cdiv64(rows, tile_edge(h.tile));
   p.tiles_n = cdiv64(d, tile_edge(h.tile));
   p.k_tiles = cdiv64(V, dt == DT_BF16 ? 64 : 32);

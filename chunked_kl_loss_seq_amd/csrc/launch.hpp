@@ -64,6 +64,9 @@ hipError_t launch_logits(Dtype dt, const void* Wt, const void* Hc, int64_t V, in
                          int64_t pblk, float2* part, int n_slices, const IdTables* tab, const GradTerms* grad,
                          const int* live, hipStream_t s);
 
+// Rows of a dH tile: the most of 256, 128 and 64 whose span in the tiled G fits the
+// copies' 2 GiB (see kernels_gemm.hip).
+int dh_tile_rows(Dtype dt, int64_t rows, int64_t V);
 // dH partial slabs of one chunk: slab[s][n][j] = sum over the s-th vocabulary
 // split of G[n][v] W[v][j].  G is tiled like P, tile rows gblk elements apart;
 // Wt is the tiled copy of the weight, or the row-major weight where `tiled` is false.
@@ -251,14 +254,15 @@ struct HeadGradArgs {
 // G of a chunk (tiled, tile rows gblk elements apart); coef: [rows].
 hipError_t launch_head_grad(Dtype dt, const HeadGradArgs& a, const void* W, const void* Hc, int64_t r0, int64_t rows,
                             const int* vidx, const int* live, float4* coef, void* G, int64_t gblk, hipStream_t s);
-// dH's partial slabs as launch_dh leaves them, in the given tile and splits.
+// dH's partial slabs as launch_dh leaves them, in the given tile (of at most
+// dh_tile_rows rows) and splits.
 struct HeadSplit {
   HeadTile tile;
   int splits;
 };
 HeadSplit head_dh_split(Dtype dt, int64_t rows, int64_t d, int64_t V);
 hipError_t launch_head_dh(Dtype dt, const HeadSplit& h, const void* G, int64_t gblk, const void* W, int64_t V, int64_t d,
-                          int64_t rows, float* slab, const int* live, hipStream_t s);
+                          int64_t rows, float* slab, const int* live, hipStream_t s, bool tiled = false);
 // dW: fp32 `sums` (+)= G^T H_c; or, where `rounded` is not null, that bf16 array = G^T
 // H_c, plus the fp32 `old` where given (bf16 operands).
 hipError_t launch_head_dw(Dtype dt, const void* G, int64_t gblk, const void* Hc, int64_t V, int64_t d, int64_t rows,
