@@ -241,10 +241,14 @@ add_norm_kernel(NormArgs p, Team team) {
     const uint64_t group0 = (uint64_t)row0 * (uint64_t)d8 + (uint64_t)(uint32_t)(at.sub * d8);
     float b[NV][8], o[NV][8];  // the branch before its norm, then r'
     float s[1] = {0.f};
+    uint32_t all = 0;  // the kept ones of all vectors, none past the row's end
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       uint32_t kept = 0xFFu;
-      if constexpr (DROP) kept = kept_bits(p.drop, offset, group0 + (uint32_t)(at.t + i * at.width));
+      if constexpr (DROP) {
+        kept = kept_bits(p.drop, offset, group0 + (uint32_t)(at.t + i * at.width));
+        all |= (at.t + i * at.width < d8 ? kept : 0u) << (8 * i);
+      }
       const int c = at.t + i * at.width;
       if (c >= d8) {
         y[i].clear();
@@ -267,13 +271,22 @@ add_norm_kernel(NormArgs p, Team team) {
       team_sums(s, team, red, half);
       inv1 = 1.f / sqrtf(s[0] * inv_d + p.eps);
     }
+    float by = inv1;
+    if (DROP && __builtin_expect(!(inv1 < INFINITY), 0)) {  // 0 x NaN: what goes adds nothing to r, whatever y holds
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[i][e] = (all >> (8 * i + e)) & 1u ? b[i][e] * inv1 : 0.f;
+      }
+      by = 1.f;
+    }
     s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = at.t + i * at.width;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[i][e] = __builtin_fmaf(b[i][e], inv1, o[i][e]);
+        o[i][e] = __builtin_fmaf(b[i][e], by, o[i][e]);
         s[0] = __builtin_fmaf(o[i][e], o[i][e], s[0]);
       }
       Eight<T> v;
@@ -386,12 +399,13 @@ add_norm_bwd_kernel(NormArgs p, NormGrads q, Team team) {
         co[i].clear();
         if constexpr (ROWS) cg[i].clear();
       }
+      const float j1 = !DROP || (live && c < d8) ? i1 : 0.f;  // nor 0 x NaN
       float k[8], k2[8], b[8];
       read8(f, (int)p.d, c < d8 ? c : 0, k);
       read8(w2, (int)p.d, c < d8 ? c : 0, k2);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n1[i][e] = cy[i].get(e) * i1;
+        n1[i][e] = cy[i].get(e) * j1;
         b[e] = k[e] * n1[i][e];
         if constexpr (ROWS) b[e] *= gr[i][e] = cg[i].get(e);
         if (DROP && !((kept[i] >> e) & 1u)) b[e] = 0.f;
