@@ -39,8 +39,7 @@ constexpr int kDropThreads = 256;
 constexpr int kDropGroups = 4;  // groups of eight elements per thread
 
 template <typename T>
-__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* __restrict__ x, int64_t n, Drop r,
-                                                              T* __restrict__ out) {
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* x, int64_t n, Drop r, T* out) {  // out may be x
   const uint64_t offset = drop_offset(r);
   const int64_t g0 = (int64_t)blockIdx.x * (kDropThreads * kDropGroups) + threadIdx.x;
   Eight<T> v[kDropGroups];
