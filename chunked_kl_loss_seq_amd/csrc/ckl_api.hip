@@ -536,8 +536,8 @@ int logprob_shape(int dtype, const void* logits, int64_t N, int64_t V, int64_t l
 struct HeadLayout {
   int64_t C = 0, pblk = 0;
   int n_slices = 0;
-  HeadTiling tiling{TILE_256, TILE_256, 0};  // forward: the contraction's
-  HeadSplit split{TILE_256, 0};
+  HeadTiling tiling{TILE_256, TILE_256, 0};  // forward: the contraction's, and its slices of a row
+  HeadSplit split{TILE_256, 0};              // backward: dH's
   uint64_t live_off = 0, hc_off = 0, vidx_off = 0, pos_off = 0, part_off = 0, parta_off = 0, g_off = 0, coef_off = 0, slab_off = 0, dw_off = 0, total = 0;
 };
 
@@ -545,8 +545,6 @@ HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C
   HeadLayout L;
   L.C = C;
   L.pblk = tile_row_stride(V);
-  L.tiling = head_logits_tiling(esz == 2 ? DT_BF16 : DT_F32, C, V, d);
-  L.n_slices = head_slices(L.tiling, V);
   uint64_t off = 0;
   const auto take = [&off](uint64_t bytes) {
     const uint64_t at = off;
@@ -558,6 +556,8 @@ HeadLayout head_layout(bool backward, int64_t N, int64_t d, int64_t V, int64_t C
   L.vidx_off = take((uint64_t)C * 4);
   L.pos_off = take((uint64_t)C * 4);
   if (!backward) {
+    L.tiling = head_logits_tiling(esz == 2 ? DT_BF16 : DT_F32, C, V, d);
+    L.n_slices = head_slices(L.tiling, V);
     L.part_off = take((uint64_t)C * L.n_slices * 8);
     L.parta_off = take((uint64_t)C * L.n_slices * 4);
   } else {

@@ -685,12 +685,9 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(LogprobGradA
   for (int q = 0; q < nm; ++q) out[mine[q]] = (T)(add[q] + grad_of(zt[q], m, logs, c, u));
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool TOP>
 void logprob_rows(const LogprobArgs& p, hipStream_t s) {
-  if (p.top)
-    hipLaunchKernelGGL((logprob_kernel<T, NT, true>), dim3((unsigned)p.N), dim3(NT), 0, s, p);
-  else
-    hipLaunchKernelGGL((logprob_kernel<T, NT, false>), dim3((unsigned)p.N), dim3(NT), 0, s, p);
+  hipLaunchKernelGGL((logprob_kernel<T, NT, TOP>), dim3((unsigned)p.N), dim3(NT), 0, s, p);
 }
 
 template <typename T>
@@ -708,14 +705,20 @@ hipError_t logprob_of(const LogprobArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((logprob_join_kernel<T, 256>), dim3((unsigned)p.N), dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  if (p.V <= 1024)
-    logprob_rows<T, 64>(p, s);
-  else if (p.V <= 8192 && p.top <= kWideTop)
-    logprob_rows<T, 256>(p, s);
-  else if (p.top)
-    logprob_rows<T, 512>(p, s);
-  else
-    logprob_rows<T, 1024>(p, s);
+  if (p.top == 0) {
+    if (p.V <= 1024)
+      logprob_rows<T, 64, false>(p, s);
+    else if (p.V <= 8192)
+      logprob_rows<T, 256, false>(p, s);
+    else
+      logprob_rows<T, 1024, false>(p, s);
+  } else if (p.V <= 1024) {
+    logprob_rows<T, 64, true>(p, s);
+  } else if (p.V <= 8192 && p.top <= kWideTop) {
+    logprob_rows<T, 256, true>(p, s);
+  } else {
+    logprob_rows<T, 512, true>(p, s);
+  }
   return hipGetLastError();
 }
 
