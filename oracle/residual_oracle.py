@@ -12,16 +12,16 @@ import numpy as np
 
 def philox(counters, offset, seed):
     """Philox4x32-10 under the key `seed`, counter words (low, high) of `counters` and of `offset`: uint32 [n, 4]."""
-    out = np.empty((len(counters), 4), np.uint32)
-    for i, g in enumerate(counters):
-        c = [int(g) & 0xFFFFFFFF, int(g) >> 32, offset & 0xFFFFFFFF, offset >> 32]
-        k = [seed & 0xFFFFFFFF, seed >> 32]
-        for _ in range(10):
-            a, b = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
-            c = [(b >> 32) ^ c[1] ^ k[0], b & 0xFFFFFFFF, (a >> 32) ^ c[3] ^ k[1], a & 0xFFFFFFFF]
-            k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
-        out[i] = c
-    return out
+    low = np.uint64(0xFFFFFFFF)
+    g = np.array(counters, np.uint64)
+    half = np.uint64(32)
+    c = [g & low, g >> half, np.full_like(g, offset & 0xFFFFFFFF), np.full_like(g, offset >> 32)]
+    k = [seed & 0xFFFFFFFF, seed >> 32]
+    for _ in range(10):
+        a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(b >> half) ^ c[1] ^ np.uint64(k[0]), b & low, (a >> half) ^ c[3] ^ np.uint64(k[1]), a & low]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return np.stack(c, 1).astype(np.uint32)
 
 
 def factors(n, p, seed, offset=0):
