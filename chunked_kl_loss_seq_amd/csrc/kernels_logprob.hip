@@ -19,15 +19,19 @@
 // is a bound that at least K logits reach.  The halves whose maximum reaches it are
 // read again, each by several lanes at once, and what reaches it is collected; up
 // to 128 are placed by the number of larger (logit, lower id) pairs, more are
-// sorted.  Where more than 1,024 reach the bound (equal logits), a binary search over
-// the pairs narrows it first.  All of it is inlined: as calls, which the compiler
-// made of what two kernels share, the registers saved around them cost 20 to 50 us
-// of every case with alternatives below.
+// sorted.  Where more than 1,024 reach the bound (equal logits, or fp32 ones under a
+// common offset, whose keys differ in their lower 16 bits alone), a binary search over
+// the pairs narrows it first, a pass over the row a step.  All of it is inlined: as
+// calls, which the compiler made of what two kernels share, the registers saved around
+// them cost 20 to 50 us of every case with alternatives below.
 //
 // Bound by reading the logits.  Measured (MI355X):
 //  1,024 x 201,088 bf16: 72 us, 5.7 TB/s (with 100 given tokens a row 74); 20
 //    alternatives 75 us, 128 110 us, 400 154 us.  fp32 140 us, with 20 148 us.
 //  3,000 x 40,001 bf16, 20 alternatives: 51 us for 46 without.
+//  The search: 1,024 x 201,088 fp32 normal logits about 300, top 1 / 20 / 128 / 400, 381 /
+//    937 / 1,046 / 1,283 us (about 0: 144 / 148 / 193 / 266); about 5,000, 1,400 to 1,900;
+//    bf16 about 300, where they take a dozen values, 130 / 132 / 137 / 7,800 us.
 //  2,048 x 128,256 bf16 forward and gradient, a tenth of the rows masked: 284 us,
 //    5.2 TB/s of 1.47 GB.
 //  1 x 201,088 bf16, 20 alternatives: 7.7 us for the slices and 4.6 for joining them.

@@ -17,11 +17,14 @@
 // numbers' generator (about 30 us of vector instructions for 94 M elements) hides
 // behind them.
 // Measured (MI355X, bf16): 32,768 x 2,880 with both weights, a gate [d] and p = 0.1:
-// forward 140 us (5.4 TB/s), backward 240 us (4.7 TB/s), of which the sums of columns
-// take 5.  8,192 x 8,192 backward 163 us (4.9 TB/s).  One row of 2,880: 3.7 us.
+// forward 141 us (5.3 TB/s), backward 237 us (4.8 TB/s), of which the sums of columns
+// take 5.  8,192 x 8,192 backward 162 us (5.0 TB/s).  One row of 2,880: 3.7 us.
 // dropout of 94 M bf16 elements 67 us (5.6 TB/s).
-// Rows wider than 8,192 are far from that backward (4,096 x 12,288: 254 us, 117 at the
-// copy's rate): 1,024 threads hold two vectors each, which do not fit 128 registers.
+// Rows wider than 8,192 are far from that backward (4,096 x 12,288: 260 us, 117 at the
+// copy's rate): 1,024 threads hold two vectors each, which do not fit 128 registers, and
+// 144 to 208 bytes a lane go to scratch (fp32 170 to 300).  Besides those only fp32 with a
+// gate of [N, d] spills: backward from 4,104 columns 20 to 36 bytes, forward above 8,192
+// 68 to 96 (4,096 x 12,288 with dropout 244 us).
 // What carried it: loads of the next row under way for a whole turn (a select right
 // after each load had made every load wait for the one before), a barrier for LDS
 // alone (the ordinary one waits for all loads), the columns' weights in LDS instead
@@ -71,9 +74,10 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* x, int64
 // A row goes to a team: `lanes` lanes of one wave (a power of two that covers
 // d / 8; several rows a wave for short rows), or all waves of a workgroup.  Lane
 // t of it holds elements 8 (t + i width) .. + 7, i < NV, in registers, so a row is
-// read once; the weights of its columns stay there too.  Workgroups walk over
-// rows, and the next row's loads are issued before the current row's sums are
-// joined.
+// read once; the weights of its columns are in LDS, for all rows of a workgroup.
+// Workgroups walk over rows, and the next row's loads are issued before the current
+// row's sums are joined (not in the backward pass of rows above 8,192, which has no
+// registers for them).
 struct Team {
   int lanes;   // lanes of one row within a wave
   int rows;    // rows side by side in a workgroup
